@@ -454,6 +454,149 @@ int ssm_causal_conv1d_silu(const void* x, const float* weight, const float* bias
                            const float* state_in, int silu, void* u, float* state_out,
                            int64_t B, int64_t L, int64_t D, int64_t K, int dtype, void* stream);
 
+/*
+ * -------------------------------------------- conv1d + SiLU, backward
+ * Gradients of ssm_causal_conv1d_silu for L = sum(du * u) +
+ * sum(dstate_out * state_out): what takes the scan's du to the block's input.
+ * Nothing of the forward is stored; s is formed again.
+ *   g_t         = du_t * sigma(s_t) * (1 + s_t * (1 - sigma(s_t)))  (silu != 0; else du_t)
+ *   dx[t]       = sum_k weight[k] * g[t+(K-1)-k]       (g = 0 from t = L on)
+ *   dweight[k]  = sum_{b,t} g[t] * x[t-(K-1)+k];  dbias = sum_{b,t} g[t]
+ *   dstate_in   : the same sum for the K-1 inputs before t = 0
+ * (plus dstate_out, the gradient of state_out, where the inputs it copies are).
+ *   x, du, dx : [B, L, D] dtype;  weight, dweight : [D, K] fp32
+ *   bias, dbias : [D] fp32 or NULL (dbias NULL: not computed)
+ *   state_in, dstate_out, dstate_in : [B, D, K-1] fp32 or NULL
+ *   1 <= K <= 4; L >= 0 (L = 0: dweight, dbias zero, dstate_in = dstate_out).
+ * Outputs are written, never accumulated into, and must not overlap inputs.
+ * The workspace (256-byte aligned) holds partial sums, added in a fixed
+ * order: results are deterministic.
+ */
+size_t ssm_causal_conv1d_silu_bwd_workspace_bytes(int64_t B, int64_t L, int64_t D, int64_t K);
+
+int ssm_causal_conv1d_silu_bwd(const void* x, const float* weight, const float* bias,
+                               const float* state_in, int silu, const void* du,
+                               const float* dstate_out, void* dx, float* dweight, float* dbias,
+                               float* dstate_in, int64_t B, int64_t L, int64_t D, int64_t K,
+                               int dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * -------------------------------------------- gated linear recurrence
+ * A diagonal recurrence with one fp32 state per channel whose decay and input
+ * are gated by the token; per batch row b and channel d, over tokens t:
+ *
+ *   r = sigma(gate_a[b,t,d] + bias_a[d]),  i = sigma(gate_x[b,t,d] + bias_x[d])
+ *   a = exp(A[d] * r)                                            (A <= 0)
+ *   h = a * h + sqrt(1 - a^2) * i * x[b,t,d],   y[b,t,d] = h
+ *
+ * (the square root keeps the state's variance at the input's; 1 - a^2 is
+ * formed without cancellation for slow channels).
+ *
+ *   x, gate_a, gate_x, y : [B, L, D] dtype
+ *   A              : [D] fp32, not positive (a positive A makes NaN)
+ *   bias_a, bias_x : [D] fp32 or NULL (zeros)
+ *   h0, h_last     : [B, D] fp32 or NULL (zeros; not wanted)
+ *   ckpt           : [B, ceil(L / SSM_GATED_TILE), D] fp32 or NULL: for the
+ *                    backward, ckpt[b,k,d] = the state before token
+ *                    SSM_GATED_TILE * k (not written where that token is
+ *                    behind the row's end; the first always is)
+ *   seq_lens       : device int32 [B] or NULL: row b has its first
+ *                    seq_lens[b] tokens (clamped to [0, L]); the padding is
+ *                    not read, y there is left untouched, and h_last is the
+ *                    state after the row's last token
+ *   B, D >= 1; L >= 0; B * ceil(D / 64) below 2^25.
+ * The sequence is walked in tiles of SSM_GATED_TILE tokens by 64 channels.
+ * With enough of those strips of 64 channels to fill the GPU (or few tiles) a
+ * workgroup walks a strip alone; else several walk it together, each taking
+ * the next tile, and hand the state on through the workspace (256-byte
+ * aligned, 0 bytes for one walker; the call clears what it needs of it).
+ * ssm_gated_scan_walkers returns their number (0 for invalid sizes), a pure
+ * function of the sizes; the environment variable SSM_GATED_WALKERS (1..64)
+ * overrides it, for the queries and the calls.  Results do not depend on the
+ * number of walkers, bit for bit.
+ */
+#define SSM_GATED_TILE 128
+
+int ssm_gated_scan_walkers(int64_t B, int64_t L, int64_t D);
+size_t ssm_gated_scan_workspace_bytes(int64_t B, int64_t L, int64_t D, int dtype);
+size_t ssm_gated_scan_ckpt_bytes(int64_t B, int64_t L, int64_t D, int dtype);
+
+int ssm_gated_scan_fwd(const void* x, const void* gate_a, const void* gate_x, const float* A,
+                       const float* bias_a, const float* bias_x, const float* h0, void* y,
+                       float* h_last, float* ckpt, const int32_t* seq_lens, int64_t B, int64_t L,
+                       int64_t D, int dtype, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
+/*
+ * Gradients of ssm_gated_scan_fwd for L = sum(dy * y) + sum(dh_last * h_last).
+ * Inputs as the forward's, plus dy [B, L, D] dtype and dh_last [B, D] fp32 or
+ * NULL.  ckpt: what the forward saved over the same inputs, or NULL: the call
+ * first runs the forward's states itself (h0 is read only then).  Outputs,
+ * all written, never accumulated into:
+ *   dx, dgate_a, dgate_x : [B, L, D] dtype, zeros behind a row's end
+ *   dA                   : [D] fp32 (zero where A is zero: the square root has
+ *                          no finite derivative there)
+ *   dbias_a, dbias_x     : [D] fp32 or NULL (not computed)
+ *   dh0                  : [B, D] fp32 or NULL
+ * L = 0: dh0 = dh_last, the sums zero.  The workspace (256-byte aligned) holds
+ * partial sums added in a fixed order, what the walkers share, and without
+ * ckpt the saved states; results are deterministic (no atomics on results).
+ */
+size_t ssm_gated_scan_bwd_workspace_bytes(int64_t B, int64_t L, int64_t D, int dtype,
+                                          int with_ckpt);
+
+int ssm_gated_scan_bwd(const void* x, const void* gate_a, const void* gate_x, const float* A,
+                       const float* bias_a, const float* bias_x, const float* h0,
+                       const float* ckpt, const void* dy, const float* dh_last, void* dx,
+                       void* dgate_a, void* dgate_x, float* dA, float* dbias_a, float* dbias_x,
+                       float* dh0, const int32_t* seq_lens, int64_t B, int64_t L, int64_t D,
+                       int dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One token of the gated recurrence per sequence against a resident state
+ * (decode): state [B, D] fp32 is read and overwritten in place; x, gate_a,
+ * gate_x, y [B, D] dtype; the rest as ssm_gated_scan_fwd.  Equals the scan
+ * over one token bit for bit.
+ */
+int ssm_gated_state_update(float* state, const void* x, const void* gate_a, const void* gate_x,
+                           const float* A, const float* bias_a, const float* bias_x, void* y,
+                           int64_t B, int64_t D, int dtype, void* stream);
+
+/*
+ * -------------------------------------------- layer norm
+ * The norm in front of a block, over the last axis of [rows, D], with the
+ * residual stream's addition (kept in fp32) fused in front of it:
+ *   s = x (+ residual);  mean = sum(s) / D;  rstd = 1 / sqrt(var(s) + eps)
+ *   y = (s - mean) * rstd * weight + bias;   residual_out = s
+ *   x, y                   : [rows, D] dtype
+ *   residual, residual_out : [rows, D] fp32 or NULL (residual_out only with residual)
+ *   weight, bias           : [D] fp32 or NULL (ones; zeros)
+ *   mean, rstd             : [rows] fp32 or NULL, for the backward
+ *   D >= 1; 0 <= rows < 2^31; eps >= 0 and finite.
+ * var is the mean square of s - mean; sums are fp32 in a fixed order.
+ */
+int ssm_layer_norm_fwd(const void* x, const float* residual, const float* weight,
+                       const float* bias, float eps, void* y, float* residual_out, float* mean,
+                       float* rstd, int64_t rows, int64_t D, int dtype, void* stream);
+
+/*
+ * Its gradients for L = sum(dy * y) + sum(dresidual_out * residual_out).  x is
+ * the tensor that was normalised: the forward's x (x_dtype = dtype), or its
+ * residual_out (x_dtype = SSM_F32).  With n = (x - mean) * rstd, v = dy * weight:
+ *   ds = rstd * (v - mean_D(v) - n * mean_D(v * n)) (+ dresidual_out)
+ *   dx = ds [rows, D] dtype;  dresidual = ds [rows, D] fp32 or NULL
+ *   dweight = sum over rows of dy * n, dbias = sum over rows of dy : [D] fp32 or NULL
+ * Outputs are written, never accumulated into; rows = 0 gives zero sums.  The
+ * workspace (256-byte aligned) holds partial sums, added in a fixed order.
+ */
+size_t ssm_layer_norm_bwd_workspace_bytes(int64_t rows, int64_t D);
+
+int ssm_layer_norm_bwd(const void* x, int x_dtype, const void* dy, const float* mean,
+                       const float* rstd, const float* weight, const float* dresidual_out,
+                       void* dx, float* dresidual, float* dweight, float* dbias, int64_t rows,
+                       int64_t D, int dtype, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -15,8 +15,9 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import _native
+from . import _args, _native, recurrent_block
 from ._native import SSMError
+from .recurrent_block import *  # noqa: F401,F403
 
 __all__ = ["selective_scan_fwd", "selective_scan_fwd_noalloc", "selective_scan_conv_fwd",
            "selective_scan_bwd", "selective_scan_fwd_ckpt", "selective_scan_ckpt_bytes",
@@ -24,83 +25,16 @@ __all__ = ["selective_scan_fwd", "selective_scan_fwd_noalloc", "selective_scan_c
            "causal_conv1d_silu", "selective_scan_workspace_bytes",
            "selective_scan_segments", "selective_scan_lanes", "selective_scan_bwd_segments",
            "ssd_chunk_workspace_bytes",
-           "SSMError"]
+           "SSMError", *recurrent_block.__all__]
 
-_DT = {torch.float32: _native.SSM_F32, torch.bfloat16: _native.SSM_BF16}
+_DT = _args.DTYPES
 _F32 = torch.float32
-
-
-def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
-    return None if t is None else t.data_ptr()
-
-
-def _dev_tensor(name, t, dtype=None, device=None):
-    if t is None:
-        return None
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
-        raise ValueError(f"{name} must be a device tensor (got {t.device})")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t
-
-
-def _check_args(device, *specs) -> None:
-    """specs: (name, tensor or None, expected shape, dtype).  Types, shapes and
-    dtypes of every argument are checked first, then device and contiguity."""
-    for name, t, shape, dtype in specs:
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-        if dtype is not None and t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
-    for name, t, _shape, dtype in specs:
-        _dev_tensor(name, t, dtype, device)
-
-
-def _check_workspace(ws, need: int, device):
-    """A caller-supplied workspace: a contiguous uint8 tensor on the call's
-    device holding at least `need` bytes, or None."""
-    if ws is None:
-        return None
-    if not isinstance(ws, torch.Tensor):
-        raise TypeError("workspace must be a torch.Tensor")
-    if ws.dtype != torch.uint8:
-        raise TypeError(f"workspace must be uint8 (got {ws.dtype})")
-    if ws.numel() < need:
-        raise ValueError(f"workspace holds {ws.numel()} bytes, the call needs {need}")
-    if ws.device.type != "cuda" or ws.device != device:
-        raise ValueError(f"workspace is on {ws.device}, expected {device}")
-    if not ws.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    return ws
-
-
-def _workspace(ws, need: int, device):
-    ws = _check_workspace(ws, need, device)
-    if need and ws is None:
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
-    return ws, (0 if ws is None else ws.numel())
-
-
-def _act_dtype(name, t):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in _DT:
-        raise TypeError(f"{name} must be float32 or bfloat16 (got {t.dtype})")
-    return t.dtype
-
-
-def _stream_handle(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+_ptr = _args.ptr
+_check_args = _args.check_args
+_check_workspace = _args.check_workspace
+_workspace = _args.workspace
+_act_dtype = _args.act_dtype
+_stream_handle = _args.stream_handle
 
 
 def selective_scan_workspace_bytes(B: int, L: int, D: int, N: int, dtype=torch.bfloat16) -> int:

@@ -16,6 +16,7 @@ SSM_F32 = 0
 SSM_BF16 = 1
 FLAG_DELTA_SOFTPLUS = 1
 FLAG_ZOH = 2
+GATED_TILE = 128
 
 STATUS = {
     0: "SSM_OK", 1: "SSM_ERR_NULL_ARG", 2: "SSM_ERR_BAD_SHAPE", 3: "SSM_ERR_BAD_DTYPE",
@@ -29,6 +30,7 @@ _i64 = ctypes.c_int64
 _sz = ctypes.c_size_t
 _u = ctypes.c_uint
 _i = ctypes.c_int
+_f = ctypes.c_float
 SIGNATURES = {
     "ssm_abi_version": (_i, []),
     "ssm_status_string": (ctypes.c_char_p, [_i]),
@@ -67,6 +69,19 @@ SIGNATURES = {
                                     _i, _vp]),
     "ssm_selective_state_update": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _u, _vp,
                                         _i64, _i64, _i64, _i, _vp]),
+    "ssm_causal_conv1d_silu_bwd_workspace_bytes": (_sz, [_i64] * 4),
+    "ssm_causal_conv1d_silu_bwd": (_i, [_vp] * 4 + [_i] + [_vp] * 6 + [_i64] * 4 +
+                                   [_i, _vp, _sz, _vp]),
+    "ssm_gated_scan_walkers": (_i, [_i64] * 3),
+    "ssm_gated_scan_workspace_bytes": (_sz, [_i64] * 3 + [_i]),
+    "ssm_gated_scan_ckpt_bytes": (_sz, [_i64] * 3 + [_i]),
+    "ssm_gated_scan_fwd": (_i, [_vp] * 11 + [_i64] * 3 + [_i, _vp, _sz, _vp]),
+    "ssm_gated_scan_bwd_workspace_bytes": (_sz, [_i64] * 3 + [_i, _i]),
+    "ssm_gated_scan_bwd": (_i, [_vp] * 18 + [_i64] * 3 + [_i, _vp, _sz, _vp]),
+    "ssm_gated_state_update": (_i, [_vp] * 8 + [_i64] * 2 + [_i, _vp]),
+    "ssm_layer_norm_fwd": (_i, [_vp] * 4 + [_f] + [_vp] * 4 + [_i64] * 2 + [_i, _vp]),
+    "ssm_layer_norm_bwd_workspace_bytes": (_sz, [_i64] * 2),
+    "ssm_layer_norm_bwd": (_i, [_vp, _i] + [_vp] * 9 + [_i64] * 2 + [_i, _vp, _sz, _vp]),
 }
 
 _lock = threading.Lock()

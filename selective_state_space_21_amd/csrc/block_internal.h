@@ -1,0 +1,173 @@
+// Internal declarations of the calls around the scan in a recurrent block
+// (gated linear recurrence, layer norm, the causal conv's backward), shared
+// by their C-ABI layer, planners and kernel launchers.  Not part of the
+// public interface (include/ssm.h is).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "ssm.h"
+
+namespace ssm {
+
+// ---------------------------------------------------------------- gated scan
+
+// Tiling the planner shares with the kernels.
+namespace gated {
+constexpr int kTile = SSM_GATED_TILE;   // tokens per tile (and per saved state)
+constexpr int kStrip = 64;              // channels per strip: one workgroup's width
+constexpr int kThreads = 512;
+constexpr int kMaxWalkers = 64;         // workgroups per strip at most
+}  // namespace gated
+
+// How a call walks the sequence: every strip (64 channels of one batch row)
+// is a chain of 128-token tiles, walked by `walkers` workgroups.
+struct GatedPlan {
+    int64_t strips;        // B * ceil(D / 64)
+    int64_t dblocks;       // ceil(D / 64)
+    int64_t tiles;         // ceil(L / 128)
+    int walkers;           // 1: a workgroup walks its strip alone, nothing is shared
+    size_t chain_bytes;    // what the walkers of a strip share (0 for one)
+};
+
+// A pure function of the sizes (and the SSM_GATED_WALKERS override).
+GatedPlan plan_gated(int64_t B, int64_t L, int64_t D);
+
+struct GatedArgs {
+    const void* x;
+    const void* gate_a;
+    const void* gate_x;
+    const float* A;
+    const float* bias_a;
+    const float* bias_x;
+    const float* h0;
+    void* y;               // NULL: states only
+    float* h_last;
+    float* ckpt;           // [B, tiles, D] or NULL
+    const int32_t* seq_lens;
+    int64_t B, L, D;
+    int bf16;
+    GatedPlan plan;
+    void* chain;           // plan.chain_bytes, or NULL
+};
+
+struct GatedBwdArgs {
+    GatedArgs f;           // the forward call's inputs; f.ckpt holds the saved states
+    const void* dy;
+    const float* dh_last;
+    void* dx;
+    void* dgate_a;
+    void* dgate_x;
+    float* dA;
+    float* dbias_a;
+    float* dbias_x;
+    float* dh0;
+    bool own_ckpt;         // f.ckpt lies in the workspace and the call fills it first
+    void* chain;           // the adjoint's, apart from the forward sweep's f.chain
+    float* part;           // [B * tiles][3][D]: a tile's sums for dA, dbias_a, dbias_x
+};
+
+size_t gated_bwd_workspace_bytes(int64_t B, int64_t L, int64_t D, bool own_ckpt);
+void gated_bwd_carve(GatedBwdArgs& a, void* workspace);
+
+hipError_t launch_gated_fwd(const GatedArgs& a, hipStream_t stream);
+hipError_t launch_gated_bwd(const GatedBwdArgs& a, hipStream_t stream);
+
+struct GatedStepArgs {
+    float* state;
+    const void* x;
+    const void* gate_a;
+    const void* gate_x;
+    const float* A;
+    const float* bias_a;
+    const float* bias_x;
+    void* y;
+    int64_t B, D;
+    int bf16;
+};
+
+hipError_t launch_gated_step(const GatedStepArgs& a, hipStream_t stream);
+
+// ---------------------------------------------------------------- layer norm
+
+struct NormArgs {
+    const void* x;             // [rows, D] dtype
+    const float* residual;     // [rows, D] or NULL
+    const float* weight;       // [D] or NULL (ones)
+    const float* bias;         // [D] or NULL (zeros)
+    float eps;
+    void* y;
+    float* residual_out;       // [rows, D] or NULL
+    float* mean;               // [rows] or NULL
+    float* rstd;               // [rows] or NULL
+    int64_t rows, D;
+    int bf16;
+};
+
+hipError_t launch_layer_norm(const NormArgs& a, hipStream_t stream);
+
+struct NormBwdArgs {
+    const void* x;             // [rows, D] x_bf16 ? bf16 : fp32
+    const void* dy;            // [rows, D] dtype
+    const float* mean;
+    const float* rstd;
+    const float* weight;       // or NULL
+    const float* dresidual_out;   // [rows, D] or NULL
+    void* dx;                  // [rows, D] dtype
+    float* dresidual;          // [rows, D] or NULL
+    float* dweight;            // [D] or NULL
+    float* dbias;              // [D] or NULL
+    int64_t rows, D;
+    int x_bf16, bf16;
+    int64_t groups;            // workgroups that each sum a share of the rows
+    float* part;               // [2][groups][D]
+};
+
+// Workgroups of a backward call, each with a share of the rows and a row of
+// partial sums: a pure function of the sizes.
+int64_t norm_bwd_groups(int64_t rows, int64_t D);
+size_t norm_bwd_workspace_bytes(int64_t rows, int64_t D);
+hipError_t launch_layer_norm_bwd(const NormBwdArgs& a, hipStream_t stream);
+
+// ---------------------------------------------------------------- conv1d backward
+
+struct ConvBwdArgs {
+    const void* x;             // [B, L, D]
+    const float* weight;       // [D, K]
+    const float* bias;         // [D] or NULL
+    const float* state_in;     // [B, D, K-1] or NULL
+    const void* du;            // [B, L, D]
+    const float* dstate_out;   // [B, D, K-1] or NULL
+    void* dx;                  // [B, L, D]
+    float* dweight;            // [D, K]
+    float* dbias;              // [D] or NULL
+    float* dstate_in;          // [B, D, K-1] or NULL
+    int64_t B, L, D, K;
+    int silu;
+    int bf16;
+    int64_t blocks;            // token blocks per batch row
+    float* part;               // [B * blocks][K + 1][D]
+};
+
+int64_t conv_bwd_blocks(int64_t L);
+size_t conv_bwd_workspace_bytes(int64_t B, int64_t L, int64_t D, int64_t K);
+hipError_t launch_conv1d_bwd(const ConvBwdArgs& a, hipStream_t stream);
+
+// ---------------------------------------------------------------- column sums
+
+// out[j][c] = (sum over n rows of part[row][j][c]) (/ divide[c] for j = 0,
+// zero where divide[c] is zero), j < m, in a fixed order: the last step of the
+// parameters' gradients.  part: [n][m][D].  out[j] NULL: skipped.  strided:
+// out[0] is [D][m - 1] with the last sum in out[1] (the conv's weight layout).
+struct ColumnSums {
+    const float* part;
+    int64_t n, D;
+    int m;
+    float* out[3];
+    const float* divide;
+    int strided;
+};
+hipError_t launch_column_sums(const ColumnSums& a, hipStream_t stream);
+
+}  // namespace ssm

@@ -1,0 +1,232 @@
+// Backward pass of the short causal depthwise convolution + SiLU, which takes
+// the scan's input gradient du to the block's input.  With
+//   s_t = bias + sum_k w[k] x_{t-(K-1)+k},   u_t = s_t sigma(s_t)
+//   g_t  = du_t sigma(s_t) (1 + s_t (1 - sigma(s_t)))     (du_t without SiLU)
+//   dx_t = sum_k w[k] g_{t+(K-1)-k}                       (g = 0 behind the end)
+//   dw[k] = sum_t g_t x_{t-(K-1)+k},   dbias = sum_t g_t
+// and the K-1 inputs before t = 0 (the carried state) get their share of the
+// same sum.  Nothing of the forward is stored: s_t is formed again.  Per
+// element the call reads x and du and writes dx: it is bound by those bytes.
+//
+// A thread owns VEC channels and a run of tokens; it walks the run and the
+// K-1 tokens after it (whose g it needs for its last outputs) with the last
+// inputs and the last g in registers.
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+
+#include "block_internal.h"
+#include "gated_tile.h"
+#include "lane_ops.h"
+
+namespace ssm {
+namespace {
+
+constexpr int kWaves = 8;
+constexpr int kRun = 32;                        // tokens per thread
+constexpr int kBlockTokens = kWaves * kRun;     // a workgroup: 64 * VEC channels of these
+static_assert(kBlockTokens == 256, "conv_bwd_blocks counts blocks of 256 tokens");
+
+template <typename T, int VEC, int K, bool SILU>
+__global__ __launch_bounds__(kWaves * 64) void conv1d_bwd_kernel(ConvBwdArgs p) {
+    using V = Row<T, VEC>;
+    __shared__ float sSum[kWaves][K + 1][64 * VEC];
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    const int64_t dblocks = (p.D + 64 * VEC - 1) / (64 * VEC);
+    const int64_t db = blockIdx.x % dblocks;
+    const int64_t cell = blockIdx.x / dblocks;                  // b * blocks + block
+    const int64_t b = cell / p.blocks, block = cell % p.blocks;
+    const int64_t d0 = (db * 64 + lane) * VEC;
+    const bool in = d0 < p.D;
+    const int64_t t0 = block * kBlockTokens + wave * kRun;
+    const int64_t t1 = t0 + kRun < p.L ? t0 + kRun : p.L;       // t0 >= L: an empty run
+
+    float sum[K + 1][VEC];
+#pragma unroll
+    for (int k = 0; k <= K; ++k)
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) sum[k][c] = 0.0f;
+
+    if (in && t0 < p.L) {
+        const T* x = static_cast<const T*>(p.x) + b * p.L * p.D + d0;
+        const T* du = static_cast<const T*>(p.du) + b * p.L * p.D + d0;
+        T* dx = static_cast<T*>(p.dx) + b * p.L * p.D + d0;
+        float w[VEC][K], bias[VEC];
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) w[c][k] = p.weight[(d0 + c) * K + k];
+            bias[c] = p.bias ? p.bias[d0 + c] : 0.0f;
+        }
+        float win[K][VEC];         // x_{t-(K-1)} .. x_t
+        float g[K][VEC];           // g_{t-(K-1)} .. g_t
+#pragma unroll
+        for (int i = 0; i < K - 1; ++i) {
+            const int64_t t = t0 - (K - 1) + i;
+            if (t >= 0) {
+                V::unpack(V::load(x + t * p.D), win[i]);
+            } else {
+#pragma unroll
+                for (int c = 0; c < VEC; ++c)
+                    win[i][c] = p.state_in ? p.state_in[(b * p.D + d0 + c) * (K - 1) + (t + K - 1)] : 0.0f;
+            }
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) g[i][c] = 0.0f;
+        }
+        // token t's own part, then the output of token t - (K-1), whose last
+        // term it is
+        for (int64_t t = t0; t < t1 + K - 1; ++t) {
+            const bool there = t < p.L;
+            float y[VEC];
+            V::unpack(there ? V::load(x + t * p.D) : V::zero(), win[K - 1]);
+            V::unpack(there ? V::load(du + t * p.D) : V::zero(), y);
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) {
+                float v = y[c];
+                if (SILU) {
+                    float s = bias[c];
+#pragma unroll
+                    for (int k = 0; k < K; ++k) s = fmaf(w[c][k], win[k][c], s);
+                    const float e = fast_exp2(fminf(-s * kLog2e, 126.0f));
+                    const float sg = fast_rcp(1.0f + e);
+                    v *= sg * fmaf(s, e * sg, 1.0f);          // 1 - sigma = e sigma
+                }
+                if (!there) v = 0.0f;
+                g[K - 1][c] = v;
+                if (t < t1) {
+#pragma unroll
+                    for (int k = 0; k < K; ++k) sum[k][c] = fmaf(v, win[k][c], sum[k][c]);
+                    sum[K][c] += v;
+                }
+            }
+            const int64_t to = t - (K - 1);
+            if (to >= t0) {
+                float o[VEC];
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) {
+                    o[c] = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < K; ++k) o[c] = fmaf(w[c][k], g[K - 1 - k][c], o[c]);
+                    const int64_t slot = to + (K - 1) - p.L;        // in the state handed on
+                    if (p.dstate_out && slot >= 0)
+                        o[c] += p.dstate_out[(b * p.D + d0 + c) * (K - 1) + slot];
+                }
+                V::store(dx + to * p.D, o);
+            }
+#pragma unroll
+            for (int i = 0; i < K - 1; ++i)
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) {
+                    win[i][c] = win[i + 1][c];
+                    g[i][c] = g[i + 1][c];
+                }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k <= K; ++k)
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) sSum[wave][k][lane * VEC + c] = sum[k][c];
+    lds_barrier();
+    for (int i = threadIdx.x; i < (K + 1) * 64 * VEC; i += kWaves * 64) {
+        const int k = i / (64 * VEC), ch = i % (64 * VEC);
+        float s = 0.0f;
+#pragma unroll
+        for (int m = 0; m < kWaves; ++m) s += sSum[m][k][ch];
+        const int64_t d = db * 64 * VEC + ch;
+        if (d < p.D) p.part[(cell * (K + 1) + k) * p.D + d] = s;
+    }
+}
+
+// The carried state's gradient: slot j is the input at t = j - (K-1), which
+// reaches the first j + 1 tokens, and (when the call has fewer than K-1
+// tokens) the state that it hands on.  One thread per channel.
+template <typename T, int K, bool SILU>
+__global__ __launch_bounds__(256) void conv1d_bwd_state(ConvBwdArgs p) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= p.B * p.D) return;
+    const int64_t b = i / p.D, d = i % p.D;
+    const T* x = static_cast<const T*>(p.x) + b * p.L * p.D + d;
+    const T* du = static_cast<const T*>(p.du) + b * p.L * p.D + d;
+    float w[K], win[2 * K - 1], g[K];        // win: the state, then the first K-1 inputs
+#pragma unroll
+    for (int k = 0; k < K; ++k) w[k] = p.weight[d * K + k];
+#pragma unroll
+    for (int j = 0; j < 2 * (K - 1); ++j) {
+        const int64_t t = j - (K - 1);
+        win[j] = 0.0f;
+        if (t < 0) win[j] = p.state_in ? p.state_in[i * (K - 1) + j] : 0.0f;
+        else if (t < p.L) win[j] = Elem<T>::load(x, t * p.D);
+    }
+#pragma unroll
+    for (int t = 0; t < K - 1; ++t) {
+        g[t] = 0.0f;
+        if (t < p.L) {
+            float v = Elem<T>::load(du, t * p.D);
+            if (SILU) {
+                float s = p.bias ? p.bias[d] : 0.0f;
+#pragma unroll
+                for (int k = 0; k < K; ++k) s = fmaf(w[k], win[t + k], s);
+                const float e = fast_exp2(fminf(-s * kLog2e, 126.0f));
+                const float sg = fast_rcp(1.0f + e);
+                v *= sg * fmaf(s, e * sg, 1.0f);
+            }
+            g[t] = v;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) {
+        float o = 0.0f;
+#pragma unroll
+        for (int t = 0; t <= j; ++t) o = fmaf(w[j - t], g[t], o);
+        if (p.dstate_out && j >= p.L) o += p.dstate_out[i * (K - 1) + (j - p.L)];
+        p.dstate_in[i * (K - 1) + j] = o;
+    }
+}
+
+template <typename T, int VEC, int K, bool SILU>
+hipError_t launch_s(const ConvBwdArgs& a, hipStream_t stream) {
+    if (a.blocks > 0) {
+        const int64_t dblocks = (a.D + 64 * VEC - 1) / (64 * VEC);
+        conv1d_bwd_kernel<T, VEC, K, SILU>
+            <<<(unsigned)(dblocks * a.B * a.blocks), kWaves * 64, 0, stream>>>(a);
+    }
+    if constexpr (K > 1) {
+        if (a.dstate_in)
+            conv1d_bwd_state<T, K, SILU><<<(unsigned)((a.B * a.D + 255) / 256), 256, 0, stream>>>(a);
+    }
+    return hipGetLastError();
+}
+
+template <typename T, int VEC>
+hipError_t launch_v(const ConvBwdArgs& a, hipStream_t stream) {
+    switch (a.K * 2 + (a.silu ? 1 : 0)) {
+        case 2: return launch_s<T, VEC, 1, false>(a, stream);
+        case 3: return launch_s<T, VEC, 1, true>(a, stream);
+        case 4: return launch_s<T, VEC, 2, false>(a, stream);
+        case 5: return launch_s<T, VEC, 2, true>(a, stream);
+        case 6: return launch_s<T, VEC, 3, false>(a, stream);
+        case 7: return launch_s<T, VEC, 3, true>(a, stream);
+        case 8: return launch_s<T, VEC, 4, false>(a, stream);
+        default: return launch_s<T, VEC, 4, true>(a, stream);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_conv1d_bwd(const ConvBwdArgs& a, hipStream_t stream) {
+    hipError_t e;
+    if (a.bf16) e = launch_v<uint16_t, 1>(a, stream);
+    else e = launch_v<float, 1>(a, stream);
+    if (e != hipSuccess) return e;
+    ColumnSums s{};
+    s.part = a.part;
+    s.n = a.B * a.blocks;
+    s.D = a.D;
+    s.m = (int)a.K + 1;
+    s.out[0] = a.dweight;
+    s.out[1] = a.dbias;
+    s.strided = 1;
+    return launch_column_sums(s, stream);
+}
+
+}  // namespace ssm

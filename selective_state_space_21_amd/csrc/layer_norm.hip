@@ -1,0 +1,414 @@
+// Layer norm over the last axis, forward and backward, with the fp32 residual
+// stream's addition in front of it.  Per row s = x (+ residual):
+//   mu = mean(s), rstd = 1 / sqrt(mean((s - mu)^2) + eps),  n = (s - mu) rstd
+//   y  = n weight + bias
+// and backward, with v = dy weight:
+//   ds = rstd (v - mean(v) - n mean(v n)) (+ the gradient of s itself)
+//   dweight = sum over rows of dy n,   dbias = sum over rows of dy
+//
+// A row is read once and kept in registers: mean, then the mean square of the
+// differences from it (two passes over registers, so nothing cancels).  TPR
+// threads share a row (a wavefront, or a whole workgroup for long rows) and
+// each holds NV vectors of VEC elements, vector i of thread j being vector
+// i * TPR + j of the row.  Rows too long for that are read from memory again
+// for every pass.  Both directions are bound by the bytes they move.
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+
+#include "block_internal.h"
+#include "device_math.h"
+#include "gated_tile.h"
+#include "lane_ops.h"
+
+namespace ssm {
+namespace {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// VEC elements as fp32; 16-byte vectors for the activations, and for fp32
+// operands beside bf16 ones two of them
+template <typename T, int VEC> struct Lane;
+template <> struct Lane<uint16_t, 8> {
+    static __device__ __forceinline__ void load(const uint16_t* p, float (&v)[8]) {
+        const u32x4 r = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            v[2 * k] = __uint_as_float(r[k] << 16);
+            v[2 * k + 1] = __uint_as_float(r[k] & 0xffff0000u);
+        }
+    }
+    static __device__ __forceinline__ void store(uint16_t* p, const float (&v)[8]) {
+        u32x4 r;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            r[k] = (uint32_t)f32_to_bf16_bits(v[2 * k]) | ((uint32_t)f32_to_bf16_bits(v[2 * k + 1]) << 16);
+        __builtin_nontemporal_store(r, reinterpret_cast<u32x4*>(p));
+    }
+};
+template <> struct Lane<float, 8> {
+    static __device__ __forceinline__ void load(const float* p, float (&v)[8]) {
+        const f32x4 a = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p));
+        const f32x4 b = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p) + 1);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) { v[k] = a[k]; v[k + 4] = b[k]; }
+    }
+    static __device__ __forceinline__ void store(float* p, const float (&v)[8]) {
+        __builtin_nontemporal_store((f32x4){v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4*>(p));
+        __builtin_nontemporal_store((f32x4){v[4], v[5], v[6], v[7]}, reinterpret_cast<f32x4*>(p) + 1);
+    }
+};
+template <> struct Lane<float, 4> {
+    static __device__ __forceinline__ void load(const float* p, float (&v)[4]) {
+        Row<float, 4>::unpack(Row<float, 4>::load(p), v);
+    }
+    static __device__ __forceinline__ void store(float* p, const float (&v)[4]) {
+        Row<float, 4>::store(p, v);
+    }
+};
+template <typename T> struct Lane<T, 1> {
+    static __device__ __forceinline__ void load(const T* p, float (&v)[1]) {
+        Row<T, 1>::unpack(Row<T, 1>::load(p), v);
+    }
+    static __device__ __forceinline__ void store(T* p, const float (&v)[1]) { Row<T, 1>::store(p, v); }
+};
+
+// the parameters are read by every row: through the cache
+template <int VEC> __device__ __forceinline__ void load_param(const float* p, float (&v)[VEC], float none) {
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) v[k] = p ? p[k] : none;
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+    v += __shfl_xor(v, 32, 64);
+    v += lane_xor<16>(v);
+    v += lane_xor<8>(v);
+    v += lane_xor<4>(v);
+    v += lane_xor<2>(v);
+    v += lane_xor<1>(v);
+    return v;
+}
+
+// the sum over the TPR threads of a row, in all of them; `s` holds one float
+// per wavefront of the workgroup
+template <int TPR> __device__ __forceinline__ float row_sum(float v, float* s) {
+    v = wave_sum(v);
+    if constexpr (TPR > 64) {
+        constexpr int W = TPR / 64;
+        lds_barrier();                       // the previous sum has been read
+        if (threadIdx.x % 64 == 0) s[threadIdx.x / 64] = v;
+        lds_barrier();
+        v = s[0];
+#pragma unroll
+        for (int k = 1; k < W; ++k) v += s[k];
+    }
+    return v;
+}
+
+template <typename T, bool RES, int VEC, int NV, int TPR>
+__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd(NormArgs p) {
+    constexpr int kThreads = TPR > 256 ? TPR : 256;
+    __shared__ float s[kThreads / 64];
+    const int j = threadIdx.x % TPR;
+    const int64_t row = (int64_t)blockIdx.x * (kThreads / TPR) + threadIdx.x / TPR;
+    if (row >= p.rows) return;               // a whole wavefront (TPR = 64) or nobody
+    const int64_t o = row * p.D;
+    const T* x = static_cast<const T*>(p.x) + o;
+    float v[NV][VEC];
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int64_t d = (int64_t)(i * TPR + j) * VEC;
+        if (d < p.D) {
+            Lane<T, VEC>::load(x + d, v[i]);
+            if (RES) {
+                float r[VEC];
+                Lane<float, VEC>::load(p.residual + o + d, r);
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) v[i][k] += r[k];
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) v[i][k] = 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) sum += v[i][k];
+    }
+    const float inv = 1.0f / (float)p.D;
+    const float mean = row_sum<TPR>(sum, s) * inv;
+    sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if ((int64_t)(i * TPR + j) * VEC < p.D) {
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {
+                const float c = v[i][k] - mean;
+                sum = fmaf(c, c, sum);
+            }
+        }
+    }
+    const float rstd = 1.0f / sqrtf(fmaf(row_sum<TPR>(sum, s), inv, p.eps));
+    if (j == 0) {
+        if (p.mean) p.mean[row] = mean;
+        if (p.rstd) p.rstd[row] = rstd;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int64_t d = (int64_t)(i * TPR + j) * VEC;
+        if (d < p.D) {
+            if (RES && p.residual_out) Lane<float, VEC>::store(p.residual_out + o + d, v[i]);
+            float w[VEC], b[VEC];
+            load_param<VEC>(p.weight ? p.weight + d : nullptr, w, 1.0f);
+            load_param<VEC>(p.bias ? p.bias + d : nullptr, b, 0.0f);
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) v[i][k] = fmaf((v[i][k] - mean) * rstd, w[k], b[k]);
+            Lane<T, VEC>::store(static_cast<T*>(p.y) + o + d, v[i]);
+        }
+    }
+}
+
+// rows of any length: read again for each pass
+template <typename T, bool RES>
+__global__ __launch_bounds__(1024) void norm_fwd_long(NormArgs p) {
+    __shared__ float s[16];
+    const int64_t o = (int64_t)blockIdx.x * p.D;
+    const T* x = static_cast<const T*>(p.x) + o;
+    auto at = [&](int64_t d) {
+        const float v = Elem<T>::load(x, d);
+        return RES ? v + p.residual[o + d] : v;
+    };
+    const float inv = 1.0f / (float)p.D;
+    float sum = 0.0f;
+    for (int64_t d = threadIdx.x; d < p.D; d += 1024) sum += at(d);
+    const float mean = row_sum<1024>(sum, s) * inv;
+    sum = 0.0f;
+    for (int64_t d = threadIdx.x; d < p.D; d += 1024) {
+        const float c = at(d) - mean;
+        sum = fmaf(c, c, sum);
+    }
+    const float rstd = 1.0f / sqrtf(fmaf(row_sum<1024>(sum, s), inv, p.eps));
+    if (threadIdx.x == 0) {
+        if (p.mean) p.mean[blockIdx.x] = mean;
+        if (p.rstd) p.rstd[blockIdx.x] = rstd;
+    }
+    for (int64_t d = threadIdx.x; d < p.D; d += 1024) {
+        const float v = at(d);
+        if (RES && p.residual_out) p.residual_out[o + d] = v;
+        Elem<T>::store(static_cast<T*>(p.y) + o, d,
+                       fmaf((v - mean) * rstd, p.weight ? p.weight[d] : 1.0f,
+                            p.bias ? p.bias[d] : 0.0f));
+    }
+}
+
+// X: the type of the normalised input (the fp32 stream, or the activations'),
+// T: the activations' type.
+template <typename X, typename T, int VEC, int NV, int TPR>
+__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd(NormBwdArgs p) {
+    constexpr int kThreads = TPR > 256 ? TPR : 256;
+    constexpr int kRows = kThreads / TPR;
+    __shared__ float s[kThreads / 64];
+    __shared__ float join[kRows > 1 ? kRows - 1 : 1][TPR > 64 ? 1 : VEC][TPR];
+    const int j = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+    const float inv = 1.0f / (float)p.D;
+    float w[NV][VEC], dw[NV][VEC], db[NV][VEC];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int64_t d = (int64_t)(i * TPR + j) * VEC;
+        load_param<VEC>(p.weight && d < p.D ? p.weight + d : nullptr, w[i], 1.0f);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) dw[i][k] = db[i][k] = 0.0f;
+    }
+    for (int64_t row = (int64_t)blockIdx.x * kRows + sub; row < p.rows; row += p.groups * kRows) {
+        const int64_t o = row * p.D;
+        const float mean = p.mean[row], rstd = p.rstd[row];
+        float n[NV][VEC], v[NV][VEC];
+        float c1 = 0.0f, c2 = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int64_t d = (int64_t)(i * TPR + j) * VEC;
+            if (d < p.D) {
+                Lane<X, VEC>::load(static_cast<const X*>(p.x) + o + d, n[i]);
+                Lane<T, VEC>::load(static_cast<const T*>(p.dy) + o + d, v[i]);
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) {
+                    n[i][k] = (n[i][k] - mean) * rstd;
+                    dw[i][k] = fmaf(v[i][k], n[i][k], dw[i][k]);
+                    db[i][k] += v[i][k];
+                    v[i][k] *= w[i][k];
+                    c1 = fmaf(v[i][k], n[i][k], c1);
+                    c2 += v[i][k];
+                }
+            }
+        }
+        c1 = row_sum<TPR>(c1, s) * inv;
+        c2 = row_sum<TPR>(c2, s) * inv;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int64_t d = (int64_t)(i * TPR + j) * VEC;
+            if (d < p.D) {
+                float g[VEC];
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) g[k] = 0.0f;
+                if (p.dresidual_out) Lane<float, VEC>::load(p.dresidual_out + o + d, g);
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) g[k] = fmaf(rstd, v[i][k] - c2 - n[i][k] * c1, g[k]);
+                if (p.dresidual) Lane<float, VEC>::store(p.dresidual + o + d, g);
+                Lane<T, VEC>::store(static_cast<T*>(p.dx) + o + d, g);
+            }
+        }
+    }
+    // join the rows that ran side by side, then this workgroup's row of part
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            float (&a)[VEC] = which ? db[i] : dw[i];
+            if constexpr (kRows > 1) {
+                lds_barrier();
+                if (sub > 0) {
+#pragma unroll
+                    for (int k = 0; k < VEC; ++k) join[sub - 1][k][j] = a[k];
+                }
+                lds_barrier();
+                if (sub == 0) {
+#pragma unroll
+                    for (int m = 0; m < kRows - 1; ++m)
+#pragma unroll
+                        for (int k = 0; k < VEC; ++k) a[k] += join[m][k][j];
+                }
+            }
+            const int64_t d = (int64_t)(i * TPR + j) * VEC;
+            if (sub == 0 && d < p.D) {
+                float* out = p.part + ((int64_t)blockIdx.x * 2 + which) * p.D + d;
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) out[k] = a[k];
+            }
+        }
+    }
+}
+
+// rows of any length: dx row by row, then the parameters' sums column by column
+template <typename X, typename T>
+__global__ __launch_bounds__(1024) void norm_bwd_long(NormBwdArgs p) {
+    __shared__ float s[16];
+    const int64_t o = (int64_t)blockIdx.x * p.D;
+    const X* x = static_cast<const X*>(p.x) + o;
+    const T* dy = static_cast<const T*>(p.dy) + o;
+    const float mean = p.mean[blockIdx.x], rstd = p.rstd[blockIdx.x], inv = 1.0f / (float)p.D;
+    float c1 = 0.0f, c2 = 0.0f;
+    for (int64_t d = threadIdx.x; d < p.D; d += 1024) {
+        const float v = Elem<T>::load(dy, d) * (p.weight ? p.weight[d] : 1.0f);
+        c1 = fmaf(v, (Elem<X>::load(x, d) - mean) * rstd, c1);
+        c2 += v;
+    }
+    c1 = row_sum<1024>(c1, s) * inv;
+    c2 = row_sum<1024>(c2, s) * inv;
+    for (int64_t d = threadIdx.x; d < p.D; d += 1024) {
+        const float v = Elem<T>::load(dy, d) * (p.weight ? p.weight[d] : 1.0f);
+        const float n = (Elem<X>::load(x, d) - mean) * rstd;
+        const float g = fmaf(rstd, v - c2 - n * c1, p.dresidual_out ? p.dresidual_out[o + d] : 0.0f);
+        if (p.dresidual) p.dresidual[o + d] = g;
+        Elem<T>::store(static_cast<T*>(p.dx) + o, d, g);
+    }
+}
+
+template <typename X, typename T>
+__global__ __launch_bounds__(256) void norm_bwd_columns(NormBwdArgs p) {
+    const int64_t d = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t group = blockIdx.y;
+    if (d >= p.D) return;
+    float dw = 0.0f, db = 0.0f;
+    for (int64_t row = group; row < p.rows; row += p.groups) {
+        const float v = Elem<T>::load(static_cast<const T*>(p.dy), row * p.D + d);
+        const float n = (Elem<X>::load(static_cast<const X*>(p.x), row * p.D + d) - p.mean[row]) * p.rstd[row];
+        dw = fmaf(v, n, dw);
+        db += v;
+    }
+    p.part[(group * 2) * p.D + d] = dw;
+    p.part[(group * 2 + 1) * p.D + d] = db;
+}
+
+template <typename T, bool RES, int VEC, int NV, int TPR>
+hipError_t launch_fwd(const NormArgs& a, hipStream_t stream) {
+    constexpr int threads = TPR > 256 ? TPR : 256;
+    constexpr int rows = threads / TPR;
+    norm_fwd<T, RES, VEC, NV, TPR>
+        <<<(unsigned)((a.rows + rows - 1) / rows), threads, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+// the thread layout of a row of `nv` vectors
+template <typename T, bool RES, int VEC>
+hipError_t launch_fwd_v(const NormArgs& a, hipStream_t stream) {
+    const int64_t nv = a.D / VEC;
+    if (nv <= 64) return launch_fwd<T, RES, VEC, 1, 64>(a, stream);
+    if (nv <= 128) return launch_fwd<T, RES, VEC, 2, 64>(a, stream);
+    if (nv <= 256) return launch_fwd<T, RES, VEC, 4, 64>(a, stream);
+    if (nv <= 512) return launch_fwd<T, RES, VEC, 2, 256>(a, stream);
+    if (nv <= 1024) return launch_fwd<T, RES, VEC, 4, 256>(a, stream);
+    if (nv <= 2048) return launch_fwd<T, RES, VEC, 2, 1024>(a, stream);
+    if (nv <= 4096) return launch_fwd<T, RES, VEC, 4, 1024>(a, stream);
+    norm_fwd_long<T, RES><<<(unsigned)a.rows, 1024, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+template <typename T, int VEC>
+hipError_t launch_fwd_t(const NormArgs& a, hipStream_t stream) {
+    if (a.D % VEC == 0)
+        return a.residual ? launch_fwd_v<T, true, VEC>(a, stream) : launch_fwd_v<T, false, VEC>(a, stream);
+    return a.residual ? launch_fwd_v<T, true, 1>(a, stream) : launch_fwd_v<T, false, 1>(a, stream);
+}
+
+template <typename X, typename T, int VEC, int NV, int TPR>
+hipError_t launch_bwd(const NormBwdArgs& a, hipStream_t stream) {
+    norm_bwd<X, T, VEC, NV, TPR><<<(unsigned)a.groups, TPR > 256 ? TPR : 256, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+template <typename X, typename T, int VEC>
+hipError_t launch_bwd_v(const NormBwdArgs& a, hipStream_t stream) {
+    const int64_t nv = a.D / VEC;
+    if (nv <= 64) return launch_bwd<X, T, VEC, 1, 64>(a, stream);
+    if (nv <= 128) return launch_bwd<X, T, VEC, 2, 64>(a, stream);
+    if (nv <= 256) return launch_bwd<X, T, VEC, 1, 256>(a, stream);
+    if (nv <= 512) return launch_bwd<X, T, VEC, 2, 256>(a, stream);
+    if (nv <= 1024) return launch_bwd<X, T, VEC, 1, 1024>(a, stream);
+    if (nv <= 2048) return launch_bwd<X, T, VEC, 2, 1024>(a, stream);
+    norm_bwd_long<X, T><<<(unsigned)a.rows, 1024, 0, stream>>>(a);
+    norm_bwd_columns<X, T>
+        <<<dim3((unsigned)((a.D + 255) / 256), (unsigned)a.groups), 256, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+template <typename X, typename T, int VEC>
+hipError_t launch_bwd_t(const NormBwdArgs& a, hipStream_t stream) {
+    return a.D % VEC == 0 ? launch_bwd_v<X, T, VEC>(a, stream) : launch_bwd_v<X, T, 1>(a, stream);
+}
+
+}  // namespace
+
+hipError_t launch_layer_norm(const NormArgs& a, hipStream_t stream) {
+    if (a.rows == 0) return hipSuccess;
+    return a.bf16 ? launch_fwd_t<uint16_t, 8>(a, stream) : launch_fwd_t<float, 4>(a, stream);
+}
+
+hipError_t launch_layer_norm_bwd(const NormBwdArgs& a, hipStream_t stream) {
+    if (a.rows > 0) {
+        hipError_t e;
+        if (!a.bf16) e = launch_bwd_t<float, float, 4>(a, stream);
+        else if (a.x_bf16) e = launch_bwd_t<uint16_t, uint16_t, 8>(a, stream);
+        else e = launch_bwd_t<float, uint16_t, 8>(a, stream);
+        if (e != hipSuccess) return e;
+    }
+    if (!a.dweight && !a.dbias) return hipSuccess;
+    ColumnSums s{};
+    s.part = a.part;
+    s.n = a.rows > 0 ? a.groups : 0;
+    s.D = a.D;
+    s.m = 2;
+    s.out[0] = a.dweight;
+    s.out[1] = a.dbias;
+    return launch_column_sums(s, stream);
+}
+
+}  // namespace ssm

@@ -504,20 +504,21 @@ int ssm_causal_conv1d_silu_bwd(const void* x, const float* weight, const float* 
  *                    seq_lens[b] tokens (clamped to [0, L]); the padding is
  *                    not read, y there is left untouched, and h_last is the
  *                    state after the row's last token
- *   B, D >= 1; L >= 0; B * ceil(D / 64) below 2^25.
- * The sequence is walked in tiles of SSM_GATED_TILE tokens by 64 channels.
- * With enough of those strips of 64 channels to fill the GPU (or few tiles) a
+ *   B >= 1; 1 <= D <= 2^21; L >= 0; B * ceil(D / 64) below 2^25.
+ * The sequence is walked in tiles of 256 tokens by 64 channels (128 tokens in
+ * the backward).  With enough of those strips of 64 channels to fill the GPU (or few tiles) a
  * workgroup walks a strip alone; else several walk it together, each taking
  * the next tile, and hand the state on through the workspace (256-byte
  * aligned, 0 bytes for one walker; the call clears what it needs of it).
- * ssm_gated_scan_walkers returns their number (0 for invalid sizes), a pure
- * function of the sizes; the environment variable SSM_GATED_WALKERS (1..64)
+ * ssm_gated_scan_walkers and ssm_gated_scan_bwd_walkers return their number
+ * for the two directions (0 for invalid sizes), a pure function of the sizes; the environment variable SSM_GATED_WALKERS (1..64)
  * overrides it, for the queries and the calls.  Results do not depend on the
  * number of walkers, bit for bit.
  */
 #define SSM_GATED_TILE 128
 
 int ssm_gated_scan_walkers(int64_t B, int64_t L, int64_t D);
+int ssm_gated_scan_bwd_walkers(int64_t B, int64_t L, int64_t D);
 size_t ssm_gated_scan_workspace_bytes(int64_t B, int64_t L, int64_t D, int dtype);
 size_t ssm_gated_scan_ckpt_bytes(int64_t B, int64_t L, int64_t D, int dtype);
 

@@ -36,6 +36,13 @@ def _dev_tensor(name, t, dtype=None, device=None):
 def check_args(device, *specs) -> None:
     """specs: (name, tensor or None, expected shape, dtype).  Types, shapes and
     dtypes of every argument are checked first, then device and contiguity."""
+    for _name, t, shape, dtype in specs:      # all as they should be: one pass
+        if t is not None and not (
+                isinstance(t, torch.Tensor) and t.shape == shape and (dtype is None or t.dtype is dtype)
+                and t.is_cuda and (device is None or t.device == device) and t.is_contiguous()):
+            break
+    else:
+        return
     for name, t, shape, dtype in specs:
         if t is None:
             continue

@@ -73,6 +73,7 @@ SIGNATURES = {
     "ssm_causal_conv1d_silu_bwd": (_i, [_vp] * 4 + [_i] + [_vp] * 6 + [_i64] * 4 +
                                    [_i, _vp, _sz, _vp]),
     "ssm_gated_scan_walkers": (_i, [_i64] * 3),
+    "ssm_gated_scan_bwd_walkers": (_i, [_i64] * 3),
     "ssm_gated_scan_workspace_bytes": (_sz, [_i64] * 3 + [_i]),
     "ssm_gated_scan_ckpt_bytes": (_sz, [_i64] * 3 + [_i]),
     "ssm_gated_scan_fwd": (_i, [_vp] * 11 + [_i64] * 3 + [_i, _vp, _sz, _vp]),

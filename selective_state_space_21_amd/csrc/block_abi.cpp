@@ -37,9 +37,10 @@ int gated_check_sizes(int64_t B, int64_t L, int64_t D, int dtype) {
     if (B < 1 || D < 1 || L < 0) return SSM_ERR_BAD_SHAPE;
     if (mul(mul(B, D), L) < 0 || mul(B, D) < 0 || L > kMaxElems) return SSM_ERR_BAD_SHAPE;
     const int64_t strips = mul(B, (D + ssm::gated::kStrip - 1) / ssm::gated::kStrip);
-    const int64_t tiles = (L + ssm::gated::kTile - 1) / ssm::gated::kTile;
+    const int64_t tiles = (L + ssm::gated::kBwdTile - 1) / ssm::gated::kBwdTile;
+    if (D > (int64_t(1) << 21)) return SSM_ERR_UNSUPPORTED;          // a tile within 32-bit offsets
     if (strips < 0 || strips > kMaxGrid / ssm::gated::kMaxWalkers) return SSM_ERR_UNSUPPORTED;
-    if (tiles > kMaxGrid) return SSM_ERR_UNSUPPORTED;               // tile numbers are 32-bit
+    if (tiles > (int64_t(1) << 30)) return SSM_ERR_UNSUPPORTED;     // drawn from a 32-bit counter
     if (mul(mul(strips, tiles), 64 * 16) < 0 || mul(mul(B, tiles), mul(D, 32)) < 0)
         return SSM_ERR_BAD_SHAPE;
     return SSM_OK;
@@ -77,17 +78,22 @@ extern "C" {
 
 int ssm_gated_scan_walkers(int64_t B, int64_t L, int64_t D) {
     if (gated_check_sizes(B, L, D, SSM_F32) != SSM_OK) return 0;
-    return ssm::plan_gated(B, L, D).walkers;
+    return ssm::plan_gated_fwd(B, L, D).walkers;
+}
+
+int ssm_gated_scan_bwd_walkers(int64_t B, int64_t L, int64_t D) {
+    if (gated_check_sizes(B, L, D, SSM_F32) != SSM_OK) return 0;
+    return ssm::plan_gated_bwd(B, L, D).walkers;
 }
 
 size_t ssm_gated_scan_workspace_bytes(int64_t B, int64_t L, int64_t D, int dtype) {
     if (gated_check_sizes(B, L, D, dtype) != SSM_OK) return 0;
-    return ssm::plan_gated(B, L, D).chain_bytes;
+    return ssm::plan_gated_fwd(B, L, D).chain_bytes;
 }
 
 size_t ssm_gated_scan_ckpt_bytes(int64_t B, int64_t L, int64_t D, int dtype) {
     if (gated_check_sizes(B, L, D, dtype) != SSM_OK) return 0;
-    return (size_t)(B * ssm::plan_gated(B, L, D).tiles * D * 4);
+    return (size_t)(B * ssm::gated_saved(L) * D * 4);
 }
 
 int ssm_gated_scan_fwd(const void* x, const void* gate_a, const void* gate_x, const float* A,
@@ -102,7 +108,8 @@ int ssm_gated_scan_fwd(const void* x, const void* gate_a, const void* gate_x, co
     if (!all_aligned({x, gate_a, gate_x, y, ckpt}, 16)) return SSM_ERR_MISALIGNED;
     if (!all_aligned({A, bias_a, bias_x, h0, h_last, seq_lens}, 4)) return SSM_ERR_MISALIGNED;
     ssm::GatedArgs a{};
-    a.plan = ssm::plan_gated(B, L, D);
+    a.plan = ssm::plan_gated_fwd(B, L, D);
+    a.saved = ssm::gated_saved(L);
     if (a.plan.chain_bytes) {
         if (!workspace || workspace_bytes < a.plan.chain_bytes) return SSM_ERR_WORKSPACE;
         if (!aligned(workspace, 256)) return SSM_ERR_MISALIGNED;
@@ -142,7 +149,9 @@ int ssm_gated_scan_bwd(const void* x, const void* gate_a, const void* gate_x, co
         if (!workspace || workspace_bytes < need) return SSM_ERR_WORKSPACE;
         if (!aligned(workspace, 256)) return SSM_ERR_MISALIGNED;
     }
-    a.f.plan = ssm::plan_gated(B, L, D);
+    a.f.plan = ssm::plan_gated_fwd(B, L, D);
+    a.f.saved = ssm::gated_saved(L);
+    a.plan = ssm::plan_gated_bwd(B, L, D);
     a.f.x = x; a.f.gate_a = gate_a; a.f.gate_x = gate_x; a.f.A = A; a.f.bias_a = bias_a;
     a.f.bias_x = bias_x; a.f.h0 = h0; a.f.ckpt = const_cast<float*>(ckpt);
     a.f.seq_lens = seq_lens; a.f.B = B; a.f.L = L; a.f.D = D; a.f.bf16 = dtype == SSM_BF16;

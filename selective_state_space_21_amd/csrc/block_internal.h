@@ -15,24 +15,35 @@ namespace ssm {
 
 // Tiling the planner shares with the kernels.
 namespace gated {
-constexpr int kTile = SSM_GATED_TILE;   // tokens per tile (and per saved state)
+constexpr int kFwdTile = 256;           // tokens per tile of the forward walk
+constexpr int kBwdTile = SSM_GATED_TILE;   // of the backward walk, which starts from saved states
+static_assert(kFwdTile % SSM_GATED_TILE == 0, "a forward tile holds whole saved states");
 constexpr int kStrip = 64;              // channels per strip: one workgroup's width
-constexpr int kThreads = 512;
+constexpr int kFwdThreads = 1024;
+constexpr int kBwdThreads = 1024;
 constexpr int kMaxWalkers = 64;         // workgroups per strip at most
+constexpr int kBack = 8;                // tiles a walker looks back over for a known state
+// What the walkers of a call share, in order: a counter per strip; a map (8
+// bytes) per slot; a state (4 bytes) per slot.  A strip has a slot per channel
+// and tile, and kBack - 1 empty tiles in front.
+__host__ __device__ constexpr int64_t chain_head(int64_t strips) { return (strips * 4 + 255) / 256 * 256; }
+__host__ __device__ constexpr int64_t chain_slots(int64_t tiles) { return (tiles + kBack - 1) * kStrip; }
 }  // namespace gated
 
 // How a call walks the sequence: every strip (64 channels of one batch row)
-// is a chain of 128-token tiles, walked by `walkers` workgroups.
+// is a chain of tiles, walked by `walkers` workgroups.
 struct GatedPlan {
     int64_t strips;        // B * ceil(D / 64)
     int64_t dblocks;       // ceil(D / 64)
-    int64_t tiles;         // ceil(L / 128)
+    int64_t tiles;         // ceil(L / tile)
     int walkers;           // 1: a workgroup walks its strip alone, nothing is shared
     size_t chain_bytes;    // what the walkers of a strip share (0 for one)
 };
 
 // A pure function of the sizes (and the SSM_GATED_WALKERS override).
-GatedPlan plan_gated(int64_t B, int64_t L, int64_t D);
+GatedPlan plan_gated_fwd(int64_t B, int64_t L, int64_t D);
+GatedPlan plan_gated_bwd(int64_t B, int64_t L, int64_t D);
+inline int64_t gated_saved(int64_t L) { return (L + SSM_GATED_TILE - 1) / SSM_GATED_TILE; }
 
 struct GatedArgs {
     const void* x;
@@ -44,16 +55,19 @@ struct GatedArgs {
     const float* h0;
     void* y;               // NULL: states only
     float* h_last;
-    float* ckpt;           // [B, tiles, D] or NULL
+    float* ckpt;           // [B, saved, D] or NULL
+    int64_t saved;         // ceil(L / SSM_GATED_TILE)
     const int32_t* seq_lens;
     int64_t B, L, D;
     int bf16;
     GatedPlan plan;
     void* chain;           // plan.chain_bytes, or NULL
+    bool cleared;          // the caller has zeroed it
 };
 
 struct GatedBwdArgs {
-    GatedArgs f;           // the forward call's inputs; f.ckpt holds the saved states
+    GatedArgs f;           // the forward call's inputs and plan; f.ckpt holds the saved states
+    GatedPlan plan;
     const void* dy;
     const float* dh_last;
     void* dx;
@@ -65,12 +79,14 @@ struct GatedBwdArgs {
     float* dh0;
     bool own_ckpt;         // f.ckpt lies in the workspace and the call fills it first
     void* chain;           // the adjoint's, apart from the forward sweep's f.chain
-    float* part;           // [B * tiles][3][D]: a tile's sums for dA, dbias_a, dbias_x
+    float* part;           // [B * plan.tiles][3][D]: a tile's sums for dA, dbias_a, dbias_x
 };
 
 size_t gated_bwd_workspace_bytes(int64_t B, int64_t L, int64_t D, bool own_ckpt);
 void gated_bwd_carve(GatedBwdArgs& a, void* workspace);
 
+// Zeroes what the walkers of a call share (bytes: a multiple of 16).
+hipError_t launch_chain_clear(void* chain, size_t bytes, hipStream_t stream);
 hipError_t launch_gated_fwd(const GatedArgs& a, hipStream_t stream);
 hipError_t launch_gated_bwd(const GatedBwdArgs& a, hipStream_t stream);
 

@@ -27,9 +27,18 @@ constexpr int kRun = 32;                        // tokens per thread
 constexpr int kBlockTokens = kWaves * kRun;     // a workgroup: 64 * VEC channels of these
 static_assert(kBlockTokens == 256, "conv_bwd_blocks counts blocks of 256 tokens");
 
+template <typename T, int VEC> struct Vec;
+template <typename T> struct Vec<T, 1> {
+    using Raw = T;
+    static __device__ __forceinline__ Raw load(const T* p) { return __builtin_nontemporal_load(p); }
+    static __device__ __forceinline__ Raw zero() { return Raw(0); }
+    static __device__ __forceinline__ void unpack(const Raw& r, float (&v)[1]) { v[0] = Elem<T>::load(&r, 0); }
+    static __device__ __forceinline__ void store(T* p, const float (&v)[1]) { Elem<T>::store(p, 0, v[0]); }
+};
+
 template <typename T, int VEC, int K, bool SILU>
 __global__ __launch_bounds__(kWaves * 64) void conv1d_bwd_kernel(ConvBwdArgs p) {
-    using V = Row<T, VEC>;
+    using V = Vec<T, VEC>;
     __shared__ float sSum[kWaves][K + 1][64 * VEC];
     const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
     const int64_t dblocks = (p.D + 64 * VEC - 1) / (64 * VEC);

@@ -26,207 +26,352 @@ namespace ssm {
 namespace {
 
 using gated::kStrip;
-using gated::kThreads;
-using gated::kTile;
+constexpr int kThreads = gated::kBwdThreads;
+constexpr int kTile = gated::kBwdTile;
 constexpr int kWaves = kThreads / 64;
 
-template <typename T, int V>
+template <typename T, int V, bool CHAIN>
 __global__ __launch_bounds__(kThreads, 4) void gated_bwd(GatedBwdArgs q) {
-    using S = TileShape<V>;
+    using S = TileShape<V, kTile, kThreads>;
     using RowT = Row<T, V>;
     constexpr int R = S::kRun;
     const GatedArgs& p = q.f;
-    __shared__ __attribute__((aligned(16))) float sA[2][S::kGroups][kStrip];   // decay before the group
-    __shared__ __attribute__((aligned(16))) float sH[2][S::kGroups][kStrip];   // state entering it
-    __shared__ __attribute__((aligned(16))) float sQ[2][S::kGroups][kStrip];   // adjoint entering it
-    __shared__ float sSum[kWaves][3][kStrip];
+    // per wavefront and channel, two copies by turns: the pair of its tokens,
+    // then the pair from the tile's start to it (sA, sH); the adjoint's
+    // offset, then its pair from the tile's end to it (sP, sQ)
+    __shared__ __attribute__((aligned(16))) float sA[2][S::kWaves][kStrip];
+    __shared__ __attribute__((aligned(16))) float sH[2][S::kWaves][kStrip];
+    __shared__ __attribute__((aligned(16))) float sQ[2][S::kWaves][kStrip];
+    __shared__ __attribute__((aligned(16))) float sP[2][S::kWaves][kStrip];
+    __shared__ __attribute__((aligned(16))) float sS[2][kStrip];   // state entering the tile
+    __shared__ __attribute__((aligned(16))) float sC[2][kStrip];   // adjoint entering it
+    __shared__ float sSum[2][kWaves][3][kStrip];                   // wavefronts' sums of a tile
+    __shared__ int sNext[2];
 
-    const int tid = threadIdx.x, wave = tid / 64;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / 64), lane = tid % 64;
     const int c = tid % S::kLanes, g = tid / S::kLanes;
-    const int64_t strip = blockIdx.x;
-    const int64_t b = strip / p.plan.dblocks;
-    const int64_t ds = (strip % p.plan.dblocks) * kStrip;
-    const int64_t d = ds + c * V;
-    const bool in = d < p.D;
+    const int64_t strip = CHAIN ? blockIdx.x % (unsigned)q.plan.strips : blockIdx.x;
+    const int64_t b = strip / q.plan.dblocks;
+    const int64_t ds = (strip % q.plan.dblocks) * kStrip;
+    const int left = (int)(p.D - ds < kStrip ? p.D - ds : kStrip);  // the strip's channels
+    const bool in = c * V < left;
     const int64_t len = row_tokens(p, b);
-    const int64_t last = len > 0 ? (len - 1) / kTile : 0;
+    const int last = len > 0 ? (int)((len - 1) / kTile) : 0;       // the walk starts there
 
-    float A[V], ba[V], bx[V];
+    GatedChannel ch[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        A[v] = in ? p.A[d + v] : 0.0f;
-        ba[v] = in && p.bias_a ? p.bias_a[d + v] : 0.0f;
-        bx[v] = in && p.bias_x ? p.bias_x[d + v] : 0.0f;
+        const int64_t d = ds + c * V + v;
+        ch[v] = gated_channel(in ? p.A[d] : 0.0f, in && p.bias_a ? p.bias_a[d] : 0.0f,
+                              in && p.bias_x ? p.bias_x[d] : 0.0f);
     }
-    const int64_t row0 = b * p.L * p.D + d;
-    const T* x = static_cast<const T*>(p.x) + row0;
-    const T* ga = static_cast<const T*>(p.gate_a) + row0;
-    const T* gx = static_cast<const T*>(p.gate_x) + row0;
-    const T* dy = static_cast<const T*>(q.dy) + row0;
-    T* dx = static_cast<T*>(q.dx) + row0;
-    T* dga = static_cast<T*>(q.dgate_a) + row0;
-    T* dgx = static_cast<T*>(q.dgate_x) + row0;
+    const uint32_t pitch = (uint32_t)(p.D * sizeof(T));
+    const uint32_t off = in ? (uint32_t)(g * R) * pitch + (uint32_t)((ds + c * V) * sizeof(T)) : kNoChannel;
+    const bool keeper = lane < left;             // a folding lane has channel ds + lane
+    // a strip's row of a [rows][D] fp32 tensor; the lane is added last, to a
+    // uniform address
+    auto row = [&](auto* base, int64_t r) { return base + (r * p.D + ds); };
+    const uint32_t ul = lane;
 
-    const int64_t dc = ds + tid;
-    const bool keeper = tid < kStrip && dc < p.D;
-    float carry = keeper && q.dh_last ? q.dh_last[b * p.D + dc] : 0.0f;
-
-    for (int64_t tile = p.plan.tiles - 1; tile >= 0; --tile) {
-        const int buf = tile & 1;
-        const int64_t t0 = tile * kTile + g * R;
-        const int64_t cell = b * p.plan.tiles + tile;
-        if (tile > last) {                       // behind the row's end: zeros
-            const float z[V] = {};
-#pragma unroll
-            for (int j = 0; j < R; ++j) {
-                if (in && t0 + j < p.L) {
-                    const int64_t o = (t0 + j) * p.D;
-                    RowT::store(dx + o, z);
-                    RowT::store(dga + o, z);
-                    RowT::store(dgx + o, z);
-                }
-            }
-            if (keeper)
-                for (int k = 0; k < 3; ++k) q.part[(cell * 3 + k) * p.D + dc] = 0.0f;
-            continue;
-        }
-        typename RowT::Raw rx[R], ra[R], rg[R], ry[R];
+    // tiles behind the row's end: zeros
+    for (int64_t t = last + 1 + (CHAIN ? blockIdx.x / (unsigned)q.plan.strips : 0); t < q.plan.tiles;
+         t += q.plan.walkers) {
+        const __amdgpu_buffer_rsrc_t ox = tile_rows<T>(q.dx, p, b, t * kTile, p.L, kTile);
+        const __amdgpu_buffer_rsrc_t oa = tile_rows<T>(q.dgate_a, p, b, t * kTile, p.L, kTile);
+        const __amdgpu_buffer_rsrc_t og = tile_rows<T>(q.dgate_x, p, b, t * kTile, p.L, kTile);
+        const float z[V] = {};
 #pragma unroll
         for (int j = 0; j < R; ++j) {
-            const bool ok = in && t0 + j < len;
-            const int64_t o = (t0 + j) * p.D;
-            rx[j] = ok ? RowT::load(x + o) : RowT::zero();
-            ra[j] = ok ? RowT::load(ga + o) : RowT::zero();
-            rg[j] = ok ? RowT::load(gx + o) : RowT::zero();
-            ry[j] = ok ? RowT::load(dy + o) : RowT::zero();
+            RowT::store(ox, off + j * pitch, z);
+            RowT::store(oa, off + j * pitch, z);
+            RowT::store(og, off + j * pitch, z);
         }
-        const float first = keeper ? p.ckpt[cell * p.D + dc] : 0.0f;
-        // forward pair and adjoint offset of the thread's run
-        float a[R][V], w[R][V], r[R][V], i[R][V], e1[R][V], e2[R][V];
-        float pa[V], ph[V], pq[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) { pa[v] = 1.0f; ph[v] = 0.0f; pq[v] = 0.0f; }
+        if (wave < 3 && keeper) row(q.part, (b * q.plan.tiles + t) * 3 + wave)[ul] = 0.0f;
+    }
+
+    // wavefront 0 folds the states; wavefront kKeep folds the adjoint, hands
+    // it on and waits for it
+    constexpr int kKeep = kWaves - 1;
+    const bool drawer = tid == kKeep * 64;
+    float carry = wave == kKeep && keeper && q.dh_last ? row(q.dh_last, b)[ul] : 0.0f;
+    typename RowT::Raw rx[R], ra[R], rg[R], ry[R], nx[R], na[R], ng[R], ny[R];
+    float first = 0.0f;                          // wavefront 0: the saved state before the tile
+    auto load = [&](int tile) {
+        const int64_t t = (int64_t)tile * kTile;
+        const int64_t end = tile < 0 ? t : len;
+        const __amdgpu_buffer_rsrc_t bx = tile_rows<T>(p.x, p, b, t, end, kTile);
+        const __amdgpu_buffer_rsrc_t ba = tile_rows<T>(p.gate_a, p, b, t, end, kTile);
+        const __amdgpu_buffer_rsrc_t bg = tile_rows<T>(p.gate_x, p, b, t, end, kTile);
+        const __amdgpu_buffer_rsrc_t by = tile_rows<T>(q.dy, p, b, t, end, kTile);
 #pragma unroll
         for (int j = 0; j < R; ++j) {
-            float xv[V], av[V], gv[V];
-            RowT::unpack(rx[j], xv);
+            na[j] = RowT::load(ba, off + j * pitch);
+            ny[j] = RowT::load(by, off + j * pitch);
+        }
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            ng[j] = RowT::load(bg, off + j * pitch);
+            nx[j] = RowT::load(bx, off + j * pitch);
+        }
+        if (wave == 0 && keeper && tile >= 0) first = row(p.ckpt, b * p.saved + tile)[ul];
+    };
+    auto advance = [&]() {
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            rx[j] = nx[j];
+            ra[j] = na[j];
+            rg[j] = ng[j];
+            ry[j] = ny[j];
+        }
+    };
+    // the sums of the tile before: wavefronts' shares in order
+    auto put_sums = [&](int buf, int tile) {
+        if (wave < 3 && keeper) {
+            float t = 0.0f;
+#pragma unroll
+            for (int m = 0; m < kWaves; ++m) t += sSum[buf][m][wave][lane];
+            row(q.part, (b * q.plan.tiles + tile) * 3 + wave)[ul] = t;
+        }
+    };
+
+    const Chain chain = CHAIN ? chain_of(q.chain, q.plan, strip) : Chain{};
+    int tile = last, drawn = last - 1;           // drawn: the tile after this one
+    if (CHAIN) {
+        if (drawer) {
+            sNext[1] = chain_draw(chain);
+            drawn = chain_draw(chain);
+        }
+        lds_barrier();
+        tile = last - __builtin_amdgcn_readfirstlane(sNext[1]);
+        drawn = last - drawn;
+    }
+    int before = -1;                             // the tile whose sums are still in LDS
+    if (tile >= 0) load(tile);
+    int buf = 0;
+    for (; tile >= 0; buf ^= 1) {
+        advance();
+        const int64_t t0 = (int64_t)tile * kTile;
+        // what the adjoint's recurrence needs comes first, so that its map is
+        // up, and the state before it on its way, while the rest is computed
+        float a[R][V], y[R][V], cr[R][V], pa[V], pq[V];
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            float av[V];
             RowT::unpack(ra[j], av);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float e = exp_neg_finite(av[v], ch[v].ba), r = sigma_of(e);
+                y[j][v] = ch[v].A2 * r;
+                a[j][v] = fast_exp2(y[j][v]);
+                cr[j][v] = e * r;                // 1 - r
+            }
+        }
+        const bool ragged = t0 + kTile > len;    // tokens that do not exist: the adjoint passes
+        if (ragged) {
+#pragma unroll
+            for (int j = 0; j < R; ++j)
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    if (t0 + g * R + j >= len) {
+                        a[j][v] = 1.0f;
+                        y[j][v] = 0.0f;
+                    }
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            pa[v] = 1.0f;
+            pq[v] = 0.0f;
+        }
+#pragma unroll
+        for (int j = R - 1; j >= 0; --j) {
+            float dy[V];
+            RowT::unpack(ry[j], dy);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                pa[v] *= a[j][v];
+                pq[v] = a[j][v] * (dy[v] + pq[v]);
+            }
+        }
+        // a wavefront's two runs to one map; the lower one starts behind the
+        // upper (op, oq), and in the states the upper behind the lower (op, oh)
+        float op[V], oq[V], oh[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            op[v] = 1.0f;
+            oq[v] = 0.0f;
+            if constexpr (S::kPair) {
+                op[v] = __shfl_xor(pa[v], 32, 64);
+                oq[v] = __shfl_xor(pq[v], 32, 64);
+                pq[v] = fmaf(pa[v], oq[v], pq[v]);   // right in the lower half, which stores it
+                pa[v] *= op[v];
+            }
+        }
+        if (lane < S::kLanes) {
+            lds_put<V>(&sA[buf][wave][c * V], pa);
+            lds_put<V>(&sQ[buf][wave][c * V], pq);
+        }
+        if (drawer) sNext[buf] = CHAIN ? drawn : tile - 1;
+        lds_barrier();
+        const int next = __builtin_amdgcn_readfirstlane(sNext[buf]);
+        if (before >= 0) put_sums(buf ^ 1, before);
+        const int pos = last - tile;             // tiles walked before this one
+        float P = 1.0f, Q = 0.0f;
+        if (wave == kKeep) {
+#pragma unroll
+            for (int k = S::kWaves - 1; k >= 0; --k) {
+                const float ka = sA[buf][k][lane], kq = sQ[buf][k][lane];
+                sP[buf][k][lane] = P;
+                sQ[buf][k][lane] = Q;
+                Q = fmaf(ka, Q, kq);
+                P *= ka;
+            }
+            if (CHAIN && pos > 0 && tile > 0) chain_put_map(chain, pos, ul, P, Q);
+        }
+        // the weighted inputs, for the state's map; what else the gradients
+        // need of them is formed again behind the barriers, which costs less
+        // than the registers to keep it in
+        float ph[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) ph[v] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            float xv[V], gv[V];
+            RowT::unpack(rx[j], xv);
             RowT::unpack(rg[j], gv);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                e1[j][v] = exp_neg(av[v] + ba[v]);
-                e2[j][v] = exp_neg(gv[v] + bx[v]);
-                r[j][v] = sigma_of(e1[j][v]);
-                i[j][v] = sigma_of(e2[j][v]);
-                const float la = A[v] * r[j][v];
-                a[j][v] = fast_exp2(la * kLog2e);
-                w[j][v] = __builtin_amdgcn_sqrtf(one_minus_sq(la, a[j][v]));
-                float h = w[j][v] * (i[j][v] * xv[v]);
-                if (t0 + j >= len) { a[j][v] = 1.0f; h = 0.0f; }
-                pa[v] *= a[j][v];
-                ph[v] = fmaf(a[j][v], ph[v], h);
+                const float i = sigma_of(exp_neg(gv[v], ch[v].bx));
+                const float w = __builtin_amdgcn_sqrtf(one_minus_sq(y[j][v], a[j][v]));
+                ph[v] = fmaf(a[j][v], ph[v], w * (i * xv[v]));
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            oh[v] = 0.0f;
+            if constexpr (S::kPair) {
+                oh[v] = __shfl_xor(ph[v], 32, 64);
+                ph[v] = fmaf(op[v], ph[v], oh[v]);
             }
         }
-#pragma unroll
-        for (int j = R - 1; j >= 0; --j) {
-            float yv[V];
-            RowT::unpack(ry[j], yv);
-#pragma unroll
-            for (int v = 0; v < V; ++v) pq[v] = a[j][v] * (yv[v] + pq[v]);
-        }
-        lds_put<V>(&sA[buf][g][c * V], pa);
-        lds_put<V>(&sH[buf][g][c * V], ph);
-        lds_put<V>(&sQ[buf][g][c * V], pq);
+        if (lane < S::kLanes) lds_put<V>(&sH[buf][wave][c * V], ph);
         lds_barrier();
-        if (tid < kStrip) {
-            float H = first;
-#pragma unroll 8
-            for (int k = 0; k < S::kGroups; ++k) {
-                const float kh = sH[buf][k][tid];
-                sH[buf][k][tid] = H;
-                H = fmaf(sA[buf][k][tid], H, kh);
-            }
-#pragma unroll 8
-            for (int k = S::kGroups - 1; k >= 0; --k) {
-                const float kq = sQ[buf][k][tid];
-                sQ[buf][k][tid] = carry;
-                carry = fmaf(sA[buf][k][tid], carry, kq);
-            }
-            if (keeper && tile == 0 && q.dh0) q.dh0[b * p.D + dc] = carry;
-        }
-        lds_barrier();
-        float h[V], G[V], before[R][V], sum[3][V];
-        lds_get<V>(&sH[buf][g][c * V], h);
-        lds_get<V>(&sQ[buf][g][c * V], G);
+        if (wave == 0) {
+            float Ps = 1.0f, H = 0.0f;
 #pragma unroll
-        for (int v = 0; v < V; ++v) sum[0][v] = sum[1][v] = sum[2][v] = 0.0f;
+            for (int k = 0; k < S::kWaves; ++k) {
+                const float ka = sA[buf][k][lane], kh = sH[buf][k][lane];
+                sA[buf][k][lane] = Ps;
+                sH[buf][k][lane] = H;
+                H = fmaf(ka, H, kh);
+                Ps *= ka;
+            }
+            sS[buf][lane] = first;
+        } else if (wave == kKeep) {
+            if (CHAIN && pos > 0) carry = chain_state_before(chain, pos, lane);
+            sC[buf][lane] = carry;
+            carry = fmaf(P, carry, Q) + 0.0f;    // -0 is 0
+            if (CHAIN && tile > 0) chain_put_state(chain, pos, ul, carry);
+            if (keeper && tile == 0 && q.dh0) row(q.dh0, b)[ul] = carry;
+        }
+        load(next);                              // after the chain: loads return in order
+        if (CHAIN && drawer) drawn = last - chain_draw(chain);
+        lds_barrier();
+        const bool upper = lane >= 32;
+        float s[V], sp[V], sh[V];                // the state before the thread's run
+        lds_get<V>(&sS[buf][c * V], s);
+        lds_get<V>(&sA[buf][wave][c * V], sp);
+        lds_get<V>(&sH[buf][wave][c * V], sh);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            s[v] = fmaf(sp[v], s[v], sh[v]);
+            if (S::kPair && upper) s[v] = fmaf(op[v], s[v], oh[v]);
+        }
+        float G[V], gp[V], gq[V], sum[3][V];
+        lds_get<V>(&sC[buf][c * V], G);
+        lds_get<V>(&sP[buf][wave][c * V], gp);
+        lds_get<V>(&sQ[buf][wave][c * V], gq);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            G[v] = fmaf(gp[v], G[v], gq[v]);
+            if (S::kPair && !upper) G[v] = fmaf(op[v], G[v], oq[v]);
+            sum[0][v] = sum[1][v] = sum[2][v] = 0.0f;
+        }
+        // E = G ef, dgate_a = E (1 - r), dx = G wi, dgate_x = G hc; ef needs the
+        // state before the token: left to right
+        float ef[R][V], wi[R][V], hc[R][V];
 #pragma unroll
         for (int j = 0; j < R; ++j) {
-            float xv[V];
+            float xv[V], gv[V];
+            asm volatile("" : "+v"(rg[j]));          // not the values from before the barriers
             RowT::unpack(rx[j], xv);
+            RowT::unpack(rg[j], gv);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                before[j][v] = h[v];
-                h[v] = fmaf(a[j][v], h[v], w[j][v] * (i[j][v] * xv[v]));
+                asm volatile("" : "+v"(y[j][v]));
+                const float e = exp_neg_finite(gv[v], ch[v].bx), i = sigma_of(e);
+                const float w2 = one_minus_sq(y[j][v], a[j][v]);
+                const float w = __builtin_amdgcn_sqrtf(w2);
+                const float h = w * (i * xv[v]);
+                // (la / w) a^2 i x = (la a / w^2) a b, whose first factor is at
+                // most a half; where w^2 leaves fp32's range, so does the term
+                const float ya = y[j][v] * (kLn2 * a[j][v]);
+                const float s2 = w2 > 1e-37f ? (ya * fast_rcp(w2)) * (a[j][v] * h) : 0.0f;
+                ef[j][v] = fmaf(ya, s[v], -s2);
+                wi[j][v] = w * i;
+                hc[j][v] = h * (e * i);              // 1 - i = e i
+                s[v] = fmaf(a[j][v], s[v], h);
             }
+            __builtin_amdgcn_sched_barrier(0);       // tokens in turn: the registers allow no more
         }
+        const __amdgpu_buffer_rsrc_t ox = tile_rows<T>(q.dx, p, b, t0, p.L, kTile);
+        const __amdgpu_buffer_rsrc_t oa = tile_rows<T>(q.dgate_a, p, b, t0, p.L, kTile);
+        const __amdgpu_buffer_rsrc_t og = tile_rows<T>(q.dgate_x, p, b, t0, p.L, kTile);
 #pragma unroll
         for (int j = R - 1; j >= 0; --j) {
-            const bool ok = in && t0 + j < len;
-            float xv[V], yv[V], ox[V], oa[V], og[V];
-            RowT::unpack(rx[j], xv);
-            RowT::unpack(ry[j], yv);
+            float gx[V], ga[V], gg[V], dy[V];
+            RowT::unpack(ry[j], dy);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float qn = G[v];                     // the adjoint from the right
-                const float gh = yv[v] + qn;               // gradient of h_t
-                G[v] = t0 + j < len ? a[j][v] * gh : qn;
-                const float la = A[v] * r[j][v];
-                const float ix = i[j][v] * xv[v];
-                // la / w, zero where the decay is one
-                const float law = w[j][v] > 0.0f ? la * fast_rcp(w[j][v]) : 0.0f;
-                const float E = gh * (la * a[j][v] * before[j][v] - law * (a[j][v] * a[j][v]) * ix);
-                ox[v] = gh * w[j][v] * i[j][v];
-                og[v] = gh * w[j][v] * ix * (e2[j][v] * i[j][v]);     // 1 - i = e2 i
-                oa[v] = E * (e1[j][v] * r[j][v]);                     // 1 - r = e1 r
-                sum[0][v] += ok ? E : 0.0f;
-                sum[1][v] += ok ? oa[v] : 0.0f;
-                sum[2][v] += ok ? og[v] : 0.0f;
-                if (!ok) ox[v] = oa[v] = og[v] = 0.0f;
+                const float gh = dy[v] + G[v];
+                G[v] = a[j][v] * gh;
+                const float E = gh * ef[j][v];
+                gx[v] = gh * wi[j][v];
+                ga[v] = E * cr[j][v];
+                gg[v] = gh * hc[j][v];
+                sum[0][v] += E;
+                sum[1][v] += ga[v];
+                sum[2][v] += gg[v];
             }
-            if (in && t0 + j < p.L) {
-                const int64_t o = (t0 + j) * p.D;
-                RowT::store(dx + o, ox);
-                RowT::store(dga + o, oa);
-                RowT::store(dgx + o, og);
-            }
+            RowT::store(ox, off + j * pitch, gx);
+            RowT::store(oa, off + j * pitch, ga);
+            RowT::store(og, off + j * pitch, gg);
         }
-        // the tile's sums: over the wavefront's groups, then over wavefronts
 #pragma unroll
         for (int k = 0; k < 3; ++k)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                float s = sum[k][v];
-                if constexpr (S::kLanes <= 16) s += __shfl_xor(s, 16, 64);
-                if constexpr (S::kLanes <= 32) s += __shfl_xor(s, 32, 64);
-                if (tid % 64 < S::kLanes) sSum[wave][k][c * V + v] = s;
+                float t = sum[k][v];
+                if constexpr (S::kPair) t += __shfl_xor(t, 32, 64);
+                if (lane < S::kLanes) sSum[buf][wave][k][c * V + v] = t;
             }
-        lds_barrier();
-        if (tid < 3 * kStrip) {
-            const int k = tid / kStrip, ch = tid % kStrip;
-            float s = 0.0f;
-#pragma unroll
-            for (int m = 0; m < kWaves; ++m) s += sSum[m][k][ch];
-            if (ds + ch < p.D) q.part[(cell * 3 + k) * p.D + ds + ch] = s;
-        }
+        before = tile;
+        tile = next;
     }
+    lds_barrier();
+    if (before >= 0) put_sums(buf ^ 1, before);
 }
 
 template <typename T>
 hipError_t launch_bwd(const GatedBwdArgs& a, hipStream_t stream) {
-    const unsigned grid = (unsigned)a.f.plan.strips;
-    if (a.f.D % 4 == 0) gated_bwd<T, 4><<<grid, kThreads, 0, stream>>>(a);
-    else gated_bwd<T, 1><<<grid, kThreads, 0, stream>>>(a);
+    const unsigned grid = (unsigned)(a.plan.strips * a.plan.walkers);
+    if (a.plan.walkers > 1) {
+        if (a.f.D % 2 == 0) gated_bwd<T, 2, true><<<grid, kThreads, 0, stream>>>(a);
+        else gated_bwd<T, 1, true><<<grid, kThreads, 0, stream>>>(a);
+    } else {
+        if (a.f.D % 2 == 0) gated_bwd<T, 2, false><<<grid, kThreads, 0, stream>>>(a);
+        else gated_bwd<T, 1, false><<<grid, kThreads, 0, stream>>>(a);
+    }
     return hipGetLastError();
 }
 
@@ -245,8 +390,12 @@ hipError_t launch_gated_bwd(const GatedBwdArgs& a, hipStream_t stream) {
         if (a.dh0) gated_bwd_pass<<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(a.dh_last, a.dh0, n);
         e = hipGetLastError();
     } else {
+        // the adjoint's chain and behind it the forward sweep's, at once
+        e = launch_chain_clear(a.chain, a.plan.chain_bytes + (a.own_ckpt ? f.plan.chain_bytes : 0), stream);
+        if (e != hipSuccess) return e;
         if (a.own_ckpt) {
             GatedArgs sweep = f;
+            sweep.cleared = true;
             sweep.y = nullptr;
             sweep.h_last = nullptr;
             e = launch_gated_fwd(sweep, stream);
@@ -257,7 +406,7 @@ hipError_t launch_gated_bwd(const GatedBwdArgs& a, hipStream_t stream) {
     if (e != hipSuccess) return e;
     ColumnSums s{};
     s.part = a.part;
-    s.n = f.B * f.plan.tiles;
+    s.n = f.B * a.plan.tiles;
     s.D = f.D;
     s.m = 3;
     s.out[0] = a.dA;

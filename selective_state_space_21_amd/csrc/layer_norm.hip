@@ -24,8 +24,6 @@
 namespace ssm {
 namespace {
 
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-
 // VEC elements as fp32; 16-byte vectors for the activations, and for fp32
 // operands beside bf16 ones two of them
 template <typename T, int VEC> struct Lane;
@@ -60,17 +58,19 @@ template <> struct Lane<float, 8> {
 };
 template <> struct Lane<float, 4> {
     static __device__ __forceinline__ void load(const float* p, float (&v)[4]) {
-        Row<float, 4>::unpack(Row<float, 4>::load(p), v);
+        const f32x4 a = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = a[k];
     }
     static __device__ __forceinline__ void store(float* p, const float (&v)[4]) {
-        Row<float, 4>::store(p, v);
+        __builtin_nontemporal_store((f32x4){v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4*>(p));
     }
 };
 template <typename T> struct Lane<T, 1> {
     static __device__ __forceinline__ void load(const T* p, float (&v)[1]) {
-        Row<T, 1>::unpack(Row<T, 1>::load(p), v);
+        v[0] = Elem<T>::load(p, 0);
     }
-    static __device__ __forceinline__ void store(T* p, const float (&v)[1]) { Row<T, 1>::store(p, v); }
+    static __device__ __forceinline__ void store(T* p, const float (&v)[1]) { Elem<T>::store(p, 0, v[0]); }
 };
 
 // the parameters are read by every row: through the cache

@@ -17,7 +17,7 @@ import torch
 from . import _args, _native
 
 __all__ = ["gated_scan_fwd", "gated_scan_fwd_ckpt", "gated_scan_bwd", "gated_state_update",
-           "gated_scan_walkers", "gated_scan_workspace_bytes", "gated_scan_ckpt_bytes",
+           "gated_scan_walkers", "gated_scan_bwd_walkers", "gated_scan_workspace_bytes", "gated_scan_ckpt_bytes",
            "gated_scan_bwd_workspace_bytes", "layer_norm_fwd", "layer_norm_bwd",
            "layer_norm_bwd_workspace_bytes", "causal_conv1d_silu_bwd",
            "causal_conv1d_silu_bwd_workspace_bytes"]
@@ -27,16 +27,24 @@ _DT = _args.DTYPES
 _ptr = _args.ptr
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _on(device):
     """The kernels are launched on the current device: make it the tensors'."""
     if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
+        return _HERE
     return torch.cuda.device(device)
 
 
 def gated_scan_walkers(B: int, L: int, D: int) -> int:
     """Workgroups that walk one strip of 64 channels together at these sizes."""
     return int(_native.load().ssm_gated_scan_walkers(B, L, D))
+
+
+def gated_scan_bwd_walkers(B: int, L: int, D: int) -> int:
+    """The same for the backward."""
+    return int(_native.load().ssm_gated_scan_bwd_walkers(B, L, D))
 
 
 def gated_scan_workspace_bytes(B: int, L: int, D: int, dtype=torch.bfloat16) -> int:

@@ -44,24 +44,29 @@ def _gates(ga, gx, A, ba, bx):
     za = ga + (ba if ba is not None else 0.0)
     zx = gx + (bx if bx is not None else 0.0)
 
-    def sigma(z):
-        # e = exp2(-z log2e): the sum z and the product's rounding shift the
-        # exponent by 3u|z| (the constant's own included), exp2 2u; 1 + e: u;
-        # rcp: 2u.  The error of e counts by its share of 1 + e, at most 1.
-        return torch.sigmoid(z), (3 * z.abs() + 2 + 1 + 2) * U
+    def sigma(gate, bias):
+        # e = exp2(-gate log2e - bias log2e): the bias's product, the fused
+        # sum and the constant's own rounding shift the exponent by
+        # u (|bias| + |z| + |gate| + |bias|), at most u (2|z| + 3|bias|);
+        # exp2 2u; 1 + e: u; rcp: 2u.  The error of e counts by its share of
+        # 1 + e, at most 1.
+        z = gate + bias
+        return torch.sigmoid(z), (2 * z.abs() + 3 * bias.abs() + 2 + 1 + 2) * U
 
-    r, er = sigma(za)
-    i, ei = sigma(zx)
+    zero = torch.zeros(1, dtype=F64)
+    r, er = sigma(ga, ba if ba is not None else zero)
+    i, ei = sigma(gx, bx if bx is not None else zero)
     la = A * r
-    ela = er + U
+    ela = er + 3 * U                               # A log2e, its constant, times r
     a = torch.exp(la)
-    ea = la.abs() * (ela + 2 * U) + 2 * U          # la log2e rounded (and the constant), exp2
+    ea = la.abs() * ela + 2 * U                    # exp2
     w = torch.sqrt(-torch.expm1(2 * la))
-    # series: nine fma of terms below one (2u covers their falling weights),
-    # the product u, what is left out u; and la's own error, whose effect on
-    # 1 - e^{2la} is at most its relative size.  1 - a a (z <= -1/2, value at
-    # least 0.39): 2 a^2 ea + u over 0.39.  The root halves, and adds 2u.
-    ew = 0.5 * torch.where(2 * la > -0.5, ela + 4 * U, (2 * a * a * ea + U) / 0.39) + 2 * U
+    # -2 l a s(l^2) for l above -1/2 (-0.72 ln 2): l's error moves 1 - e^{2l}
+    # by at most its own relative size; the rounding of a 2u (exp2), of s 3u
+    # (three fma of falling weight, the constants, what is left out), of two
+    # products 2u.  1 - a a below, at least 0.63: 2 a^2 ea + u over 0.63.  The
+    # root halves, and adds 2u.
+    ew = 0.5 * torch.where(la > -0.5, ela + 7 * U, (2 * a * a * ea + U) / 0.63) + 2 * U
     return r, i, la, a, w, er, ei, ela, ea, ew, torch.sigmoid(-za), torch.sigmoid(-zx)
 
 
@@ -126,7 +131,8 @@ def gated_bwd(keep, dy, dh_last=None):
     first_err = first * (k["ela"] + k["ea"] + 3 * U) + la.abs() * a * k["before_err"]
     law = torch.where(w > 0, la.abs() / w, zero)
     second = law * a * a * ix
-    second_err = second * (k["ela"] + k["ew"] + 2 * k["ea"] + eix + 7 * U)
+    # formed as la a a b / w^2: la a, a, b = w i x, rcp(w^2) and the products
+    second_err = second * (k["ela"] + 3 * k["ew"] + 2 * k["ea"] + eix + 9 * U)
     E = G * (first + second)
     Ee = Ge * (first + second) + G * (first_err + second_err) + 2 * U * E
     c_r, c_i = k["c_r"], k["c_i"]

@@ -99,8 +99,7 @@ int main(int argc, char** argv) {
         const size_t with = ssm_gated_scan_bwd_workspace_bytes(B, L, D, SSM_BF16, 1);
         const size_t without = ssm_gated_scan_bwd_workspace_bytes(B, L, D, SSM_BF16, 0);
         holds("one walker shares nothing", w > 1 || f == 0, B, L, D);
-        holds("the backward needs what the forward does", with >= f, B, L, D);
-        holds("and its own sweep more",
+        holds("the backward's own sweep adds what the forward needs, and the states",
               without >= with + f && (w == 0 || without >= with + ssm_gated_scan_ckpt_bytes(B, L, D, SSM_BF16)),
               B, L, D);
         (void)ssm_layer_norm_bwd_workspace_bytes(B, D);

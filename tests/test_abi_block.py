@@ -45,6 +45,7 @@ def test_gated_refusals(lib, call):
     assert call(lib, dt=2) == 3 and call(lib, dt=-1) == 3
     assert call(lib, B=1 << 26, L=1, D=1) == 4                    # strips
     assert call(lib, B=1, L=1 << 40, D=1) == 4                    # tiles
+    assert call(lib, B=1, L=1, D=(1 << 21) + 1) == 4              # a tile's rows
     for name in ("x", "ga", "gx", "ck"):
         assert call(lib, **{name: MIS}) == 5
     for name in ("A", "ba", "bx", "h0", "lens"):

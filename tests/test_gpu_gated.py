@@ -290,6 +290,38 @@ def test_long_sequence_sampled(dtype):
         Bd.check(g[k][..., ch], ref, eg[k], k)
 
 
+@pytest.mark.parametrize("dtype", [F, BF])
+@pytest.mark.parametrize("shape", [(1, 129, 64, None), (2, 700, 68, None), (1, 2600, 33, None),
+                                   (4, 1100, 128, [0, 1100, 129, 640]), (3, 3000, 8, [2999, 1, 1500])])
+def test_walkers_agree(shape, dtype, monkeypatch):
+    """Any number of workgroups per strip gives the same bits as one."""
+    B, L, D, lens = shape
+    t, dy, dh = make(B, L, D, dtype, seed=L, lens=lens)
+    d, dy, dh = dev(t), dy.cuda(), dh.cuda()
+
+    def run():
+        y, h, ck = ssm.gated_scan_fwd_ckpt(**d, out=torch.zeros(B, L, D, dtype=dtype, device="cuda"),
+                                           ckpt=torch.zeros(B, -(-L // 128), D, device="cuda"))
+        r = {"y": y, "h": h, "ck": ck}
+        r.update(ssm.gated_scan_bwd(**d, dy=dy, dh_last=dh, ckpt=ck))
+        r.update({"own " + k: v for k, v in ssm.gated_scan_bwd(**d, dy=dy, dh_last=dh).items()})
+        torch.cuda.synchronize()
+        return r
+
+    monkeypatch.setenv("SSM_GATED_WALKERS", "1")
+    assert ssm.gated_scan_walkers(B, L, D) == 1 and ssm.gated_scan_workspace_bytes(B, L, D) == 0
+    want = run()
+    for n in (2, 3, 7, 64):
+        monkeypatch.setenv("SSM_GATED_WALKERS", str(n))
+        tiles = -(-L // 256)
+        assert ssm.gated_scan_walkers(B, L, D) == min(n, tiles)
+        assert ssm.gated_scan_bwd_walkers(B, L, D) == min(n, -(-L // 128))
+        assert ssm.gated_scan_workspace_bytes(B, L, D) >= (B * -(-D // 64) * (tiles * 64 * 12 + 4) if tiles > 1 else 0)
+        got = run()
+        for k in want:
+            assert torch.equal(got[k], want[k]), (n, k)
+
+
 def test_offsets_past_32_bits():
     """A tensor of more than 2^31 elements: its last rows against the same
     rows alone, bit for bit."""

@@ -60,6 +60,7 @@ int conv_bwd_check_sizes(int64_t B, int64_t L, int64_t D, int64_t K, int dtype) 
     if (B < 1 || D < 1 || L < 0 || K < 1) return SSM_ERR_BAD_SHAPE;
     if (mul(mul(B, L), D) < 0 || L > kMaxElems) return SSM_ERR_BAD_SHAPE;
     if (K > 4) return SSM_ERR_UNSUPPORTED;
+    if (D > (int64_t(1) << 21)) return SSM_ERR_UNSUPPORTED;          // a run within 32-bit offsets
     if (mul(mul(B, D), 16) < 0) return SSM_ERR_BAD_SHAPE;           // states, and their grid
     if ((B * D + 255) / 256 > kMaxGrid) return SSM_ERR_UNSUPPORTED;
     const int64_t cells = mul(B, ssm::conv_bwd_blocks(L));

@@ -166,6 +166,9 @@ struct ConvBwdArgs {
     float* part;               // [B * blocks][K + 1][D]
 };
 
+namespace conv {
+constexpr int kBlockTokens = 256;       // tokens per workgroup of the backward
+}
 int64_t conv_bwd_blocks(int64_t L);
 size_t conv_bwd_workspace_bytes(int64_t B, int64_t L, int64_t D, int64_t K);
 hipError_t launch_conv1d_bwd(const ConvBwdArgs& a, hipStream_t stream);

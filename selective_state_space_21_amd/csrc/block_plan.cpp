@@ -89,7 +89,7 @@ size_t norm_bwd_workspace_bytes(int64_t rows, int64_t D) {
     return (size_t)al256(2 * norm_bwd_groups(rows, D) * D * 4);
 }
 
-int64_t conv_bwd_blocks(int64_t L) { return (L + 255) / 256; }
+int64_t conv_bwd_blocks(int64_t L) { return (L + conv::kBlockTokens - 1) / conv::kBlockTokens; }
 
 size_t conv_bwd_workspace_bytes(int64_t B, int64_t L, int64_t D, int64_t K) {
     return (size_t)al256(B * conv_bwd_blocks(L) * (K + 1) * D * 4);

@@ -24,7 +24,7 @@ __global__ __launch_bounds__(kCols * kWaves) void column_sums(ColumnSums a) {
     if (c < a.D) {
         const float* p = a.part + j * a.D + c;
         const int64_t step = a.m * a.D;
-#pragma unroll 4
+#pragma unroll 8
         for (int64_t r = wave; r < a.n; r += kWaves) sum += p[r * step];
     }
     s[wave][lane] = sum;

@@ -8,9 +8,12 @@
 // same sum.  Nothing of the forward is stored: s_t is formed again.  Per
 // element the call reads x and du and writes dx: it is bound by those bytes.
 //
-// A thread owns VEC channels and a run of tokens; it walks the run and the
-// K-1 tokens after it (whose g it needs for its last outputs) with the last
-// inputs and the last g in registers.
+// A thread owns VEC channels (two where the row length is even) and a run of
+// tokens; it walks the run and the K-1 tokens after it (whose g it needs for
+// its last outputs) with the last inputs and the last g in registers, and the
+// loads of kFlight tokens under way at a time.  Rows are addressed through
+// buffer resources that end with the sequence: behind it x and du read as
+// zero, so g is zero there, and stores are dropped.
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>
@@ -24,31 +27,29 @@ namespace {
 
 constexpr int kWaves = 8;
 constexpr int kRun = 32;                        // tokens per thread
+constexpr int kFlight = 8;
 constexpr int kBlockTokens = kWaves * kRun;     // a workgroup: 64 * VEC channels of these
-static_assert(kBlockTokens == 256, "conv_bwd_blocks counts blocks of 256 tokens");
+static_assert(kBlockTokens == conv::kBlockTokens && kRun % kFlight == 0, "the planner's blocks");
 
-template <typename T, int VEC> struct Vec;
-template <typename T> struct Vec<T, 1> {
-    using Raw = T;
-    static __device__ __forceinline__ Raw load(const T* p) { return __builtin_nontemporal_load(p); }
-    static __device__ __forceinline__ Raw zero() { return Raw(0); }
-    static __device__ __forceinline__ void unpack(const Raw& r, float (&v)[1]) { v[0] = Elem<T>::load(&r, 0); }
-    static __device__ __forceinline__ void store(T* p, const float (&v)[1]) { Elem<T>::store(p, 0, v[0]); }
-};
+// du u'(s): the derivative of s sigma(s)
+__device__ __forceinline__ float silu_grad(float du, float s) {
+    const float e = fast_exp2(fminf(-s * kLog2e, 126.0f));
+    const float sg = fast_rcp(1.0f + e);
+    return du * (sg * fmaf(s, e * sg, 1.0f));   // 1 - sigma = e sigma
+}
 
 template <typename T, int VEC, int K, bool SILU>
 __global__ __launch_bounds__(kWaves * 64) void conv1d_bwd_kernel(ConvBwdArgs p) {
-    using V = Vec<T, VEC>;
+    using V = Row<T, VEC>;
     __shared__ float sSum[kWaves][K + 1][64 * VEC];
-    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int64_t dblocks = (p.D + 64 * VEC - 1) / (64 * VEC);
     const int64_t db = blockIdx.x % dblocks;
     const int64_t cell = blockIdx.x / dblocks;                  // b * blocks + block
     const int64_t b = cell / p.blocks, block = cell % p.blocks;
     const int64_t d0 = (db * 64 + lane) * VEC;
     const bool in = d0 < p.D;
-    const int64_t t0 = block * kBlockTokens + wave * kRun;
-    const int64_t t1 = t0 + kRun < p.L ? t0 + kRun : p.L;       // t0 >= L: an empty run
+    const int64_t t0 = block * kBlockTokens + wave * kRun;      // t0 >= L: an empty run
 
     float sum[K + 1][VEC];
 #pragma unroll
@@ -56,71 +57,68 @@ __global__ __launch_bounds__(kWaves * 64) void conv1d_bwd_kernel(ConvBwdArgs p) 
 #pragma unroll
         for (int c = 0; c < VEC; ++c) sum[k][c] = 0.0f;
 
-    if (in && t0 < p.L) {
-        const T* x = static_cast<const T*>(p.x) + b * p.L * p.D + d0;
-        const T* du = static_cast<const T*>(p.du) + b * p.L * p.D + d0;
-        T* dx = static_cast<T*>(p.dx) + b * p.L * p.D + d0;
+    if (t0 < p.L) {
+        const uint32_t pitch = (uint32_t)(p.D * sizeof(T));
+        const uint32_t off = in ? (uint32_t)(d0 * sizeof(T)) : kNoChannel;
+        const int64_t row0 = (b * p.L + t0) * p.D;
+        const int64_t n = p.L - t0;                             // tokens from here on
+        const int mine = n < kRun ? (int)n : kRun;
+        const uint32_t seen = (uint32_t)((n < kRun + K - 1 ? n : kRun + K - 1) * p.D * sizeof(T));
+        const __amdgpu_buffer_rsrc_t rx = make_rsrc(static_cast<const T*>(p.x) + row0, seen);
+        const __amdgpu_buffer_rsrc_t ru = make_rsrc(static_cast<const T*>(p.du) + row0, seen);
+        const __amdgpu_buffer_rsrc_t ro = make_rsrc(static_cast<T*>(p.dx) + row0, (uint32_t)mine * pitch);
         float w[VEC][K], bias[VEC];
 #pragma unroll
         for (int c = 0; c < VEC; ++c) {
 #pragma unroll
-            for (int k = 0; k < K; ++k) w[c][k] = p.weight[(d0 + c) * K + k];
-            bias[c] = p.bias ? p.bias[d0 + c] : 0.0f;
+            for (int k = 0; k < K; ++k) w[c][k] = in ? p.weight[(d0 + c) * K + k] : 0.0f;
+            bias[c] = in && p.bias ? p.bias[d0 + c] : 0.0f;
         }
         float win[K][VEC];         // x_{t-(K-1)} .. x_t
         float g[K][VEC];           // g_{t-(K-1)} .. g_t
 #pragma unroll
         for (int i = 0; i < K - 1; ++i) {
             const int64_t t = t0 - (K - 1) + i;
-            if (t >= 0) {
-                V::unpack(V::load(x + t * p.D), win[i]);
-            } else {
-#pragma unroll
-                for (int c = 0; c < VEC; ++c)
-                    win[i][c] = p.state_in ? p.state_in[(b * p.D + d0 + c) * (K - 1) + (t + K - 1)] : 0.0f;
-            }
-#pragma unroll
-            for (int c = 0; c < VEC; ++c) g[i][c] = 0.0f;
-        }
-        // token t's own part, then the output of token t - (K-1), whose last
-        // term it is
-        for (int64_t t = t0; t < t1 + K - 1; ++t) {
-            const bool there = t < p.L;
-            float y[VEC];
-            V::unpack(there ? V::load(x + t * p.D) : V::zero(), win[K - 1]);
-            V::unpack(there ? V::load(du + t * p.D) : V::zero(), y);
 #pragma unroll
             for (int c = 0; c < VEC; ++c) {
-                float v = y[c];
+                g[i][c] = 0.0f;
+                win[i][c] = 0.0f;
+                if (in && t >= 0) win[i][c] = Elem<T>::load(static_cast<const T*>(p.x), (b * p.L + t) * p.D + d0 + c);
+                else if (in && p.state_in) win[i][c] = p.state_in[(b * p.D + d0 + c) * (K - 1) + (t + K - 1)];
+            }
+        }
+        // token t0 + u: its own part of the sums (when it is of this run), then
+        // the output of token u - (K-1), whose last term it is
+        auto token = [&](int u, bool own) {
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) {
                 if (SILU) {
                     float s = bias[c];
 #pragma unroll
                     for (int k = 0; k < K; ++k) s = fmaf(w[c][k], win[k][c], s);
-                    const float e = fast_exp2(fminf(-s * kLog2e, 126.0f));
-                    const float sg = fast_rcp(1.0f + e);
-                    v *= sg * fmaf(s, e * sg, 1.0f);          // 1 - sigma = e sigma
+                    g[K - 1][c] = silu_grad(g[K - 1][c], s);
                 }
-                if (!there) v = 0.0f;
-                g[K - 1][c] = v;
-                if (t < t1) {
+                if (own) {
 #pragma unroll
-                    for (int k = 0; k < K; ++k) sum[k][c] = fmaf(v, win[k][c], sum[k][c]);
-                    sum[K][c] += v;
+                    for (int k = 0; k < K; ++k) sum[k][c] = fmaf(g[K - 1][c], win[k][c], sum[k][c]);
+                    sum[K][c] += g[K - 1][c];
                 }
             }
-            const int64_t to = t - (K - 1);
-            if (to >= t0) {
+            const int to = u - (K - 1);
+            if (to >= 0) {
                 float o[VEC];
 #pragma unroll
                 for (int c = 0; c < VEC; ++c) {
                     o[c] = 0.0f;
 #pragma unroll
                     for (int k = 0; k < K; ++k) o[c] = fmaf(w[c][k], g[K - 1 - k][c], o[c]);
-                    const int64_t slot = to + (K - 1) - p.L;        // in the state handed on
-                    if (p.dstate_out && slot >= 0)
-                        o[c] += p.dstate_out[(b * p.D + d0 + c) * (K - 1) + slot];
                 }
-                V::store(dx + to * p.D, o);
+                if (p.dstate_out && to + (K - 1) >= n && to < n && in) {     // handed on in the state
+#pragma unroll
+                    for (int c = 0; c < VEC; ++c)
+                        o[c] += p.dstate_out[(b * p.D + d0 + c) * (K - 1) + (to + (K - 1) - n)];
+                }
+                V::store(ro, off + (uint32_t)to * pitch, o);
             }
 #pragma unroll
             for (int i = 0; i < K - 1; ++i)
@@ -129,6 +127,31 @@ __global__ __launch_bounds__(kWaves * 64) void conv1d_bwd_kernel(ConvBwdArgs p) 
                     win[i][c] = win[i + 1][c];
                     g[i][c] = g[i + 1][c];
                 }
+        };
+        for (int u0 = 0; u0 < mine; u0 += kFlight) {
+            typename V::Raw xs[kFlight], us[kFlight];
+#pragma unroll
+            for (int j = 0; j < kFlight; ++j) {
+                xs[j] = V::load(rx, off + (uint32_t)(u0 + j) * pitch);
+                us[j] = V::load(ru, off + (uint32_t)(u0 + j) * pitch);
+            }
+#pragma unroll
+            for (int j = 0; j < kFlight; ++j) {
+                V::unpack(xs[j], win[K - 1]);
+                V::unpack(us[j], g[K - 1]);
+                token(u0 + j, true);
+            }
+        }
+        // (mine up to kRun: a shorter run ended in the tokens behind the
+        // sequence that its last batch held, or does here)
+        const int done = (mine + kFlight - 1) / kFlight * kFlight;
+        if (done < mine + K - 1) {
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) {
+                V::unpack(V::load(rx, off + (uint32_t)(done + j) * pitch), win[K - 1]);
+                V::unpack(V::load(ru, off + (uint32_t)(done + j) * pitch), g[K - 1]);
+                token(done + j, false);
+            }
         }
     }
 #pragma unroll
@@ -175,9 +198,7 @@ __global__ __launch_bounds__(256) void conv1d_bwd_state(ConvBwdArgs p) {
                 float s = p.bias ? p.bias[d] : 0.0f;
 #pragma unroll
                 for (int k = 0; k < K; ++k) s = fmaf(w[k], win[t + k], s);
-                const float e = fast_exp2(fminf(-s * kLog2e, 126.0f));
-                const float sg = fast_rcp(1.0f + e);
-                v *= sg * fmaf(s, e * sg, 1.0f);
+                v = silu_grad(v, s);
             }
             g[t] = v;
         }
@@ -224,8 +245,8 @@ hipError_t launch_v(const ConvBwdArgs& a, hipStream_t stream) {
 
 hipError_t launch_conv1d_bwd(const ConvBwdArgs& a, hipStream_t stream) {
     hipError_t e;
-    if (a.bf16) e = launch_v<uint16_t, 1>(a, stream);
-    else e = launch_v<float, 1>(a, stream);
+    if (a.bf16) e = a.D % 2 == 0 ? launch_v<uint16_t, 2>(a, stream) : launch_v<uint16_t, 1>(a, stream);
+    else e = a.D % 2 == 0 ? launch_v<float, 2>(a, stream) : launch_v<float, 1>(a, stream);
     if (e != hipSuccess) return e;
     ColumnSums s{};
     s.part = a.part;

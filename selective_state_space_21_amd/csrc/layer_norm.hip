@@ -24,59 +24,83 @@
 namespace ssm {
 namespace {
 
-// VEC elements as fp32; 16-byte vectors for the activations, and for fp32
-// operands beside bf16 ones two of them
-template <typename T, int VEC> struct Lane;
-template <> struct Lane<uint16_t, 8> {
-    static __device__ __forceinline__ void load(const uint16_t* p, float (&v)[8]) {
-        const u32x4 r = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            v[2 * k] = __uint_as_float(r[k] << 16);
-            v[2 * k + 1] = __uint_as_float(r[k] & 0xffff0000u);
-        }
-    }
-    static __device__ __forceinline__ void store(uint16_t* p, const float (&v)[8]) {
-        u32x4 r;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            r[k] = (uint32_t)f32_to_bf16_bits(v[2 * k]) | ((uint32_t)f32_to_bf16_bits(v[2 * k + 1]) << 16);
-        __builtin_nontemporal_store(r, reinterpret_cast<u32x4*>(p));
-    }
+// VEC elements as fp32: 16-byte vectors of the activations, and for fp32
+// operands beside bf16 ones two of them.  Rows of odd length leave a vector at
+// any element's alignment, which the hardware's global accesses allow (a row
+// of 2561 fp32 elements by single elements: 24.1 us for forward and backward
+// of 777 rows where whole vectors take 13.5).
+template <typename T> struct Vec16;
+template <> struct Vec16<uint16_t> {
+    typedef uint32_t type __attribute__((ext_vector_type(4), aligned(2)));
 };
-template <> struct Lane<float, 8> {
-    static __device__ __forceinline__ void load(const float* p, float (&v)[8]) {
-        const f32x4 a = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p));
-        const f32x4 b = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p) + 1);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) { v[k] = a[k]; v[k + 4] = b[k]; }
-    }
-    static __device__ __forceinline__ void store(float* p, const float (&v)[8]) {
-        __builtin_nontemporal_store((f32x4){v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4*>(p));
-        __builtin_nontemporal_store((f32x4){v[4], v[5], v[6], v[7]}, reinterpret_cast<f32x4*>(p) + 1);
-    }
-};
-template <> struct Lane<float, 4> {
-    static __device__ __forceinline__ void load(const float* p, float (&v)[4]) {
-        const f32x4 a = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p));
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = a[k];
-    }
-    static __device__ __forceinline__ void store(float* p, const float (&v)[4]) {
-        __builtin_nontemporal_store((f32x4){v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4*>(p));
-    }
-};
-template <typename T> struct Lane<T, 1> {
-    static __device__ __forceinline__ void load(const T* p, float (&v)[1]) {
-        v[0] = Elem<T>::load(p, 0);
-    }
-    static __device__ __forceinline__ void store(T* p, const float (&v)[1]) { Elem<T>::store(p, 0, v[0]); }
+template <> struct Vec16<float> {
+    typedef float type __attribute__((ext_vector_type(4), aligned(4)));
 };
 
-// the parameters are read by every row: through the cache
-template <int VEC> __device__ __forceinline__ void load_param(const float* p, float (&v)[VEC], float none) {
+template <int VEC> __device__ __forceinline__ void load_all(const uint16_t* p, float (&v)[VEC]) {
+    static_assert(VEC == 8, "one 16-byte vector");
+    const auto r = __builtin_nontemporal_load(reinterpret_cast<const Vec16<uint16_t>::type*>(p));
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) v[k] = p ? p[k] : none;
+    for (int k = 0; k < 4; ++k) {
+        v[2 * k] = __uint_as_float(r[k] << 16);
+        v[2 * k + 1] = __uint_as_float(r[k] & 0xffff0000u);
+    }
+}
+template <int VEC> __device__ __forceinline__ void load_all(const float* p, float (&v)[VEC]) {
+#pragma unroll
+    for (int i = 0; i < VEC / 4; ++i) {
+        const auto r = __builtin_nontemporal_load(reinterpret_cast<const Vec16<float>::type*>(p) + i);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[4 * i + k] = r[k];
+    }
+}
+template <int VEC> __device__ __forceinline__ void store_all(uint16_t* p, const float (&v)[VEC]) {
+    typename Vec16<uint16_t>::type r;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        r[k] = (uint32_t)f32_to_bf16_bits(v[2 * k]) | ((uint32_t)f32_to_bf16_bits(v[2 * k + 1]) << 16);
+    __builtin_nontemporal_store(r, reinterpret_cast<Vec16<uint16_t>::type*>(p));
+}
+template <int VEC> __device__ __forceinline__ void store_all(float* p, const float (&v)[VEC]) {
+#pragma unroll
+    for (int i = 0; i < VEC / 4; ++i) {
+        const typename Vec16<float>::type r = {v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+        __builtin_nontemporal_store(r, reinterpret_cast<Vec16<float>::type*>(p) + i);
+    }
+}
+
+// the first n of VEC elements (n <= 0: none), zeros for the others; WHOLE: the
+// row is whole vectors, n is VEC or more, or 0 or less
+template <bool WHOLE, typename T, int VEC>
+__device__ __forceinline__ void get(const T* p, int64_t n, float (&v)[VEC]) {
+    if (WHOLE ? n > 0 : n >= VEC) {
+        load_all<VEC>(p, v);
+    } else {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) v[k] = !WHOLE && k < n ? Elem<T>::load(p, k) : 0.0f;
+    }
+}
+template <bool WHOLE, typename T, int VEC>
+__device__ __forceinline__ void put(T* p, int64_t n, const float (&v)[VEC]) {
+    if (WHOLE ? n > 0 : n >= VEC) {
+        store_all<VEC>(p, v);
+    } else if (!WHOLE) {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k)
+            if (k < n) Elem<T>::store(p, k, v[k]);
+    }
+}
+
+// the parameters are read by every row: through the cache
+template <bool WHOLE, int VEC>
+__device__ __forceinline__ void get_param(const float* p, int64_t d, int64_t n, float (&v)[VEC], float none) {
+    if (p && (WHOLE ? n > 0 : n >= VEC)) {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) v[k] = p[d + k];
+    } else {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) v[k] = !WHOLE && p && k < n ? p[d + k] : none;
+    }
 }
 
 __device__ __forceinline__ float wave_sum(float v) {
@@ -105,7 +129,7 @@ template <int TPR> __device__ __forceinline__ float row_sum(float v, float* s) {
     return v;
 }
 
-template <typename T, bool RES, int VEC, int NV, int TPR>
+template <bool WHOLE, typename T, bool RES, int VEC, int NV, int TPR>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd(NormArgs p) {
     constexpr int kThreads = TPR > 256 ? TPR : 256;
     __shared__ float s[kThreads / 64];
@@ -118,18 +142,13 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd(NormArgs p) {
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int64_t d = (int64_t)(i * TPR + j) * VEC;
-        if (d < p.D) {
-            Lane<T, VEC>::load(x + d, v[i]);
-            if (RES) {
-                float r[VEC];
-                Lane<float, VEC>::load(p.residual + o + d, r);
+        const int64_t d = (int64_t)(i * TPR + j) * VEC, n = p.D - d;
+        get<WHOLE, T, VEC>(x + d, n, v[i]);
+        if (RES) {
+            float r[VEC];
+            get<WHOLE, float, VEC>(p.residual + o + d, n, r);
 #pragma unroll
-                for (int k = 0; k < VEC; ++k) v[i][k] += r[k];
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < VEC; ++k) v[i][k] = 0.0f;
+            for (int k = 0; k < VEC; ++k) v[i][k] += r[k];
         }
 #pragma unroll
         for (int k = 0; k < VEC; ++k) sum += v[i][k];
@@ -139,12 +158,11 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd(NormArgs p) {
     sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        if ((int64_t)(i * TPR + j) * VEC < p.D) {
+        const int64_t n = p.D - (int64_t)(i * TPR + j) * VEC;
 #pragma unroll
-            for (int k = 0; k < VEC; ++k) {
-                const float c = v[i][k] - mean;
-                sum = fmaf(c, c, sum);
-            }
+        for (int k = 0; k < VEC; ++k) {
+            const float c = k < n ? v[i][k] - mean : 0.0f;
+            sum = fmaf(c, c, sum);
         }
     }
     const float rstd = 1.0f / sqrtf(fmaf(row_sum<TPR>(sum, s), inv, p.eps));
@@ -154,16 +172,14 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd(NormArgs p) {
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int64_t d = (int64_t)(i * TPR + j) * VEC;
-        if (d < p.D) {
-            if (RES && p.residual_out) Lane<float, VEC>::store(p.residual_out + o + d, v[i]);
-            float w[VEC], b[VEC];
-            load_param<VEC>(p.weight ? p.weight + d : nullptr, w, 1.0f);
-            load_param<VEC>(p.bias ? p.bias + d : nullptr, b, 0.0f);
+        const int64_t d = (int64_t)(i * TPR + j) * VEC, n = p.D - d;
+        if (RES && p.residual_out) put<WHOLE, float, VEC>(p.residual_out + o + d, n, v[i]);
+        float w[VEC], b[VEC];
+        get_param<WHOLE, VEC>(p.weight, d, n, w, 1.0f);
+        get_param<WHOLE, VEC>(p.bias, d, n, b, 0.0f);
 #pragma unroll
-            for (int k = 0; k < VEC; ++k) v[i][k] = fmaf((v[i][k] - mean) * rstd, w[k], b[k]);
-            Lane<T, VEC>::store(static_cast<T*>(p.y) + o + d, v[i]);
-        }
+        for (int k = 0; k < VEC; ++k) v[i][k] = fmaf((v[i][k] - mean) * rstd, w[k], b[k]);
+        put<WHOLE, T, VEC>(static_cast<T*>(p.y) + o + d, n, v[i]);
     }
 }
 
@@ -202,7 +218,7 @@ __global__ __launch_bounds__(1024) void norm_fwd_long(NormArgs p) {
 
 // X: the type of the normalised input (the fp32 stream, or the activations'),
 // T: the activations' type.
-template <typename X, typename T, int VEC, int NV, int TPR>
+template <bool WHOLE, typename X, typename T, int VEC, int NV, int TPR>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd(NormBwdArgs p) {
     constexpr int kThreads = TPR > 256 ? TPR : 256;
     constexpr int kRows = kThreads / TPR;
@@ -210,11 +226,14 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd(NormBwdArgs p)
     __shared__ float join[kRows > 1 ? kRows - 1 : 1][TPR > 64 ? 1 : VEC][TPR];
     const int j = threadIdx.x % TPR, sub = threadIdx.x / TPR;
     const float inv = 1.0f / (float)p.D;
-    float w[NV][VEC], dw[NV][VEC], db[NV][VEC];
+    // the weight stays in registers, or is read again for every row where 16
+    // elements a thread at 128 registers leave no room for it
+    constexpr bool HOLD = TPR < 1024 || NV * VEC <= 8;
+    float w[HOLD ? NV : 1][VEC], dw[NV][VEC], db[NV][VEC];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int64_t d = (int64_t)(i * TPR + j) * VEC;
-        load_param<VEC>(p.weight && d < p.D ? p.weight + d : nullptr, w[i], 1.0f);
+        if (HOLD) get_param<WHOLE, VEC>(p.weight, d, p.D - d, w[HOLD ? i : 0], 1.0f);
 #pragma unroll
         for (int k = 0; k < VEC; ++k) dw[i][k] = db[i][k] = 0.0f;
     }
@@ -225,36 +244,34 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd(NormBwdArgs p)
         float c1 = 0.0f, c2 = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int64_t d = (int64_t)(i * TPR + j) * VEC;
-            if (d < p.D) {
-                Lane<X, VEC>::load(static_cast<const X*>(p.x) + o + d, n[i]);
-                Lane<T, VEC>::load(static_cast<const T*>(p.dy) + o + d, v[i]);
+            const int64_t d = (int64_t)(i * TPR + j) * VEC, left = p.D - d;
+            get<WHOLE, X, VEC>(static_cast<const X*>(p.x) + o + d, left, n[i]);
+            get<WHOLE, T, VEC>(static_cast<const T*>(p.dy) + o + d, left, v[i]);      // zero behind the row
+            float (&wi)[VEC] = w[HOLD ? i : 0];
+            if (!HOLD) get_param<WHOLE, VEC>(p.weight, d, left, wi, 1.0f);
 #pragma unroll
-                for (int k = 0; k < VEC; ++k) {
-                    n[i][k] = (n[i][k] - mean) * rstd;
-                    dw[i][k] = fmaf(v[i][k], n[i][k], dw[i][k]);
-                    db[i][k] += v[i][k];
-                    v[i][k] *= w[i][k];
-                    c1 = fmaf(v[i][k], n[i][k], c1);
-                    c2 += v[i][k];
-                }
+            for (int k = 0; k < VEC; ++k) {
+                n[i][k] = (n[i][k] - mean) * rstd;
+                dw[i][k] = fmaf(v[i][k], n[i][k], dw[i][k]);
+                db[i][k] += v[i][k];
+                v[i][k] *= wi[k];
+                c1 = fmaf(v[i][k], n[i][k], c1);
+                c2 += v[i][k];
             }
         }
         c1 = row_sum<TPR>(c1, s) * inv;
         c2 = row_sum<TPR>(c2, s) * inv;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int64_t d = (int64_t)(i * TPR + j) * VEC;
-            if (d < p.D) {
-                float g[VEC];
+            const int64_t d = (int64_t)(i * TPR + j) * VEC, left = p.D - d;
+            float g[VEC];
 #pragma unroll
-                for (int k = 0; k < VEC; ++k) g[k] = 0.0f;
-                if (p.dresidual_out) Lane<float, VEC>::load(p.dresidual_out + o + d, g);
+            for (int k = 0; k < VEC; ++k) g[k] = 0.0f;
+            if (p.dresidual_out) get<WHOLE, float, VEC>(p.dresidual_out + o + d, left, g);
 #pragma unroll
-                for (int k = 0; k < VEC; ++k) g[k] = fmaf(rstd, v[i][k] - c2 - n[i][k] * c1, g[k]);
-                if (p.dresidual) Lane<float, VEC>::store(p.dresidual + o + d, g);
-                Lane<T, VEC>::store(static_cast<T*>(p.dx) + o + d, g);
-            }
+            for (int k = 0; k < VEC; ++k) g[k] = fmaf(rstd, v[i][k] - c2 - n[i][k] * c1, g[k]);
+            if (p.dresidual) put<WHOLE, float, VEC>(p.dresidual + o + d, left, g);
+            put<WHOLE, T, VEC>(static_cast<T*>(p.dx) + o + d, left, g);
         }
     }
     // join the rows that ran side by side, then this workgroup's row of part
@@ -281,7 +298,8 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd(NormBwdArgs p)
             if (sub == 0 && d < p.D) {
                 float* out = p.part + ((int64_t)blockIdx.x * 2 + which) * p.D + d;
 #pragma unroll
-                for (int k = 0; k < VEC; ++k) out[k] = a[k];
+                for (int k = 0; k < VEC; ++k)
+                    if (WHOLE || d + k < p.D) out[k] = a[k];
             }
         }
     }
@@ -328,26 +346,27 @@ __global__ __launch_bounds__(256) void norm_bwd_columns(NormBwdArgs p) {
     p.part[(group * 2 + 1) * p.D + d] = db;
 }
 
-template <typename T, bool RES, int VEC, int NV, int TPR>
+template <bool WHOLE, typename T, bool RES, int VEC, int NV, int TPR>
 hipError_t launch_fwd(const NormArgs& a, hipStream_t stream) {
     constexpr int threads = TPR > 256 ? TPR : 256;
     constexpr int rows = threads / TPR;
-    norm_fwd<T, RES, VEC, NV, TPR>
+    norm_fwd<WHOLE, T, RES, VEC, NV, TPR>
         <<<(unsigned)((a.rows + rows - 1) / rows), threads, 0, stream>>>(a);
     return hipGetLastError();
 }
 
 // the thread layout of a row of `nv` vectors
-template <typename T, bool RES, int VEC>
+template <bool WHOLE, typename T, bool RES, int VEC>
 hipError_t launch_fwd_v(const NormArgs& a, hipStream_t stream) {
-    const int64_t nv = a.D / VEC;
-    if (nv <= 64) return launch_fwd<T, RES, VEC, 1, 64>(a, stream);
-    if (nv <= 128) return launch_fwd<T, RES, VEC, 2, 64>(a, stream);
-    if (nv <= 256) return launch_fwd<T, RES, VEC, 4, 64>(a, stream);
-    if (nv <= 512) return launch_fwd<T, RES, VEC, 2, 256>(a, stream);
-    if (nv <= 1024) return launch_fwd<T, RES, VEC, 4, 256>(a, stream);
-    if (nv <= 2048) return launch_fwd<T, RES, VEC, 2, 1024>(a, stream);
-    if (nv <= 4096) return launch_fwd<T, RES, VEC, 4, 1024>(a, stream);
+    const int64_t nv = (a.D + VEC - 1) / VEC;
+    if (nv <= 64) return launch_fwd<WHOLE, T, RES, VEC, 1, 64>(a, stream);
+    if (nv <= 128) return launch_fwd<WHOLE, T, RES, VEC, 2, 64>(a, stream);
+    if (nv <= 256) return launch_fwd<WHOLE, T, RES, VEC, 4, 64>(a, stream);
+    if (nv <= 512) return launch_fwd<WHOLE, T, RES, VEC, 2, 256>(a, stream);
+    if (nv <= 768) return launch_fwd<WHOLE, T, RES, VEC, 3, 256>(a, stream);
+    if (nv <= 1024) return launch_fwd<WHOLE, T, RES, VEC, 4, 256>(a, stream);
+    if (nv <= 2048) return launch_fwd<WHOLE, T, RES, VEC, 2, 1024>(a, stream);
+    if (nv <= 4096) return launch_fwd<WHOLE, T, RES, VEC, 4, 1024>(a, stream);
     norm_fwd_long<T, RES><<<(unsigned)a.rows, 1024, 0, stream>>>(a);
     return hipGetLastError();
 }
@@ -355,25 +374,34 @@ hipError_t launch_fwd_v(const NormArgs& a, hipStream_t stream) {
 template <typename T, int VEC>
 hipError_t launch_fwd_t(const NormArgs& a, hipStream_t stream) {
     if (a.D % VEC == 0)
-        return a.residual ? launch_fwd_v<T, true, VEC>(a, stream) : launch_fwd_v<T, false, VEC>(a, stream);
-    return a.residual ? launch_fwd_v<T, true, 1>(a, stream) : launch_fwd_v<T, false, 1>(a, stream);
+        return a.residual ? launch_fwd_v<true, T, true, VEC>(a, stream) : launch_fwd_v<true, T, false, VEC>(a, stream);
+    return a.residual ? launch_fwd_v<false, T, true, VEC>(a, stream) : launch_fwd_v<false, T, false, VEC>(a, stream);
 }
 
-template <typename X, typename T, int VEC, int NV, int TPR>
+template <bool WHOLE, typename X, typename T, int VEC, int NV, int TPR>
 hipError_t launch_bwd(const NormBwdArgs& a, hipStream_t stream) {
-    norm_bwd<X, T, VEC, NV, TPR><<<(unsigned)a.groups, TPR > 256 ? TPR : 256, 0, stream>>>(a);
+    norm_bwd<WHOLE, X, T, VEC, NV, TPR><<<(unsigned)a.groups, TPR > 256 ? TPR : 256, 0, stream>>>(a);
     return hipGetLastError();
 }
 
-template <typename X, typename T, int VEC>
-hipError_t launch_bwd_v(const NormBwdArgs& a, hipStream_t stream) {
-    const int64_t nv = a.D / VEC;
-    if (nv <= 64) return launch_bwd<X, T, VEC, 1, 64>(a, stream);
-    if (nv <= 128) return launch_bwd<X, T, VEC, 2, 64>(a, stream);
-    if (nv <= 256) return launch_bwd<X, T, VEC, 1, 256>(a, stream);
-    if (nv <= 512) return launch_bwd<X, T, VEC, 2, 256>(a, stream);
-    if (nv <= 1024) return launch_bwd<X, T, VEC, 1, 1024>(a, stream);
-    if (nv <= 2048) return launch_bwd<X, T, VEC, 2, 1024>(a, stream);
+// (at most 16 elements a thread: five values of each are in registers)
+template <bool WHOLE, typename X, typename T, int VEC>
+hipError_t launch_bwd_w(const NormBwdArgs& a, hipStream_t stream) {
+    const int64_t nv = (a.D + VEC - 1) / VEC;
+    if (nv <= 64) return launch_bwd<WHOLE, X, T, VEC, 1, 64>(a, stream);
+    if (nv <= 128) return launch_bwd<WHOLE, X, T, VEC, 2, 64>(a, stream);
+    if (nv <= 256) return launch_bwd<WHOLE, X, T, VEC, 1, 256>(a, stream);
+    if (nv <= 512) return launch_bwd<WHOLE, X, T, VEC, 2, 256>(a, stream);
+    if constexpr (VEC == 4) {
+        if (nv <= 768) return launch_bwd<WHOLE, X, T, VEC, 3, 256>(a, stream);
+        if (nv <= 1024) return launch_bwd<WHOLE, X, T, VEC, 4, 256>(a, stream);
+    } else {
+        if (nv <= 1024) return launch_bwd<WHOLE, X, T, VEC, 1, 1024>(a, stream);
+    }
+    if (nv <= 2048) return launch_bwd<WHOLE, X, T, VEC, 2, 1024>(a, stream);
+    if constexpr (VEC == 4) {
+        if (nv <= 4096) return launch_bwd<WHOLE, X, T, VEC, 4, 1024>(a, stream);
+    }
     norm_bwd_long<X, T><<<(unsigned)a.rows, 1024, 0, stream>>>(a);
     norm_bwd_columns<X, T>
         <<<dim3((unsigned)((a.D + 255) / 256), (unsigned)a.groups), 256, 0, stream>>>(a);
@@ -381,8 +409,8 @@ hipError_t launch_bwd_v(const NormBwdArgs& a, hipStream_t stream) {
 }
 
 template <typename X, typename T, int VEC>
-hipError_t launch_bwd_t(const NormBwdArgs& a, hipStream_t stream) {
-    return a.D % VEC == 0 ? launch_bwd_v<X, T, VEC>(a, stream) : launch_bwd_v<X, T, 1>(a, stream);
+hipError_t launch_bwd_v(const NormBwdArgs& a, hipStream_t stream) {
+    return a.D % VEC == 0 ? launch_bwd_w<true, X, T, VEC>(a, stream) : launch_bwd_w<false, X, T, VEC>(a, stream);
 }
 
 }  // namespace
@@ -395,9 +423,9 @@ hipError_t launch_layer_norm(const NormArgs& a, hipStream_t stream) {
 hipError_t launch_layer_norm_bwd(const NormBwdArgs& a, hipStream_t stream) {
     if (a.rows > 0) {
         hipError_t e;
-        if (!a.bf16) e = launch_bwd_t<float, float, 4>(a, stream);
-        else if (a.x_bf16) e = launch_bwd_t<uint16_t, uint16_t, 8>(a, stream);
-        else e = launch_bwd_t<float, uint16_t, 8>(a, stream);
+        if (!a.bf16) e = launch_bwd_v<float, float, 4>(a, stream);
+        else if (a.x_bf16) e = launch_bwd_v<uint16_t, uint16_t, 8>(a, stream);
+        else e = launch_bwd_v<float, uint16_t, 8>(a, stream);
         if (e != hipSuccess) return e;
     }
     if (!a.dweight && !a.dbias) return hipSuccess;

@@ -504,7 +504,7 @@ int ssm_causal_conv1d_silu_bwd(const void* x, const float* weight, const float* 
  *                    seq_lens[b] tokens (clamped to [0, L]); the padding is
  *                    not read, y there is left untouched, and h_last is the
  *                    state after the row's last token
- *   B >= 1; 1 <= D <= 2^21; L >= 0; B * ceil(D / 64) below 2^25.
+ *   B >= 1; 1 <= D <= 2^20; L >= 0; B * ceil(D / 64) below 2^25.
  * The sequence is walked in tiles of 256 tokens by 64 channels (128 tokens in
  * the backward).  With enough of those strips of 64 channels to fill the GPU (or few tiles) a
  * workgroup walks a strip alone; else several walk it together, each taking

@@ -38,7 +38,7 @@ int gated_check_sizes(int64_t B, int64_t L, int64_t D, int dtype) {
     if (mul(mul(B, D), L) < 0 || mul(B, D) < 0 || L > kMaxElems) return SSM_ERR_BAD_SHAPE;
     const int64_t strips = mul(B, (D + ssm::gated::kStrip - 1) / ssm::gated::kStrip);
     const int64_t tiles = (L + ssm::gated::kBwdTile - 1) / ssm::gated::kBwdTile;
-    if (D > (int64_t(1) << 21)) return SSM_ERR_UNSUPPORTED;          // a tile within 32-bit offsets
+    if (D > ssm::gated::kMaxRow) return SSM_ERR_UNSUPPORTED;
     if (strips < 0 || strips > kMaxGrid / ssm::gated::kMaxWalkers) return SSM_ERR_UNSUPPORTED;
     if (tiles > (int64_t(1) << 30)) return SSM_ERR_UNSUPPORTED;     // drawn from a 32-bit counter
     if (mul(mul(strips, tiles), 64 * 16) < 0 || mul(mul(B, tiles), mul(D, 32)) < 0)
@@ -60,7 +60,7 @@ int conv_bwd_check_sizes(int64_t B, int64_t L, int64_t D, int64_t K, int dtype) 
     if (B < 1 || D < 1 || L < 0 || K < 1) return SSM_ERR_BAD_SHAPE;
     if (mul(mul(B, L), D) < 0 || L > kMaxElems) return SSM_ERR_BAD_SHAPE;
     if (K > 4) return SSM_ERR_UNSUPPORTED;
-    if (D > (int64_t(1) << 21)) return SSM_ERR_UNSUPPORTED;          // a run within 32-bit offsets
+    if (D > ssm::conv::kMaxRow) return SSM_ERR_UNSUPPORTED;
     if (mul(mul(B, D), 16) < 0) return SSM_ERR_BAD_SHAPE;           // states, and their grid
     if ((B * D + 255) / 256 > kMaxGrid) return SSM_ERR_UNSUPPORTED;
     const int64_t cells = mul(B, ssm::conv_bwd_blocks(L));

@@ -21,6 +21,9 @@ static_assert(kFwdTile % SSM_GATED_TILE == 0, "a forward tile holds whole saved 
 constexpr int kStrip = 64;              // channels per strip: one workgroup's width
 constexpr int kFwdThreads = 1024;
 constexpr int kBwdThreads = 1024;
+// Longest row: a tile's rows are addressed by 32-bit offsets below kNoChannel.
+constexpr int64_t kMaxRow = int64_t(1) << 20;
+static_assert(kFwdTile * kMaxRow * 4 < int64_t(1) << 31, "a tile's rows end below kNoChannel");
 constexpr int kMaxWalkers = 64;         // workgroups per strip at most
 constexpr int kBack = 8;                // tiles a walker looks back over for a known state
 // What the walkers of a call share, in order: a counter per strip; a map (8
@@ -168,6 +171,7 @@ struct ConvBwdArgs {
 
 namespace conv {
 constexpr int kBlockTokens = 256;       // tokens per workgroup of the backward
+constexpr int64_t kMaxRow = int64_t(1) << 21;   // 35 rows within 32-bit offsets below kNoChannel
 }
 int64_t conv_bwd_blocks(int64_t L);
 size_t conv_bwd_workspace_bytes(int64_t B, int64_t L, int64_t D, int64_t K);

@@ -244,7 +244,6 @@ __global__ __launch_bounds__(kThreads, 4) void gated_bwd(GatedBwdArgs q) {
                 const float w = __builtin_amdgcn_sqrtf(one_minus_sq(y[j][v], a[j][v]));
                 ph[v] = fmaf(a[j][v], ph[v], w * (i * xv[v]));
             }
-            __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -322,7 +321,6 @@ __global__ __launch_bounds__(kThreads, 4) void gated_bwd(GatedBwdArgs q) {
                 hc[j][v] = h * (e * i);              // 1 - i = e i
                 s[v] = fmaf(a[j][v], s[v], h);
             }
-            __builtin_amdgcn_sched_barrier(0);       // tokens in turn: the registers allow no more
         }
         const __amdgpu_buffer_rsrc_t ox = tile_rows<T>(q.dx, p, b, t0, p.L, kTile);
         const __amdgpu_buffer_rsrc_t oa = tile_rows<T>(q.dgate_a, p, b, t0, p.L, kTile);

@@ -73,9 +73,8 @@ template <> struct Row<float, 1> {
 };
 
 // Lane offset of channels that do not exist: behind the end of every resource
-// (a tile's rows are at most 2^30 bytes: the ABI refuses longer rows).
+// (the ABI refuses rows that would reach it).
 constexpr uint32_t kNoChannel = 0x80000000u;
-constexpr int64_t kMaxRow = int64_t(1) << 21;
 
 template <int V, int TILE, int THREADS> struct TileShape {
     static constexpr int kLanes = gated::kStrip / V;              // threads to a token's channels

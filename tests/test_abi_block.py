@@ -45,7 +45,7 @@ def test_gated_refusals(lib, call):
     assert call(lib, dt=2) == 3 and call(lib, dt=-1) == 3
     assert call(lib, B=1 << 26, L=1, D=1) == 4                    # strips
     assert call(lib, B=1, L=1 << 40, D=1) == 4                    # tiles
-    assert call(lib, B=1, L=1, D=(1 << 21) + 1) == 4              # a tile's rows
+    assert call(lib, B=1, L=1, D=(1 << 20) + 1) == 4              # a tile's rows
     for name in ("x", "ga", "gx", "ck"):
         assert call(lib, **{name: MIS}) == 5
     for name in ("A", "ba", "bx", "h0", "lens"):
@@ -131,7 +131,7 @@ def test_conv_bwd_refusals(lib):
     for name in ("b", "st", "dso", "db", "ds"):
         assert g(**{name: MIS}) == 5
     assert g(K=0) == 2 and g(K=5) == 4 and g(B=0) == 2 and g(L=-1) == 2 and g(L=HUGE) == 2 and g(dt=4) == 3
-    assert g(B=1 << 20, L=1 << 20, D=1 << 10) == 4
+    assert g(B=1 << 20, L=1 << 20, D=1 << 10) == 4 and g(D=(1 << 21) + 1) == 4
     need = lib.ssm_causal_conv1d_silu_bwd_workspace_bytes(2, 9, 8, 4)
     assert need > 0 and g(ws=None) == 6 and g(n=need - 1) == 6 and g(ws=FAKE + 64) == 5
 

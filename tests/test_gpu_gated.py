@@ -206,6 +206,101 @@ def test_writes_stay_inside():
     assert all(torch.equal(a[k], b[k]) for k in a)
 
 
+@pytest.mark.parametrize("walkers", ["1", "2", "5"])
+def test_workspace_is_cleared_and_kept_within(walkers, monkeypatch):
+    """A workspace full of anything, and one that a longer call has used,
+    between guards."""
+    monkeypatch.setenv("SSM_GATED_WALKERS", walkers)
+    B, L, D = 2, 2100, 100
+    t, dy, dh = make(B, L, D, BF, seed=1, lens=[2100, 1300])
+    d, dy, dh = dev(t), dy.cuda(), dh.cuda()
+    y, h = ssm.gated_scan_fwd(**d, out=torch.zeros(B, L, D, dtype=BF, device="cuda"))
+    g = ssm.gated_scan_bwd(**d, dy=dy, dh_last=dh)
+    need = ssm.gated_scan_workspace_bytes(B, L, D, BF)
+    assert (need > 0) == (walkers != "1")
+    for fill in (0, 0x7F, 0xFF):
+        ws = torch.full((need + 512,), fill, dtype=torch.uint8, device="cuda")
+        for _ in range(2):
+            y2, h2 = ssm.gated_scan_fwd(**d, workspace=ws[256:256 + need],
+                                        out=torch.zeros(B, L, D, dtype=BF, device="cuda"))
+            assert torch.equal(y, y2) and torch.equal(h, h2)
+        assert torch.all(ws[:256] == fill) and torch.all(ws[256 + need:] == fill)
+    need = ssm.gated_scan_bwd_workspace_bytes(B, L, D, BF)
+    for fill in (0, 0xFF):
+        ws = torch.full((need + 512,), fill, dtype=torch.uint8, device="cuda")
+        for _ in range(2):
+            g2 = ssm.gated_scan_bwd(**d, dy=dy, dh_last=dh, workspace=ws[256:256 + need])
+            assert all(torch.equal(g[k], g2[k]) for k in g)
+        assert torch.all(ws[:256] == fill) and torch.all(ws[256 + need:] == fill)
+
+
+def test_two_graphs_share_a_workspace():
+    """Two captured calls of different lengths over one workspace, replayed in
+    turn with eager work between."""
+    t1, _, _ = make(1, 3000, 64, BF, seed=1)
+    t2, _, _ = make(2, 1700, 96, F, seed=2)
+    d1, d2 = dev(t1), dev(t2)
+    need = max(ssm.gated_scan_workspace_bytes(1, 3000, 64, BF), ssm.gated_scan_workspace_bytes(2, 1700, 96, F))
+    assert need > 0
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    w1, w2 = ssm.gated_scan_fwd(**d1), ssm.gated_scan_fwd(**d2)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        ssm.gated_scan_fwd(**d1, workspace=ws)
+        ssm.gated_scan_fwd(**d2, workspace=ws)
+    torch.cuda.current_stream().wait_stream(s)
+    g1, g2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g1):
+        o1 = ssm.gated_scan_fwd(**d1, workspace=ws)
+    with torch.cuda.graph(g2):
+        o2 = ssm.gated_scan_fwd(**d2, workspace=ws)
+    for _ in range(4):
+        g1.replay()
+        g2.replay()
+        ws.random_(0, 255)
+        g1.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o1[0], w1[0]) and torch.equal(o1[1], w1[1])
+        assert torch.equal(o2[0], w2[0]) and torch.equal(o2[1], w2[1])
+
+
+def test_odd_values_pass_between_workgroups(monkeypatch):
+    """States and decays that are zero, denormal, infinite or NaN go through
+    the hand-over as through one workgroup (a slot's zero means empty)."""
+    B, L, D = 1, 1500, 64
+    base, dy, _ = make(B, L, D, F, seed=6)
+    base = dev(base)
+    dy = dy.cuda()
+    for case in range(5):
+        d = {k: (v.clone() if isinstance(v, torch.Tensor) else v) for k, v in base.items()}
+        if case == 0:
+            d["x"].zero_()
+            d["h0"].zero_()
+        elif case == 1:
+            d["A"].fill_(-1e5)                       # every decay zero
+            d["x"].mul_(torch.rand(L, 1, device="cuda") < 0.01)
+        elif case == 2:
+            d["x"].fill_(-1e-42)
+            d["h0"].fill_(-1e-44)
+        elif case == 3:
+            d["x"][0, 300, 5] = float("inf")
+            d["x"][0, 700, 6] = float("nan")
+        else:
+            d["x"].neg_().mul_(0.0)                  # zeros of both signs
+        got = []
+        for w in ("1", "3"):
+            monkeypatch.setenv("SSM_GATED_WALKERS", w)
+            y, h, ck = ssm.gated_scan_fwd_ckpt(**d)
+            g = ssm.gated_scan_bwd(**d, dy=dy * (0.0 if case == 0 else 1.0), ckpt=ck)
+            got.append({"y": y, "h": h, "ck": ck, **g})
+        torch.cuda.synchronize()
+        for k in got[0]:
+            a, b = got[0][k], got[1][k]
+            same = (a.view(torch.int32) == b.view(torch.int32)) | (a.isnan() & b.isnan())
+            assert same.all(), (case, k)
+
+
 def test_misaligned_views_are_refused():
     t = dev(make(1, 8, 8, BF)[0])
     flat = torch.zeros(65, dtype=BF, device="cuda")

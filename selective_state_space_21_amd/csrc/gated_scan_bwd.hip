@@ -225,7 +225,14 @@ __global__ __launch_bounds__(kThreads, 4) void gated_bwd(GatedBwdArgs q) {
                 Q = fmaf(ka, Q, kq);
                 P *= ka;
             }
-            if (CHAIN && pos > 0 && tile > 0) chain_put_map(chain, pos, ul, P, Q);
+            if (CHAIN && pos > 0) {
+                if (tile > 0) chain_put_map(chain, pos, ul, P, Q);
+                carry = chain_state_before(chain, pos, ul);
+            }
+            sC[buf][lane] = carry;
+            carry = fmaf(P, carry, Q) + 0.0f;    // -0 is 0
+            if (CHAIN && tile > 0) chain_put_state(chain, pos, ul, carry);
+            if (keeper && tile == 0 && q.dh0) row(q.dh0, b)[ul] = carry;
         }
         // the weighted inputs, for the state's map; what else the gradients
         // need of them is formed again behind the barriers, which costs less
@@ -266,12 +273,6 @@ __global__ __launch_bounds__(kThreads, 4) void gated_bwd(GatedBwdArgs q) {
                 Ps *= ka;
             }
             sS[buf][lane] = first;
-        } else if (wave == kKeep) {
-            if (CHAIN && pos > 0) carry = chain_state_before(chain, pos, lane);
-            sC[buf][lane] = carry;
-            carry = fmaf(P, carry, Q) + 0.0f;    // -0 is 0
-            if (CHAIN && tile > 0) chain_put_state(chain, pos, ul, carry);
-            if (keeper && tile == 0 && q.dh0) row(q.dh0, b)[ul] = carry;
         }
         load(next);                              // after the chain: loads return in order
         if (CHAIN && drawer) drawn = last - chain_draw(chain);

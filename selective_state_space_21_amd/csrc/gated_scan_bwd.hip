@@ -237,7 +237,7 @@ __global__ __launch_bounds__(kThreads, 4) void gated_bwd(GatedBwdArgs q) {
         // the weighted inputs, for the state's map; what else the gradients
         // need of them is formed again behind the barriers, which costs less
         // than the registers to keep it in
-        float ph[V];
+        float ph[V], e2[R][V];
 #pragma unroll
         for (int v = 0; v < V; ++v) ph[v] = 0.0f;
 #pragma unroll
@@ -247,7 +247,8 @@ __global__ __launch_bounds__(kThreads, 4) void gated_bwd(GatedBwdArgs q) {
             RowT::unpack(rg[j], gv);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float i = sigma_of(exp_neg(gv[v], ch[v].bx));
+                e2[j][v] = exp_neg_finite(gv[v], ch[v].bx);
+                const float i = sigma_of(e2[j][v]);
                 const float w = __builtin_amdgcn_sqrtf(one_minus_sq(y[j][v], a[j][v]));
                 ph[v] = fmaf(a[j][v], ph[v], w * (i * xv[v]));
             }
@@ -302,14 +303,12 @@ __global__ __launch_bounds__(kThreads, 4) void gated_bwd(GatedBwdArgs q) {
         float ef[R][V], wi[R][V], hc[R][V];
 #pragma unroll
         for (int j = 0; j < R; ++j) {
-            float xv[V], gv[V];
-            asm volatile("" : "+v"(rg[j]));          // not the values from before the barriers
+            float xv[V];
             RowT::unpack(rx[j], xv);
-            RowT::unpack(rg[j], gv);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                asm volatile("" : "+v"(y[j][v]));
-                const float e = exp_neg_finite(gv[v], ch[v].bx), i = sigma_of(e);
+                asm volatile("" : "+v"(y[j][v]), "+v"(e2[j][v]));   // not the values from before the barriers
+                const float e = e2[j][v], i = sigma_of(e);
                 const float w2 = one_minus_sq(y[j][v], a[j][v]);
                 const float w = __builtin_amdgcn_sqrtf(w2);
                 const float h = w * (i * xv[v]);

@@ -310,13 +310,11 @@ __global__ __launch_bounds__(kThreads, 4) void gated_bwd(GatedBwdArgs q) {
                 asm volatile("" : "+v"(y[j][v]), "+v"(e2[j][v]));   // not the values from before the barriers
                 const float e = e2[j][v], i = sigma_of(e);
                 const float w2 = one_minus_sq(y[j][v], a[j][v]);
-                const float w = __builtin_amdgcn_sqrtf(w2);
-                const float h = w * (i * xv[v]);
-                // (la / w) a^2 i x = (la a / w^2) a b, whose first factor is at
-                // most a half; where w^2 leaves fp32's range, so does the term
-                const float ya = y[j][v] * (kLn2 * a[j][v]);
-                const float s2 = w2 > 1e-37f ? (ya * fast_rcp(w2)) * (a[j][v] * h) : 0.0f;
-                ef[j][v] = fmaf(ya, s[v], -s2);
+                // 1 / w; where w^2 leaves fp32's range, so do its terms
+                const float rw = w2 > 1e-37f ? __builtin_amdgcn_rsqf(w2) : 0.0f;
+                const float w = w2 * rw, ix = i * xv[v], h = w * ix;
+                // la a h_{t-1} - (la / w) a^2 i x
+                ef[j][v] = (y[j][v] * a[j][v]) * kLn2 * fmaf(-(a[j][v] * ix), rw, s[v]);
                 wi[j][v] = w * i;
                 hc[j][v] = h * (e * i);              // 1 - i = e i
                 s[v] = fmaf(a[j][v], s[v], h);

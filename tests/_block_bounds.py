@@ -131,16 +131,18 @@ def gated_bwd(keep, dy, dh_last=None):
     first_err = first * (k["ela"] + k["ea"] + 3 * U) + la.abs() * a * k["before_err"]
     law = torch.where(w > 0, la.abs() / w, zero)
     second = law * a * a * ix
-    # formed as la a a b / w^2: la a, a, b = w i x, rcp(w^2) and the products
-    second_err = second * (k["ela"] + 3 * k["ew"] + 2 * k["ea"] + eix + 9 * U)
+    # formed as la a (h - a i x / w): the root's reciprocal (2u beside half the
+    # error of w^2, which ew holds), the products, and the sum's rounding
+    second_err = second * (k["ela"] + k["ew"] + 2 * k["ea"] + eix + 9 * U) + U * (first + second)
     E = G * (first + second)
     Ee = Ge * (first + second) + G * (first_err + second_err) + 2 * U * E
     c_r, c_i = k["c_r"], k["c_i"]
     ga, gx = E * c_r, G * w * ix * c_i
     # 1 - sigma = e sigma: relative errors of both, added
-    out = {"dx": (G * w * i, Ge * w * i + G * w * i * (k["ew"] + k["ei"] + 2 * U)),
+    # w = w^2 / w: one rounding more than the forward's root
+    out = {"dx": (G * w * i, Ge * w * i + G * w * i * (k["ew"] + k["ei"] + 3 * U)),
            "dgate_a": (ga, Ee * c_r + ga * (2 * k["er"] + 2 * U)),
-           "dgate_x": (gx, Ge * w * ix * c_i + gx * (k["ew"] + eix + 2 * k["ei"] + 3 * U))}
+           "dgate_x": (gx, Ge * w * ix * c_i + gx * (k["ew"] + eix + 2 * k["ei"] + 4 * U))}
     # a sum of n terms: every term passes at most 16 (a run) + 2 (lanes) + 8
     # (wavefronts) + rows / 16 + 16 additions
     rows = B * -(-L // 128)

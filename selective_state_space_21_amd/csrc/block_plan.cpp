@@ -82,7 +82,7 @@ void gated_bwd_carve(GatedBwdArgs& a, void* ws) {
 
 int64_t norm_bwd_groups(int64_t rows, int64_t D) {
     (void)D;
-    return rows < 512 ? rows : 512;
+    return rows < kCUs ? rows : kCUs;       // one workgroup per CU
 }
 
 size_t norm_bwd_workspace_bytes(int64_t rows, int64_t D) {

@@ -8,8 +8,8 @@
 //
 // A row is read once and kept in registers: mean, then the mean square of the
 // differences from it (two passes over registers, so nothing cancels).  TPR
-// threads share a row (a wavefront, or a whole workgroup for long rows) and
-// each holds NV vectors of VEC elements, vector i of thread j being vector
+// threads share a row (8 lanes for the shortest, a wavefront, a whole
+// workgroup for long rows) and each holds NV vectors of VEC elements, vector i of thread j being vector
 // i * TPR + j of the row.  Rows too long for that are read from memory again
 // for every pass.  Both directions are bound by the bytes they move.
 #include <hip/hip_runtime.h>
@@ -23,6 +23,8 @@
 
 namespace ssm {
 namespace {
+
+constexpr int kBwdThreads = 1024;
 
 // VEC elements as fp32: 16-byte vectors of the activations, and for fp32
 // operands beside bf16 ones two of them.  Rows of odd length leave a vector at
@@ -103,28 +105,30 @@ __device__ __forceinline__ void get_param(const float* p, int64_t d, int64_t n, 
     }
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
-    v += __shfl_xor(v, 32, 64);
-    v += lane_xor<16>(v);
-    v += lane_xor<8>(v);
-    v += lane_xor<4>(v);
+// the sum over aligned groups of N lanes, in all of them
+template <int N> __device__ __forceinline__ float lane_sum(float v) {
+    if constexpr (N > 32) v += __shfl_xor(v, 32, 64);
+    if constexpr (N > 16) v += lane_xor<16>(v);
+    if constexpr (N > 8) v += lane_xor<8>(v);
+    if constexpr (N > 4) v += lane_xor<4>(v);
     v += lane_xor<2>(v);
     v += lane_xor<1>(v);
     return v;
 }
 
 // the sum over the TPR threads of a row, in all of them; `s` holds one float
-// per wavefront of the workgroup
+// per wavefront of the workgroup, all of whose threads take part
 template <int TPR> __device__ __forceinline__ float row_sum(float v, float* s) {
-    v = wave_sum(v);
+    v = lane_sum<TPR < 64 ? TPR : 64>(v);
     if constexpr (TPR > 64) {
         constexpr int W = TPR / 64;
+        const int wave = threadIdx.x / 64, first = wave / W * W;
         lds_barrier();                       // the previous sum has been read
-        if (threadIdx.x % 64 == 0) s[threadIdx.x / 64] = v;
+        if (threadIdx.x % 64 == 0) s[wave] = v;
         lds_barrier();
-        v = s[0];
+        v = s[first];
 #pragma unroll
-        for (int k = 1; k < W; ++k) v += s[k];
+        for (int k = 1; k < W; ++k) v += s[first + k];
     }
     return v;
 }
@@ -134,9 +138,10 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd(NormArgs p) {
     constexpr int kThreads = TPR > 256 ? TPR : 256;
     __shared__ float s[kThreads / 64];
     const int j = threadIdx.x % TPR;
-    const int64_t row = (int64_t)blockIdx.x * (kThreads / TPR) + threadIdx.x / TPR;
-    if (row >= p.rows) return;               // a whole wavefront (TPR = 64) or nobody
-    const int64_t o = row * p.D;
+    const int64_t at = (int64_t)blockIdx.x * (kThreads / TPR) + threadIdx.x / TPR;
+    if (TPR == 64 && at >= p.rows) return;   // a whole wavefront
+    const bool there = at < p.rows;          // (the lanes of a wavefront sum together: all stay)
+    const int64_t row = there ? at : p.rows - 1, o = row * p.D;
     const T* x = static_cast<const T*>(p.x) + o;
     float v[NV][VEC];
     float sum = 0.0f;
@@ -166,6 +171,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd(NormArgs p) {
         }
     }
     const float rstd = 1.0f / sqrtf(fmaf(row_sum<TPR>(sum, s), inv, p.eps));
+    if (TPR < 64 && !there) return;
     if (j == 0) {
         if (p.mean) p.mean[row] = mean;
         if (p.rstd) p.rstd[row] = rstd;
@@ -218,17 +224,21 @@ __global__ __launch_bounds__(1024) void norm_fwd_long(NormArgs p) {
 
 // X: the type of the normalised input (the fp32 stream, or the activations'),
 // T: the activations' type.
+// A workgroup of 1024 threads takes 1024 / TPR rows at a time and a share of
+// all rows, with its sums for the parameters in registers: one workgroup per
+// CU, so that there are few partial sums to write and read (16384 x 2048 bf16:
+// 75 us with 512 workgroups of four rows, which leave a CU eight wavefronts).
 template <bool WHOLE, typename X, typename T, int VEC, int NV, int TPR>
-__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd(NormBwdArgs p) {
-    constexpr int kThreads = TPR > 256 ? TPR : 256;
-    constexpr int kRows = kThreads / TPR;
-    __shared__ float s[kThreads / 64];
-    __shared__ float join[kRows > 1 ? kRows - 1 : 1][TPR > 64 ? 1 : VEC][TPR];
+__global__ __launch_bounds__(kBwdThreads) void norm_bwd(NormBwdArgs p) {
+    constexpr int kRows = kBwdThreads / TPR;
+    constexpr int kJoin = TPR < 64 ? kBwdThreads / 64 : kRows;      // rows of partial sums left to join
+    __shared__ float s[kBwdThreads / 64];
+    __shared__ float join[kJoin > 1 ? kJoin : 1][VEC][kJoin > 1 ? TPR : 1];
     const int j = threadIdx.x % TPR, sub = threadIdx.x / TPR;
     const float inv = 1.0f / (float)p.D;
-    // the weight stays in registers, or is read again for every row where 16
-    // elements a thread at 128 registers leave no room for it
-    constexpr bool HOLD = TPR < 1024 || NV * VEC <= 8;
+    // the weight stays in registers, or is read again (through the cache) for
+    // every row where 16 elements a thread at 128 registers leave no room
+    constexpr bool HOLD = NV * VEC <= 8;
     float w[HOLD ? NV : 1][VEC], dw[NV][VEC], db[NV][VEC];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -237,8 +247,9 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd(NormBwdArgs p)
 #pragma unroll
         for (int k = 0; k < VEC; ++k) dw[i][k] = db[i][k] = 0.0f;
     }
-    for (int64_t row = (int64_t)blockIdx.x * kRows + sub; row < p.rows; row += p.groups * kRows) {
-        const int64_t o = row * p.D;
+    for (int64_t row0 = (int64_t)blockIdx.x * kRows; row0 < p.rows; row0 += p.groups * kRows) {
+        const bool there = row0 + sub < p.rows;                     // all threads sum together
+        const int64_t row = there ? row0 + sub : p.rows - 1, o = row * p.D;
         const float mean = p.mean[row], rstd = p.rstd[row];
         float n[NV][VEC], v[NV][VEC];
         float c1 = 0.0f, c2 = 0.0f;
@@ -246,7 +257,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd(NormBwdArgs p)
         for (int i = 0; i < NV; ++i) {
             const int64_t d = (int64_t)(i * TPR + j) * VEC, left = p.D - d;
             get<WHOLE, X, VEC>(static_cast<const X*>(p.x) + o + d, left, n[i]);
-            get<WHOLE, T, VEC>(static_cast<const T*>(p.dy) + o + d, left, v[i]);      // zero behind the row
+            get<WHOLE, T, VEC>(static_cast<const T*>(p.dy) + o + d, there ? left : 0, v[i]);   // zero behind the row
             float (&wi)[VEC] = w[HOLD ? i : 0];
             if (!HOLD) get_param<WHOLE, VEC>(p.weight, d, left, wi, 1.0f);
 #pragma unroll
@@ -261,6 +272,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd(NormBwdArgs p)
         }
         c1 = row_sum<TPR>(c1, s) * inv;
         c2 = row_sum<TPR>(c2, s) * inv;
+        if (!there) continue;                // (no barrier is left in the last round)
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int64_t d = (int64_t)(i * TPR + j) * VEC, left = p.D - d;
@@ -274,28 +286,39 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd(NormBwdArgs p)
             put<WHOLE, T, VEC>(static_cast<T*>(p.dx) + o + d, left, g);
         }
     }
-    // join the rows that ran side by side, then this workgroup's row of part
+    // join the rows that ran side by side -- a wavefront's by lanes, then the
+    // others in order -- for this workgroup's row of part
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
             float (&a)[VEC] = which ? db[i] : dw[i];
-            if constexpr (kRows > 1) {
-                lds_barrier();
-                if (sub > 0) {
+            if constexpr (TPR < 64) {
 #pragma unroll
-                    for (int k = 0; k < VEC; ++k) join[sub - 1][k][j] = a[k];
+                for (int k = 0; k < VEC; ++k) {
+                    if constexpr (TPR <= 8) a[k] += lane_xor<8>(a[k]);
+                    if constexpr (TPR <= 16) a[k] += lane_xor<16>(a[k]);
+                    a[k] += __shfl_xor(a[k], 32, 64);
+                }
+            }
+            const int from = TPR < 64 ? threadIdx.x / 64 : sub;
+            const bool puts = TPR >= 64 || threadIdx.x % 64 < TPR;
+            if constexpr (kJoin > 1) {
+                lds_barrier();
+                if (puts) {
+#pragma unroll
+                    for (int k = 0; k < VEC; ++k) join[from][k][j] = a[k];
                 }
                 lds_barrier();
-                if (sub == 0) {
+                if (puts && from == 0) {
 #pragma unroll
-                    for (int m = 0; m < kRows - 1; ++m)
+                    for (int m = 1; m < kJoin; ++m)
 #pragma unroll
                         for (int k = 0; k < VEC; ++k) a[k] += join[m][k][j];
                 }
             }
             const int64_t d = (int64_t)(i * TPR + j) * VEC;
-            if (sub == 0 && d < p.D) {
+            if (puts && from == 0 && d < p.D) {
                 float* out = p.part + ((int64_t)blockIdx.x * 2 + which) * p.D + d;
 #pragma unroll
                 for (int k = 0; k < VEC; ++k)
@@ -359,6 +382,9 @@ hipError_t launch_fwd(const NormArgs& a, hipStream_t stream) {
 template <bool WHOLE, typename T, bool RES, int VEC>
 hipError_t launch_fwd_v(const NormArgs& a, hipStream_t stream) {
     const int64_t nv = (a.D + VEC - 1) / VEC;
+    if (nv <= 8) return launch_fwd<WHOLE, T, RES, VEC, 1, 8>(a, stream);
+    if (nv <= 16) return launch_fwd<WHOLE, T, RES, VEC, 1, 16>(a, stream);
+    if (nv <= 32) return launch_fwd<WHOLE, T, RES, VEC, 1, 32>(a, stream);
     if (nv <= 64) return launch_fwd<WHOLE, T, RES, VEC, 1, 64>(a, stream);
     if (nv <= 128) return launch_fwd<WHOLE, T, RES, VEC, 2, 64>(a, stream);
     if (nv <= 256) return launch_fwd<WHOLE, T, RES, VEC, 4, 64>(a, stream);
@@ -380,7 +406,7 @@ hipError_t launch_fwd_t(const NormArgs& a, hipStream_t stream) {
 
 template <bool WHOLE, typename X, typename T, int VEC, int NV, int TPR>
 hipError_t launch_bwd(const NormBwdArgs& a, hipStream_t stream) {
-    norm_bwd<WHOLE, X, T, VEC, NV, TPR><<<(unsigned)a.groups, TPR > 256 ? TPR : 256, 0, stream>>>(a);
+    norm_bwd<WHOLE, X, T, VEC, NV, TPR><<<(unsigned)a.groups, kBwdThreads, 0, stream>>>(a);
     return hipGetLastError();
 }
 
@@ -388,6 +414,9 @@ hipError_t launch_bwd(const NormBwdArgs& a, hipStream_t stream) {
 template <bool WHOLE, typename X, typename T, int VEC>
 hipError_t launch_bwd_w(const NormBwdArgs& a, hipStream_t stream) {
     const int64_t nv = (a.D + VEC - 1) / VEC;
+    if (nv <= 8) return launch_bwd<WHOLE, X, T, VEC, 1, 8>(a, stream);
+    if (nv <= 16) return launch_bwd<WHOLE, X, T, VEC, 1, 16>(a, stream);
+    if (nv <= 32) return launch_bwd<WHOLE, X, T, VEC, 1, 32>(a, stream);
     if (nv <= 64) return launch_bwd<WHOLE, X, T, VEC, 1, 64>(a, stream);
     if (nv <= 128) return launch_bwd<WHOLE, X, T, VEC, 2, 64>(a, stream);
     if (nv <= 256) return launch_bwd<WHOLE, X, T, VEC, 1, 256>(a, stream);

@@ -187,7 +187,7 @@ def norm(x, weight=None, bias=None, residual=None, eps=1e-5):
         dict(n=n, en=en, rstd=rstd, er=er, w=wa, D=D)
 
 
-def norm_bwd(keep, dy, dresidual_out=None, rows=None, groups=512):
+def norm_bwd(keep, dy, dresidual_out=None, groups=256):
     n, en, rstd, er, w, D = (keep[k] for k in ("n", "en", "rstd", "er", "w", "D"))
     dy = _f64(dy)
     v = (dy * w).abs()
@@ -206,8 +206,9 @@ def norm_bwd(keep, dy, dresidual_out=None, rows=None, groups=512):
     flat = lambda t: t.reshape(-1, D)                        # noqa: E731
     rows = flat(dy).shape[0]
     # a term of a parameter's gradient: its workgroup's rows one after the
-    # other, three joins, then the groups by sixteens
-    depth = -(-rows // max(1, min(groups, rows))) + 3 + groups / 16 + 16 + 1
+    # other, three joins of lanes, 16 of wavefronts, then the workgroups by
+    # sixteens
+    depth = -(-rows // max(1, min(groups, rows))) + 3 + 16 + groups / 16 + 16 + 1
     d = flat(dy).abs()
     return dict(dx=eg, dweight=(d * flat(en) + (depth + 1) * U * d * flat(na)).sum(0),
                 dbias=(depth * U * d).sum(0))

@@ -31,19 +31,19 @@ constexpr int kBwdThreads = 1024;
 // any element's alignment, which the hardware's global accesses allow (a row
 // of 2561 fp32 elements by single elements: 24.1 us for forward and backward
 // of 777 rows where whole vectors take 13.5).
-template <typename T> struct Vec16;
-template <> struct Vec16<uint16_t> {
+template <int VEC> struct Bits;                  // VEC bf16 elements
+template <> struct Bits<8> {
     typedef uint32_t type __attribute__((ext_vector_type(4), aligned(2)));
 };
-template <> struct Vec16<float> {
-    typedef float type __attribute__((ext_vector_type(4), aligned(4)));
+template <> struct Bits<4> {
+    typedef uint32_t type __attribute__((ext_vector_type(2), aligned(2)));
 };
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 
 template <int VEC> __device__ __forceinline__ void load_all(const uint16_t* p, float (&v)[VEC]) {
-    static_assert(VEC == 8, "one 16-byte vector");
-    const auto r = __builtin_nontemporal_load(reinterpret_cast<const Vec16<uint16_t>::type*>(p));
+    const auto r = __builtin_nontemporal_load(reinterpret_cast<const typename Bits<VEC>::type*>(p));
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < VEC / 2; ++k) {
         v[2 * k] = __uint_as_float(r[k] << 16);
         v[2 * k + 1] = __uint_as_float(r[k] & 0xffff0000u);
     }
@@ -51,23 +51,23 @@ template <int VEC> __device__ __forceinline__ void load_all(const uint16_t* p, f
 template <int VEC> __device__ __forceinline__ void load_all(const float* p, float (&v)[VEC]) {
 #pragma unroll
     for (int i = 0; i < VEC / 4; ++i) {
-        const auto r = __builtin_nontemporal_load(reinterpret_cast<const Vec16<float>::type*>(p) + i);
+        const auto r = __builtin_nontemporal_load(reinterpret_cast<const f32x4_any*>(p) + i);
 #pragma unroll
         for (int k = 0; k < 4; ++k) v[4 * i + k] = r[k];
     }
 }
 template <int VEC> __device__ __forceinline__ void store_all(uint16_t* p, const float (&v)[VEC]) {
-    typename Vec16<uint16_t>::type r;
+    typename Bits<VEC>::type r;
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < VEC / 2; ++k)
         r[k] = (uint32_t)f32_to_bf16_bits(v[2 * k]) | ((uint32_t)f32_to_bf16_bits(v[2 * k + 1]) << 16);
-    __builtin_nontemporal_store(r, reinterpret_cast<Vec16<uint16_t>::type*>(p));
+    __builtin_nontemporal_store(r, reinterpret_cast<typename Bits<VEC>::type*>(p));
 }
 template <int VEC> __device__ __forceinline__ void store_all(float* p, const float (&v)[VEC]) {
 #pragma unroll
     for (int i = 0; i < VEC / 4; ++i) {
-        const typename Vec16<float>::type r = {v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
-        __builtin_nontemporal_store(r, reinterpret_cast<Vec16<float>::type*>(p) + i);
+        const f32x4_any r = {v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+        __builtin_nontemporal_store(r, reinterpret_cast<f32x4_any*>(p) + i);
     }
 }
 
@@ -238,7 +238,7 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd(NormBwdArgs p) {
     const float inv = 1.0f / (float)p.D;
     // the weight stays in registers, or is read again (through the cache) for
     // every row where 16 elements a thread at 128 registers leave no room
-    constexpr bool HOLD = NV * VEC <= 8;
+    constexpr bool HOLD = NV * VEC <= 12;
     float w[HOLD ? NV : 1][VEC], dw[NV][VEC], db[NV][VEC];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -410,26 +410,41 @@ hipError_t launch_bwd(const NormBwdArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// (at most 16 elements a thread: five values of each are in registers)
-template <bool WHOLE, typename X, typename T, int VEC>
+// At most 16 elements a thread: four or five values of each are in registers.
+// Where the normalised input is fp32 (bf16 or fp32 around it), vectors of four
+// elements, at most four to a thread, and the fewest threads to a row that can
+// hold it so: three quarters of them or more have work (the stream's 16384 x
+// 768: 40.8 us against 47.5 with vectors of eight, 96 of 128 lanes with work).
+// Where all is bf16, 16-byte vectors of eight, two to a thread (16384 x 2048:
+// 51 us against 65 with vectors of four).
+template <bool WHOLE, typename X, typename T, int TPR>
+hipError_t launch_bwd_n(const NormBwdArgs& a, int64_t nv, hipStream_t stream) {
+    return nv <= 3 * TPR ? launch_bwd<WHOLE, X, T, 4, 3, TPR>(a, stream) : launch_bwd<WHOLE, X, T, 4, 4, TPR>(a, stream);
+}
+template <bool WHOLE, typename X, typename T>
 hipError_t launch_bwd_w(const NormBwdArgs& a, hipStream_t stream) {
-    const int64_t nv = (a.D + VEC - 1) / VEC;
-    if (nv <= 8) return launch_bwd<WHOLE, X, T, VEC, 1, 8>(a, stream);
-    if (nv <= 16) return launch_bwd<WHOLE, X, T, VEC, 1, 16>(a, stream);
-    if (nv <= 32) return launch_bwd<WHOLE, X, T, VEC, 1, 32>(a, stream);
-    if (nv <= 64) return launch_bwd<WHOLE, X, T, VEC, 1, 64>(a, stream);
-    if (nv <= 128) return launch_bwd<WHOLE, X, T, VEC, 2, 64>(a, stream);
-    if (nv <= 256) return launch_bwd<WHOLE, X, T, VEC, 1, 256>(a, stream);
-    if (nv <= 512) return launch_bwd<WHOLE, X, T, VEC, 2, 256>(a, stream);
-    if constexpr (VEC == 4) {
-        if (nv <= 768) return launch_bwd<WHOLE, X, T, VEC, 3, 256>(a, stream);
-        if (nv <= 1024) return launch_bwd<WHOLE, X, T, VEC, 4, 256>(a, stream);
+    if constexpr (sizeof(X) == 4) {
+        const int64_t nv = (a.D + 3) / 4;
+        if (nv <= 16) return launch_bwd<WHOLE, X, T, 4, 1, 16>(a, stream);
+        if (nv <= 32) return launch_bwd<WHOLE, X, T, 4, 2, 16>(a, stream);
+        if (nv <= 64) return launch_bwd_n<WHOLE, X, T, 16>(a, nv, stream);
+        if (nv <= 128) return launch_bwd_n<WHOLE, X, T, 32>(a, nv, stream);
+        if (nv <= 256) return launch_bwd_n<WHOLE, X, T, 64>(a, nv, stream);
+        if (nv <= 512) return launch_bwd_n<WHOLE, X, T, 128>(a, nv, stream);
+        if (nv <= 1024) return launch_bwd_n<WHOLE, X, T, 256>(a, nv, stream);
+        if (nv <= 2048) return launch_bwd_n<WHOLE, X, T, 512>(a, nv, stream);
+        if (nv <= 4096) return launch_bwd_n<WHOLE, X, T, 1024>(a, nv, stream);
     } else {
-        if (nv <= 1024) return launch_bwd<WHOLE, X, T, VEC, 1, 1024>(a, stream);
-    }
-    if (nv <= 2048) return launch_bwd<WHOLE, X, T, VEC, 2, 1024>(a, stream);
-    if constexpr (VEC == 4) {
-        if (nv <= 4096) return launch_bwd<WHOLE, X, T, VEC, 4, 1024>(a, stream);
+        const int64_t nv = (a.D + 7) / 8;
+        if (nv <= 8) return launch_bwd<WHOLE, X, T, 8, 1, 8>(a, stream);
+        if (nv <= 16) return launch_bwd<WHOLE, X, T, 8, 1, 16>(a, stream);
+        if (nv <= 32) return launch_bwd<WHOLE, X, T, 8, 1, 32>(a, stream);
+        if (nv <= 64) return launch_bwd<WHOLE, X, T, 8, 1, 64>(a, stream);
+        if (nv <= 128) return launch_bwd<WHOLE, X, T, 8, 2, 64>(a, stream);
+        if (nv <= 256) return launch_bwd<WHOLE, X, T, 8, 2, 128>(a, stream);
+        if (nv <= 512) return launch_bwd<WHOLE, X, T, 8, 2, 256>(a, stream);
+        if (nv <= 1024) return launch_bwd<WHOLE, X, T, 8, 2, 512>(a, stream);
+        if (nv <= 2048) return launch_bwd<WHOLE, X, T, 8, 2, 1024>(a, stream);
     }
     norm_bwd_long<X, T><<<(unsigned)a.rows, 1024, 0, stream>>>(a);
     norm_bwd_columns<X, T>
@@ -437,9 +452,9 @@ hipError_t launch_bwd_w(const NormBwdArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <typename X, typename T, int VEC>
-hipError_t launch_bwd_v(const NormBwdArgs& a, hipStream_t stream) {
-    return a.D % VEC == 0 ? launch_bwd_w<true, X, T, VEC>(a, stream) : launch_bwd_w<false, X, T, VEC>(a, stream);
+template <typename X, typename T>
+hipError_t launch_bwd_t(const NormBwdArgs& a, hipStream_t stream) {
+    return a.D % (sizeof(X) == 4 ? 4 : 8) == 0 ? launch_bwd_w<true, X, T>(a, stream) : launch_bwd_w<false, X, T>(a, stream);
 }
 
 }  // namespace
@@ -452,9 +467,9 @@ hipError_t launch_layer_norm(const NormArgs& a, hipStream_t stream) {
 hipError_t launch_layer_norm_bwd(const NormBwdArgs& a, hipStream_t stream) {
     if (a.rows > 0) {
         hipError_t e;
-        if (!a.bf16) e = launch_bwd_v<float, float, 4>(a, stream);
-        else if (a.x_bf16) e = launch_bwd_v<uint16_t, uint16_t, 8>(a, stream);
-        else e = launch_bwd_v<float, uint16_t, 8>(a, stream);
+        if (!a.bf16) e = launch_bwd_t<float, float>(a, stream);
+        else if (a.x_bf16) e = launch_bwd_t<uint16_t, uint16_t>(a, stream);
+        else e = launch_bwd_t<float, uint16_t>(a, stream);
         if (e != hipSuccess) return e;
     }
     if (!a.dweight && !a.dbias) return hipSuccess;

@@ -28,13 +28,12 @@ namespace ssm {
 namespace {
 
 using gated::kStrip;
-constexpr int kThreads = gated::kFwdThreads;
-constexpr int kTile = gated::kFwdTile;
-constexpr int kSaved = kTile / SSM_GATED_TILE;       // states saved per tile
-
-template <typename T, int V, bool CHAIN>
-__global__ __launch_bounds__(kThreads, 4) void gated_fwd(GatedArgs p) {
-    using S = TileShape<V, kTile, kThreads>;
+// THREADS: 1024, or as many as the tokens of a sequence of one short tile need
+template <typename T, int V, bool CHAIN, int THREADS>
+__global__ __launch_bounds__(THREADS, 4) void gated_fwd(GatedArgs p) {
+    constexpr int kTile = gated::kFwdTile * THREADS / gated::kFwdThreads;
+    constexpr int kSaved = kTile > SSM_GATED_TILE ? kTile / SSM_GATED_TILE : 1;   // states saved per tile
+    using S = TileShape<V, kTile, THREADS>;
     using RowT = Row<T, V>;
     constexpr int R = S::kRun;
     // per wavefront and channel: the pair of its tokens, then (exclusive) the
@@ -256,21 +255,28 @@ hipError_t launch_step(const GatedStepArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <typename T>
-hipError_t launch_fwd(const GatedArgs& a, hipStream_t stream) {
+template <typename T, int V>
+hipError_t launch_fwd_v(const GatedArgs& a, hipStream_t stream) {
     const unsigned grid = (unsigned)(a.plan.strips * a.plan.walkers);
     if (a.plan.walkers > 1) {
         if (!a.cleared) {
             const hipError_t e = launch_chain_clear(a.chain, a.plan.chain_bytes, stream);
             if (e != hipSuccess) return e;
         }
-        if (a.D % 2 == 0) gated_fwd<T, 2, true><<<grid, kThreads, 0, stream>>>(a);
-        else gated_fwd<T, 1, true><<<grid, kThreads, 0, stream>>>(a);
+        gated_fwd<T, V, true, 1024><<<grid, 1024, 0, stream>>>(a);
+    } else if (a.L <= gated::kFwdTile / 4) {
+        gated_fwd<T, V, false, 256><<<grid, 256, 0, stream>>>(a);
+    } else if (a.L <= gated::kFwdTile / 2) {
+        gated_fwd<T, V, false, 512><<<grid, 512, 0, stream>>>(a);
     } else {
-        if (a.D % 2 == 0) gated_fwd<T, 2, false><<<grid, kThreads, 0, stream>>>(a);
-        else gated_fwd<T, 1, false><<<grid, kThreads, 0, stream>>>(a);
+        gated_fwd<T, V, false, 1024><<<grid, 1024, 0, stream>>>(a);
     }
     return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_fwd(const GatedArgs& a, hipStream_t stream) {
+    return a.D % 2 == 0 ? launch_fwd_v<T, 2>(a, stream) : launch_fwd_v<T, 1>(a, stream);
 }
 
 }  // namespace

@@ -26,13 +26,12 @@ namespace ssm {
 namespace {
 
 using gated::kStrip;
-constexpr int kThreads = gated::kBwdThreads;
-constexpr int kTile = gated::kBwdTile;
-constexpr int kWaves = kThreads / 64;
 
-template <typename T, int V, bool CHAIN>
-__global__ __launch_bounds__(kThreads, 4) void gated_bwd(GatedBwdArgs q) {
-    using S = TileShape<V, kTile, kThreads>;
+// THREADS: 1024, or as many as the tokens of a sequence of one short tile need
+template <typename T, int V, bool CHAIN, int THREADS>
+__global__ __launch_bounds__(THREADS, 4) void gated_bwd(GatedBwdArgs q) {
+    constexpr int kTile = gated::kBwdTile * THREADS / gated::kBwdThreads, kWaves = THREADS / 64;
+    using S = TileShape<V, kTile, THREADS>;
     using RowT = Row<T, V>;
     constexpr int R = S::kRun;
     const GatedArgs& p = q.f;
@@ -358,17 +357,19 @@ __global__ __launch_bounds__(kThreads, 4) void gated_bwd(GatedBwdArgs q) {
     if (before >= 0) put_sums(buf ^ 1, before);
 }
 
+template <typename T, int V>
+hipError_t launch_bwd_v(const GatedBwdArgs& a, hipStream_t stream) {
+    const unsigned grid = (unsigned)(a.plan.strips * a.plan.walkers);
+    if (a.plan.walkers > 1) gated_bwd<T, V, true, 1024><<<grid, 1024, 0, stream>>>(a);
+    else if (a.f.L <= gated::kBwdTile / 4) gated_bwd<T, V, false, 256><<<grid, 256, 0, stream>>>(a);
+    else if (a.f.L <= gated::kBwdTile / 2) gated_bwd<T, V, false, 512><<<grid, 512, 0, stream>>>(a);
+    else gated_bwd<T, V, false, 1024><<<grid, 1024, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
 template <typename T>
 hipError_t launch_bwd(const GatedBwdArgs& a, hipStream_t stream) {
-    const unsigned grid = (unsigned)(a.plan.strips * a.plan.walkers);
-    if (a.plan.walkers > 1) {
-        if (a.f.D % 2 == 0) gated_bwd<T, 2, true><<<grid, kThreads, 0, stream>>>(a);
-        else gated_bwd<T, 1, true><<<grid, kThreads, 0, stream>>>(a);
-    } else {
-        if (a.f.D % 2 == 0) gated_bwd<T, 2, false><<<grid, kThreads, 0, stream>>>(a);
-        else gated_bwd<T, 1, false><<<grid, kThreads, 0, stream>>>(a);
-    }
-    return hipGetLastError();
+    return a.f.D % 2 == 0 ? launch_bwd_v<T, 2>(a, stream) : launch_bwd_v<T, 1>(a, stream);
 }
 
 __global__ __launch_bounds__(256) void gated_bwd_pass(const float* dh_last, float* dh0, int64_t n) {

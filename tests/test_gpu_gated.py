@@ -37,6 +37,8 @@ SHAPES = [
     (2, 129, 60, None), (1, 255, 68, None), (2, 257, 130, None), (1, 640, 33, None),
     (4, 300, 72, [0, 1, 299, 300]), (5, 260, 67, [128, 129, 127, 256, 0]),
     (3, 131, 4, [-4, 1000, 130]), (2, 1500, 8, None), (2, 1300, 3, [1300, 5]),
+    (2, 32, 66, None), (3, 33, 64, [33, 32, 0]), (2, 64, 65, [64, 31]), (3, 65, 128, [65, 64, 1]),
+    (2, 97, 62, [97, 96]),
 ]
 
 

@@ -7,6 +7,10 @@
  *   ssm_selective_scan_fwd  -- the S6 selective scan (Mamba-1 layer scan)
  *   ssm_ssd_chunk_fwd       -- the scalar-decay-per-head SSD form (Mamba-2)
  *
+ * and the calls around them: the S6 decode step and backward, the causal
+ * conv1d + SiLU and its backward, the gated linear recurrence (forward,
+ * backward, decode step), and layer norm with the residual stream.
+ *
  * Conventions shared by every entry point
  *   - All tensor arguments are DEVICE pointers owned by the caller, row-major
  *     and contiguous in the stated shape (last axis fastest).  The library
@@ -506,10 +510,11 @@ int ssm_causal_conv1d_silu_bwd(const void* x, const float* weight, const float* 
  *                    state after the row's last token
  *   B >= 1; 1 <= D <= 2^20; L >= 0; B * ceil(D / 64) below 2^25.
  * The sequence is walked in tiles of 256 tokens by 64 channels (128 tokens in
- * the backward).  With enough of those strips of 64 channels to fill the GPU (or few tiles) a
- * workgroup walks a strip alone; else several walk it together, each taking
- * the next tile, and hand the state on through the workspace (256-byte
- * aligned, 0 bytes for one walker; the call clears what it needs of it).
+ * the backward).  With enough of those strips of 64 channels to fill the GPU
+ * (or few tiles) a workgroup walks a strip alone; else several walk it
+ * together, each taking the next tile, and hand the state on through the
+ * workspace (256-byte aligned, 0 bytes for one walker; the call clears what it
+ * needs of it).  Calls that may run at the same time need a workspace each.
  * ssm_gated_scan_walkers and ssm_gated_scan_bwd_walkers return their number
  * for the two directions (0 for invalid sizes), a pure function of the sizes; the environment variable SSM_GATED_WALKERS (1..64)
  * overrides it, for the queries and the calls.  Results do not depend on the

@@ -19,7 +19,7 @@ int64_t al256(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 // makes a tile cost `handover` percent.  Measured, bf16, L = 2048, forward: 192
 // strips 63.6 us alone, 58.3 with two walkers; 256: 67.8, 75.0; 320: 132, 116;
 // 448: 128, 131; 32 strips of L = 131072: 3451, 531 with eight (sixteen: 532).
-// Backward: 192 strips 122, 137.  With three tiles or fewer (17 us against 22
+// Backward: 192 strips 117, 122.  With three tiles or fewer (17 us against 22
 // for two at 125 strips, both mostly launch) the second launch costs more than
 // it gives.
 namespace {

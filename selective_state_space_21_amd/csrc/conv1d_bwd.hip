@@ -14,6 +14,12 @@
 // loads of kFlight tokens under way at a time.  Rows are addressed through
 // buffer resources that end with the sequence: behind it x and du read as
 // zero, so g is zero there, and stores are dropped.
+//
+// Measured at B=8 L=2048 D=1536 K=4 bf16 (151 MB): 41.5 us, 3.6 TB/s, and 4.5
+// for the sums' last step; one channel a thread and one token in flight 91.
+// Sixteen tokens in flight 44.8 us for the call against 43.8, the next eight
+// loaded ahead 44.2, runs of 64 tokens 45.0, four wavefronts to a workgroup
+// 43.9.
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>

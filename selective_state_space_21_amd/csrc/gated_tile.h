@@ -128,13 +128,13 @@ __device__ __forceinline__ int64_t row_tokens(const GatedArgs& p, int64_t b) {
 //   zero until then (the call clears them first), so a reader sees nothing or
 //   the whole value and no other ordering is needed.  A zero P or state is put
 //   up as -0 (its bits are not zero) and counts as the same number.
-// * Workgroups draw a strip's tiles in order from a counter, one or
-//   two ahead, and finish them in that order.  A tile waits for earlier ones only,
-//   and of the unfinished tiles that were drawn the earliest waits for
-//   nothing: its workgroup is running and on that tile, whatever else the
-//   GPU runs.  So every wait ends.  (Two calls at once over one workspace
-//   break that, and the rule that forbids it; a wait is given up after some
-//   seconds then, with NaN for the state, rather than never.)
+// * Workgroups draw a strip's tiles in order from a counter, one or two ahead,
+//   and finish them in that order.  A tile waits for earlier ones only, and of
+//   the unfinished tiles that were drawn the earliest waits for nothing: its
+//   workgroup is running and on that tile, whatever else the GPU runs.  So
+//   every wait ends.  (Two calls at once over one workspace break that, and the
+//   rule that forbids it; a wait is given up after some seconds then, with NaN
+//   for the state, rather than never.)
 struct Chain {
     uint32_t* ticket;     // the strip's counter
     uint64_t* maps;       // [tiles][64], P in the low half; kBack - 1 empty tiles in front
@@ -156,11 +156,13 @@ __device__ __forceinline__ int chain_draw(const Chain& c) {
     return (int)__hip_atomic_fetch_add(c.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 __device__ __forceinline__ void chain_put_map(const Chain& c, int tile, uint32_t lane, float P, float H) {
-    __hip_atomic_store(c.maps + (int64_t)tile * gated::kStrip + lane, (uint64_t)chain_bits(P) | ((uint64_t)__float_as_uint(H) << 32),
-                       __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store(c.maps + (int64_t)tile * gated::kStrip + lane,
+                       (uint64_t)chain_bits(P) | ((uint64_t)__float_as_uint(H) << 32), __ATOMIC_RELAXED,
+                       __HIP_MEMORY_SCOPE_AGENT);
 }
 __device__ __forceinline__ void chain_put_state(const Chain& c, int tile, uint32_t lane, float h) {
-    __hip_atomic_store(c.states + (int64_t)tile * gated::kStrip + lane, chain_bits(h), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store(c.states + (int64_t)tile * gated::kStrip + lane, chain_bits(h), __ATOMIC_RELAXED,
+                       __HIP_MEMORY_SCOPE_AGENT);
 }
 
 // The state before tile `pos` >= 1 of this lane's channel, by one wavefront.

@@ -12,6 +12,12 @@
 // workgroup for long rows) and each holds NV vectors of VEC elements, vector i of thread j being vector
 // i * TPR + j of the row.  Rows too long for that are read from memory again
 // for every pass.  Both directions are bound by the bytes they move.
+//
+// Measured with the residual stream, 16384 x 768 bf16: forward (151 MB) 32.0
+// us, 4.7 TB/s; backward (201 MB) 40.9 us, 4.9 TB/s, 4 of them the sums' last
+// step.  33M elements without it: D = 64 to 16384 bf16 27 to 34 us forward, 42
+// to 70 backward (at the copy rate 27 and 40), fp32 45 to 58 and 69 to 93 (54
+// and 81).
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>
@@ -28,9 +34,9 @@ constexpr int kBwdThreads = 1024;
 
 // VEC elements as fp32: 16-byte vectors of the activations, and for fp32
 // operands beside bf16 ones two of them.  Rows of odd length leave a vector at
-// any element's alignment, which the hardware's global accesses allow (a row
-// of 2561 fp32 elements by single elements: 24.1 us for forward and backward
-// of 777 rows where whole vectors take 13.5).
+// any element's alignment, which the hardware's global accesses allow (777
+// rows of 2561 fp32 elements, forward and backward without the sums' last
+// step: 25.0 us by single elements, 17.3 by vectors).
 template <int VEC> struct Bits;                  // VEC bf16 elements
 template <> struct Bits<8> {
     typedef uint32_t type __attribute__((ext_vector_type(4), aligned(2)));

@@ -21,9 +21,10 @@ __device__ __forceinline__ GatedChannel gated_channel(float A, float bias_a, flo
 __device__ __forceinline__ float exp_neg(float gate, float bias) {
     return fast_exp2(fmaf(gate, -kLog2e, bias));
 }
-// the same held below 2^126, for 1 - sigma = e sigma
+// the same held below 2^126, for 1 - sigma = e sigma; the minimum that keeps a
+// NaN (one instruction; fminf would shut the gate)
 __device__ __forceinline__ float exp_neg_finite(float gate, float bias) {
-    return fast_exp2(fminf(fmaf(gate, -kLog2e, bias), 126.0f));
+    return fast_exp2(__builtin_elementwise_minimum(fmaf(gate, -kLog2e, bias), 126.0f));
 }
 __device__ __forceinline__ float sigma_of(float e) { return fast_rcp(1.0f + e); }
 

@@ -1,0 +1,47 @@
+"""Values a caller does not expect in the calls around the scan: what is not a
+number stays visible in the gradients, and what is infinite stays where it
+belongs."""
+import pytest
+import torch
+
+import selective_state_space_21_amd as ssm
+from oracle import block as O
+
+import _block_bounds as Bd
+from test_gpu_gated import dev, make
+
+pytestmark = pytest.mark.gpu
+
+BF, F = torch.bfloat16, torch.float32
+NAN, INF = float("nan"), float("inf")
+
+
+def compare_nan(got, ref, err):
+    """NaN exactly where the definition has it, the other elements within the
+    bounds of the same call without the NaN (which they do not depend on)."""
+    for k, r in ref.items():
+        g = got[k].cpu()
+        assert torch.equal(g.isnan(), r.isnan()), (k, int(g.isnan().sum()), int(r.isnan().sum()))
+        zero = torch.zeros((), dtype=torch.float64)
+        Bd.check(torch.where(g.isnan(), zero.to(g.dtype), g), torch.where(r.isnan(), zero, r), err[k], k)
+
+
+@pytest.mark.parametrize("dtype", [F, BF])
+@pytest.mark.parametrize("shape", [(1, 20, 64), (2, 60, 33), (1, 128, 66), (2, 700, 64), (1, 1500, 33)])
+@pytest.mark.parametrize("which", ["gate_a", "gate_x", "bias_a", "bias_x"])
+def test_nan_in_a_gate_is_nan_in_the_gradients(which, shape, dtype):
+    B, L, D = shape
+    t, dy, dh = make(B, L, D, dtype, seed=L)
+    err = Bd.gated_bwd(Bd.gated(**t)[2], dy, dh)
+    if which.startswith("gate"):
+        t[which][0, L // 3, 5] = NAN
+        t[which][B - 1, L - 2, D - 1] = NAN
+    else:
+        t[which][3] = NAN
+    ref = O.gated_scan_bwd(t["x"], t["gate_a"], t["gate_x"], t["A"], dy, t["bias_a"], t["bias_x"],
+                           t["h0"], dh)
+    assert any(v.isnan().any() for v in ref.values())
+    d = dev(t)
+    _, _, ck = ssm.gated_scan_fwd_ckpt(**d)
+    for c in (ck, None):
+        compare_nan(ssm.gated_scan_bwd(**d, dy=dy.cuda(), dh_last=dh.cuda(), ckpt=c), ref, err)

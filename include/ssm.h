@@ -497,7 +497,8 @@ int ssm_causal_conv1d_silu_bwd(const void* x, const float* weight, const float* 
  * formed without cancellation for slow channels).
  *
  *   x, gate_a, gate_x, y : [B, L, D] dtype
- *   A              : [D] fp32, not positive (a positive A makes NaN)
+ *   A              : [D] fp32, from -2e38 (A log2 e is held in fp32) to 0 (a
+ *                    positive A makes NaN, in the outputs and the gradients)
  *   bias_a, bias_x : [D] fp32 or NULL (zeros)
  *   h0, h_last     : [B, D] fp32 or NULL (zeros; not wanted)
  *   ckpt           : [B, ceil(L / SSM_GATED_TILE), D] fp32 or NULL: for the

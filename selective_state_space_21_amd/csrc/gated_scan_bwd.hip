@@ -322,8 +322,9 @@ __global__ __launch_bounds__(THREADS, 4) void gated_bwd(GatedBwdArgs q) {
                 asm volatile("" : "+v"(y[j][v]), "+v"(e2[j][v]));   // not the values from before the barriers
                 const float e = e2[j][v], i = sigma_of(e);
                 const float w2 = one_minus_sq(y[j][v], a[j][v]);
-                // 1 / w; where w^2 leaves fp32's range, so do its terms
-                const float rw = w2 > 1e-37f ? __builtin_amdgcn_rsqf(w2) : 0.0f;
+                // 1 / w; where w^2 leaves fp32's range, so do its terms (a positive A
+                // makes w^2 negative: NaN)
+                const float rw = fabsf(w2) > 1e-37f ? __builtin_amdgcn_rsqf(w2) : 0.0f;
                 const float w = w2 * rw, ix = i * xv[v], h = w * ix;
                 // la a h_{t-1} - (la / w) a^2 i x
                 ef[j][v] = (y[j][v] * a[j][v]) * kLn2 * fmaf(-(a[j][v] * ix), rw, s[v]);

@@ -45,3 +45,22 @@ def test_nan_in_a_gate_is_nan_in_the_gradients(which, shape, dtype):
     _, _, ck = ssm.gated_scan_fwd_ckpt(**d)
     for c in (ck, None):
         compare_nan(ssm.gated_scan_bwd(**d, dy=dy.cuda(), dh_last=dh.cuda(), ckpt=c), ref, err)
+
+
+@pytest.mark.parametrize("dtype", [F, BF])
+@pytest.mark.parametrize("L", [20, 40, 128, 129, 700])
+def test_a_positive_decay_rate_is_nan_in_the_gradients(L, dtype):
+    """A > 0 has no weight sqrt(1 - a^2): NaN in the outputs, and in every
+    gradient of those channels that the weight enters."""
+    B, D = 2, 66
+    t, dy, dh = make(B, L, D, dtype, seed=L)
+    t["A"][7], t["A"][65] = 0.5, 1e-3
+    d = dev(t)
+    y, _, ck = ssm.gated_scan_fwd_ckpt(**d)
+    for c in (ck, None):
+        g = ssm.gated_scan_bwd(**d, dy=dy.cuda(), dh_last=dh.cuda(), ckpt=c)
+        for k in ("dx", "dgate_a", "dgate_x", "dA", "dbias_a", "dbias_x"):
+            bad = g[k].isnan()
+            assert bad[..., 7].all() and bad[..., 65].all(), k
+            assert int(bad.sum()) == bad.numel() // D * 2, k
+    assert y[..., 7].isnan().all() and y[..., 65].isnan().all()

@@ -30,6 +30,8 @@
 
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "block_internal.h"
 #include "gated_math.h"
 #include "gated_tile.h"
@@ -336,26 +338,35 @@ __global__ __launch_bounds__(THREADS, 4) void gated_bwd(GatedBwdArgs q) {
         const __amdgpu_buffer_rsrc_t ox = tile_rows<T>(q.dx, p, b, t0, p.L, kTile);
         const __amdgpu_buffer_rsrc_t oa = tile_rows<T>(q.dgate_a, p, b, t0, p.L, kTile);
         const __amdgpu_buffer_rsrc_t og = tile_rows<T>(q.dgate_x, p, b, t0, p.L, kTile);
+        auto gradients = [&](auto partial) {
+            const int own = decltype(partial)::value ? (int)(len - t0) - g * R : R;   // tokens that the run has
 #pragma unroll
-        for (int j = R - 1; j >= 0; --j) {
-            float gx[V], ga[V], gg[V], dy[V];
-            RowT::unpack(ry[j], dy);
+            for (int j = R - 1; j >= 0; --j) {
+                float gx[V], ga[V], gg[V], dy[V];
+                RowT::unpack(ry[j], dy);
+                const bool none = decltype(partial)::value && j >= own;
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float gh = dy[v] + G[v];
-                G[v] = a[j][v] * gh;
-                const float E = gh * ef[j][v];
-                gx[v] = gh * wi[j][v];
-                ga[v] = E * cr[j][v];
-                gg[v] = gh * hc[j][v];
-                sum[0][v] += E;
-                sum[1][v] += ga[v];
-                sum[2][v] += gg[v];
+                for (int v = 0; v < V; ++v) {
+                    const float gh = dy[v] + G[v];
+                    G[v] = a[j][v] * gh;
+                    const float E = none ? 0.0f : gh * ef[j][v];
+                    gx[v] = none ? 0.0f : gh * wi[j][v];
+                    ga[v] = none ? 0.0f : E * cr[j][v];
+                    gg[v] = none ? 0.0f : gh * hc[j][v];
+                    sum[0][v] += E;
+                    sum[1][v] += ga[v];
+                    sum[2][v] += gg[v];
+                }
+                RowT::store(ox, off + j * pitch, gx);
+                RowT::store(oa, off + j * pitch, ga);
+                RowT::store(og, off + j * pitch, gg);
             }
-            RowT::store(ox, off + j * pitch, gx);
-            RowT::store(oa, off + j * pitch, ga);
-            RowT::store(og, off + j * pitch, gg);
-        }
+        };
+        // a token that does not exist has no gradient whatever passes it: the
+        // adjoint or the state there may be infinite, and a product with its
+        // zero weights NaN
+        if (ragged) gradients(std::true_type{});
+        else gradients(std::false_type{});
 #pragma unroll
         for (int k = 0; k < 3; ++k)
 #pragma unroll

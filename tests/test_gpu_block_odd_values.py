@@ -64,3 +64,48 @@ def test_a_positive_decay_rate_is_nan_in_the_gradients(L, dtype):
             assert bad[..., 7].all() and bad[..., 65].all(), k
             assert int(bad.sum()) == bad.numel() // D * 2, k
     assert y[..., 7].isnan().all() and y[..., 65].isnan().all()
+
+
+@pytest.mark.parametrize("value", [INF, -INF, NAN])
+@pytest.mark.parametrize("dtype", [F, BF])
+@pytest.mark.parametrize("L,walkers", [(20, None), (50, None), (128, None), (200, None), (1500, "1"), (1500, "3")])
+def test_rows_without_tokens_do_not_reach_the_gradients(L, walkers, dtype, value, monkeypatch):
+    """An unused slot of a batch, whose carried state and whose state's
+    gradient hold anything: zeros in its rows, nothing of it in the sums, and
+    its state's gradient handed through."""
+    if walkers:
+        monkeypatch.setenv("SSM_GATED_WALKERS", walkers)
+    B, D = 4, 66
+    t, dy, dh = make(B, L, D, dtype, seed=L, lens=[0, L, 0, L - 3])
+    clean = ssm.gated_scan_bwd(**dev(t), dy=dy.cuda(), dh_last=dh.cuda())
+    t["h0"][0], dh[0] = value, value
+    t["h0"][2, 5], dh[2, 9] = value, value
+    d = dev(t)
+    _, h, ck = ssm.gated_scan_fwd_ckpt(**d)
+    same = lambda a, b: torch.equal(a.nan_to_num(7.0), b.nan_to_num(7.0))      # noqa: E731
+    assert same(h[[0, 2]], d["h0"][[0, 2]]) and torch.isfinite(h[[1, 3]]).all()
+    for c in (ck, None):
+        g = ssm.gated_scan_bwd(**d, dy=dy.cuda(), dh_last=dh.cuda(), ckpt=c)
+        for k in ("dx", "dgate_a", "dgate_x"):
+            assert not g[k][[0, 2]].any() and not g[k][3, L - 3:].any(), k
+            assert torch.equal(g[k], clean[k]), k
+        for k in ("dA", "dbias_a", "dbias_x"):
+            assert torch.equal(g[k], clean[k]), k
+        assert same(g["dh0"][[0, 2]].cpu(), dh[[0, 2]]) and torch.equal(g["dh0"][[1, 3]], clean["dh0"][[1, 3]])
+
+
+@pytest.mark.parametrize("dtype", [F, BF])
+@pytest.mark.parametrize("L", [32, 64, 100, 300, 1500])
+def test_padding_is_zero_under_an_infinite_adjoint(L, dtype):
+    B, D = 3, 33
+    n = [L - 1, 1, L // 2]
+    t, dy, dh = make(B, L, D, dtype, seed=L, lens=n)
+    dh[0], dh[1, 4], dh[2, 7] = INF, NAN, -INF
+    t["h0"][1, 8] = INF
+    d = dev(t)
+    for c in (ssm.gated_scan_fwd_ckpt(**d)[2], None):
+        g = ssm.gated_scan_bwd(**d, dy=dy.cuda(), dh_last=dh.cuda(), ckpt=c)
+        for k in ("dx", "dgate_a", "dgate_x"):
+            for b in range(B):
+                assert not g[k][b, n[b]:].any(), (k, b)
+            assert not torch.isfinite(g[k][0, n[0] - 1]).any()     # the row's own tokens show it

@@ -37,11 +37,13 @@ constexpr int kFlight = 8;
 constexpr int kBlockTokens = kWaves * kRun;     // a workgroup: 64 * VEC channels of these
 static_assert(kBlockTokens == conv::kBlockTokens && kRun % kFlight == 0, "the planner's blocks");
 
-// du u'(s): the derivative of s sigma(s)
+// du u'(s): the derivative of s sigma(s).  Where e^-s leaves fp32's range sigma
+// is zero, and with it the product, however large s is; the bound on e keeps
+// e sigma = 1 - sigma a number there.
 __device__ __forceinline__ float silu_grad(float du, float s) {
-    const float e = fast_exp2(fminf(-s * kLog2e, 126.0f));
+    const float e = fast_exp2(-s * kLog2e);
     const float sg = fast_rcp(1.0f + e);
-    return du * (sg * fmaf(s, e * sg, 1.0f));   // 1 - sigma = e sigma
+    return du * (sg * fmaf(s, fminf(e, 0x1p126f) * sg, 1.0f));   // 1 - sigma = e sigma
 }
 
 template <typename T, int VEC, int K, bool SILU>

@@ -109,3 +109,29 @@ def test_padding_is_zero_under_an_infinite_adjoint(L, dtype):
             for b in range(B):
                 assert not g[k][b, n[b]:].any(), (k, b)
             assert not torch.isfinite(g[k][0, n[0] - 1]).any()     # the row's own tokens show it
+
+
+@pytest.mark.parametrize("dtype", [F, BF])
+@pytest.mark.parametrize("D", [1, 64])
+def test_conv_gradient_of_huge_arguments(D, dtype):
+    """The derivative of s sigma(s) is 0 far below zero and 1 far above (for
+    s < -200 it is below |s| e^-200, nothing in fp32), however large s is."""
+    low, high = [-200.0, -1e4, -1e20, -1e30, -1e35, -1e37, -1e38], [200.0, 1e20, 1e35, 1e38]
+    x = torch.tensor(low + high).to(dtype)[None, :, None].repeat(2, 30, D).cuda()
+    du = torch.full_like(x, 3.0)
+    g = ssm.causal_conv1d_silu_bwd(x, torch.ones(D, 1, device="cuda"), du, bias=torch.zeros(D, device="cuda"))
+    want = torch.tensor([0.0] * len(low) + [3.0] * len(high))[None, :, None].repeat(2, 30, D)
+    assert torch.equal(g["dx"].float().cpu(), want)
+    assert torch.equal(g["dbias"].cpu(), torch.full((D,), 2 * 30 * len(high) * 3.0))
+    # and through the carried state's kernel: weights of the last inputs
+    w = torch.tensor([1.0, 0.5]).repeat(D, 1).cuda()
+    st = torch.full((1, D, 1), -1e38, device="cuda")
+    g = ssm.causal_conv1d_silu_bwd(torch.zeros(1, 2, D, dtype=dtype, device="cuda"), w,
+                                   torch.full((1, 2, D), 2.0, dtype=dtype, device="cuda"), state=st)
+    assert not g["dstate"].any()
+    # dx[0] = w[1] g[0] + w[0] g[1] with g[0] = 0, g[1] = 2 * sigma(0) = 1
+    assert torch.equal(g["dx"].float().cpu()[0], torch.tensor([[1.0], [0.5]]).repeat(1, D))
+    # what is not a number, or infinite, is not hidden
+    x = torch.tensor([NAN, -INF, INF]).to(dtype)[None, :, None].repeat(1, 1, D).cuda()
+    g = ssm.causal_conv1d_silu_bwd(x, torch.ones(D, 1, device="cuda"), torch.ones_like(x))
+    assert not torch.isfinite(g["dx"]).any()

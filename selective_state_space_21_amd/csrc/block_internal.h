@@ -171,7 +171,7 @@ struct ConvBwdArgs {
 
 namespace conv {
 constexpr int kBlockTokens = 256;       // tokens per workgroup of the backward
-constexpr int64_t kMaxRow = int64_t(1) << 21;   // 35 rows within 32-bit offsets below kNoChannel
+constexpr int64_t kMaxRow = int64_t(1) << 21;   // 40 rows within 32-bit offsets below kNoChannel
 }
 int64_t conv_bwd_blocks(int64_t L);
 size_t conv_bwd_workspace_bytes(int64_t B, int64_t L, int64_t D, int64_t K);

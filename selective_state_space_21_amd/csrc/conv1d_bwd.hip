@@ -13,7 +13,7 @@
 // its last outputs) with the last inputs and the last g in registers, and the
 // loads of kFlight tokens under way at a time.  Rows are addressed through
 // buffer resources that end with the sequence: behind it x and du read as
-// zero, so g is zero there, and stores are dropped.
+// zero, g is zero, and stores are dropped.
 //
 // Measured at B=8 L=2048 D=1536 K=4 bf16 (151 MB): 41.5 us, 3.6 TB/s, and 4.5
 // for the sums' last step; one channel a thread and one token in flight 91.
@@ -23,6 +23,8 @@
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "block_internal.h"
 #include "gated_tile.h"
@@ -34,6 +36,7 @@ namespace {
 constexpr int kWaves = 8;
 constexpr int kRun = 32;                        // tokens per thread
 constexpr int kFlight = 8;
+constexpr int kTail = 4;
 constexpr int kBlockTokens = kWaves * kRun;     // a workgroup: 64 * VEC channels of these
 static_assert(kBlockTokens == conv::kBlockTokens && kRun % kFlight == 0, "the planner's blocks");
 
@@ -71,7 +74,8 @@ __global__ __launch_bounds__(kWaves * 64) void conv1d_bwd_kernel(ConvBwdArgs p) 
         const int64_t row0 = (b * p.L + t0) * p.D;
         const int64_t n = p.L - t0;                             // tokens from here on
         const int mine = n < kRun ? (int)n : kRun;
-        const uint32_t seen = (uint32_t)((n < kRun + K - 1 ? n : kRun + K - 1) * p.D * sizeof(T));
+        const int there = n < kRun + K - 1 ? (int)n : kRun + K - 1;   // of the tokens walked
+        const uint32_t seen = (uint32_t)(there * p.D * sizeof(T));
         const __amdgpu_buffer_rsrc_t rx = make_rsrc(static_cast<const T*>(p.x) + row0, seen);
         const __amdgpu_buffer_rsrc_t ru = make_rsrc(static_cast<const T*>(p.du) + row0, seen);
         const __amdgpu_buffer_rsrc_t ro = make_rsrc(static_cast<T*>(p.dx) + row0, (uint32_t)mine * pitch);
@@ -96,20 +100,25 @@ __global__ __launch_bounds__(kWaves * 64) void conv1d_bwd_kernel(ConvBwdArgs p) 
             }
         }
         // token t0 + u: its own part of the sums (when it is of this run), then
-        // the output of token u - (K-1), whose last term it is
-        auto token = [&](int u, bool own) {
+        // the output of token u - (K-1), whose last term it is.  past: it may
+        // be behind the run or the end.  Behind the end nothing counts: s and
+        // the inputs in the window may be infinite, and g = 0 no help
+        auto token = [&](int u, auto past) {
+            constexpr bool kPast = decltype(past)::value;
+            if (!kPast || u < there) {
 #pragma unroll
-            for (int c = 0; c < VEC; ++c) {
-                if (SILU) {
-                    float s = bias[c];
+                for (int c = 0; c < VEC; ++c) {
+                    if (SILU) {
+                        float s = bias[c];
 #pragma unroll
-                    for (int k = 0; k < K; ++k) s = fmaf(w[c][k], win[k][c], s);
-                    g[K - 1][c] = silu_grad(g[K - 1][c], s);
-                }
-                if (own) {
+                        for (int k = 0; k < K; ++k) s = fmaf(w[c][k], win[k][c], s);
+                        g[K - 1][c] = silu_grad(g[K - 1][c], s);
+                    }
+                    if (!kPast || u < mine) {
 #pragma unroll
-                    for (int k = 0; k < K; ++k) sum[k][c] = fmaf(g[K - 1][c], win[k][c], sum[k][c]);
-                    sum[K][c] += g[K - 1][c];
+                        for (int k = 0; k < K; ++k) sum[k][c] = fmaf(g[K - 1][c], win[k][c], sum[k][c]);
+                        sum[K][c] += g[K - 1][c];
+                    }
                 }
             }
             const int to = u - (K - 1);
@@ -136,31 +145,27 @@ __global__ __launch_bounds__(kWaves * 64) void conv1d_bwd_kernel(ConvBwdArgs p) 
                     g[i][c] = g[i + 1][c];
                 }
         };
-        for (int u0 = 0; u0 < mine; u0 += kFlight) {
-            typename V::Raw xs[kFlight], us[kFlight];
+        // tokens [u0, u0 + N), N loads of each input under way
+        auto batch = [&](int u0, auto count, auto past) {
+            constexpr int N = decltype(count)::value;
+            typename V::Raw xs[N], us[N];
 #pragma unroll
-            for (int j = 0; j < kFlight; ++j) {
+            for (int j = 0; j < N; ++j) {
                 xs[j] = V::load(rx, off + (uint32_t)(u0 + j) * pitch);
                 us[j] = V::load(ru, off + (uint32_t)(u0 + j) * pitch);
             }
 #pragma unroll
-            for (int j = 0; j < kFlight; ++j) {
+            for (int j = 0; j < N; ++j) {
                 V::unpack(xs[j], win[K - 1]);
                 V::unpack(us[j], g[K - 1]);
-                token(u0 + j, true);
+                token(u0 + j, past);
             }
-        }
-        // (mine up to kRun: a shorter run ended in the tokens behind the
-        // sequence that its last batch held, or does here)
-        const int done = (mine + kFlight - 1) / kFlight * kFlight;
-        if (done < mine + K - 1) {
-#pragma unroll
-            for (int j = 0; j < K - 1; ++j) {
-                V::unpack(V::load(rx, off + (uint32_t)(done + j) * pitch), win[K - 1]);
-                V::unpack(V::load(ru, off + (uint32_t)(done + j) * pitch), g[K - 1]);
-                token(done + j, false);
-            }
-        }
+        };
+        int u0 = 0;
+        for (; u0 + kFlight <= mine; u0 += kFlight)
+            batch(u0, std::integral_constant<int, kFlight>{}, std::false_type{});
+        for (; u0 < mine + K - 1; u0 += kTail)      // what is left of the run, and the tokens after it
+            batch(u0, std::integral_constant<int, kTail>{}, std::true_type{});
     }
 #pragma unroll
     for (int k = 0; k <= K; ++k)

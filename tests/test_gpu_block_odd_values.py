@@ -135,3 +135,42 @@ def test_conv_gradient_of_huge_arguments(D, dtype):
     x = torch.tensor([NAN, -INF, INF]).to(dtype)[None, :, None].repeat(1, 1, D).cuda()
     g = ssm.causal_conv1d_silu_bwd(x, torch.ones(D, 1, device="cuda"), torch.ones_like(x))
     assert not torch.isfinite(g["dx"]).any()
+
+
+@pytest.mark.parametrize("dtype", [F, BF])
+@pytest.mark.parametrize("L", [1, 7, 8, 31, 32, 33, 300])
+def test_conv_tokens_behind_the_end_do_not_count(L, dtype):
+    """The last input times the first weight is an argument of a token that
+    does not exist: beyond fp32 it must not reach the tokens that do."""
+    for D in (64, 33):
+        for K in (2, 3, 4):
+            x = torch.zeros(1, L, D, dtype=dtype, device="cuda")
+            x[:, -1] = 1e30
+            w = torch.ones(D, K, device="cuda")
+            w[:, 0] = 1e20
+            g = ssm.causal_conv1d_silu_bwd(x, w, torch.full_like(x, 2.0), bias=torch.zeros(D, device="cuda"))
+            # silu' is 1 at the last token and 1/2 at the others; what follows it counts nothing
+            gs = torch.ones(L + K, dtype=torch.float64)
+            gs[L - 1], gs[L:] = 2.0, 0.0
+            want = sum(w[0, k].double().item() * gs[K - 1 - k:K - 1 - k + L] for k in range(K))
+            half = torch.finfo(dtype).eps / 2
+            off = (g["dx"].double().cpu() - want[None, :, None]).abs()
+            assert (off <= (half + K * 2.0 ** -24) * want.abs()[None, :, None]).all(), (D, K)
+            assert torch.equal(g["dbias"].cpu(), torch.full((D,), L + 1.0))
+
+
+@pytest.mark.parametrize("L", [1, 3, 8, 9, 31, 32, 40, 257])
+def test_conv_sums_do_not_take_inputs_of_tokens_behind_the_end(L):
+    """Without SiLU an infinite last input meets only the last weight of the
+    last token."""
+    for D in (64, 33):
+        for K in (2, 4):
+            x, du = torch.ones(2, L, D, device="cuda"), torch.full((2, L, D), 2.0, device="cuda")
+            x[:, -1] = 0.0
+            w = torch.ones(D, K, device="cuda")
+            want = ssm.causal_conv1d_silu_bwd(x, w, du, bias=w[:, 0].contiguous(), silu=False)
+            x[0, -1], x[1, -1] = INF, NAN
+            got = ssm.causal_conv1d_silu_bwd(x, w, du, bias=w[:, 0].contiguous(), silu=False)
+            assert torch.equal(got["dweight"][:, :-1], want["dweight"][:, :-1]), (D, K)
+            assert not torch.isfinite(got["dweight"][:, -1]).any()
+            assert torch.equal(got["dx"], want["dx"]) and torch.equal(got["dbias"], want["dbias"])

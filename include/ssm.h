@@ -563,7 +563,8 @@ int ssm_gated_scan_bwd(const void* x, const void* gate_a, const void* gate_x, co
  * One token of the gated recurrence per sequence against a resident state
  * (decode): state [B, D] fp32 is read and overwritten in place; x, gate_a,
  * gate_x, y [B, D] dtype; the rest as ssm_gated_scan_fwd.  Equals the scan
- * over one token bit for bit.
+ * over one token bit for bit.  B * D below 2^39, D below 2^32 - 255 (twice
+ * that where even).
  */
 int ssm_gated_state_update(float* state, const void* x, const void* gate_a, const void* gate_x,
                            const float* A, const float* bias_a, const float* bias_x, void* y,

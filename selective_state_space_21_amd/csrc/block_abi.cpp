@@ -168,6 +168,7 @@ int ssm_gated_state_update(float* state, const void* x, const void* gate_a, cons
     if (!is_dtype(dtype)) return SSM_ERR_BAD_DTYPE;
     if (B < 1 || D < 1 || mul(B, D) < 0) return SSM_ERR_BAD_SHAPE;
     if ((B * D + 255) / 256 > kMaxGrid) return SSM_ERR_UNSUPPORTED;
+    if ((D % 2 == 0 ? D / 2 : D) > ssm::kMaxItems - 255) return SSM_ERR_UNSUPPORTED;   // a row, in one launch
     if (!state || !x || !gate_a || !gate_x || !A || !y) return SSM_ERR_NULL_ARG;
     if (!all_aligned({state, x, gate_a, gate_x, y}, 16)) return SSM_ERR_MISALIGNED;
     if (!all_aligned({A, bias_a, bias_x}, 4)) return SSM_ERR_MISALIGNED;

@@ -11,6 +11,25 @@
 
 namespace ssm {
 
+// A launch has at most 2^32 - 1 work-items along an axis (one of more runs
+// with its size modulo 2^32, and reports nothing).
+constexpr int64_t kMaxItems = 0xffffffff;
+
+// launch(first, count) over `total` rows in slices of at most `most`.
+template <typename Launch>
+hipError_t in_slices(int64_t total, int64_t most, Launch&& launch) {
+    for (int64_t first = 0; first < total; first += most) {
+        const hipError_t e = launch(first, total - first < most ? total - first : most);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+// p + n elements; NULL stays NULL
+template <typename T> T* ahead(T* p, int64_t n) { return p ? p + n : p; }
+inline const void* ahead(const void* p, int64_t n, int bytes) { return ahead(static_cast<const char*>(p), n * bytes); }
+inline void* ahead(void* p, int64_t n, int bytes) { return ahead(static_cast<char*>(p), n * bytes); }
+
 // ---------------------------------------------------------------- gated scan
 
 // Tiling the planner shares with the kernels.
@@ -21,6 +40,9 @@ static_assert(kFwdTile % SSM_GATED_TILE == 0, "a forward tile holds whole saved 
 constexpr int kStrip = 64;              // channels per strip: one workgroup's width
 constexpr int kFwdThreads = 1024;
 constexpr int kBwdThreads = 1024;
+// threads of a workgroup: a sequence of one short tile takes no more than its
+// tokens need
+constexpr int threads(int64_t L, int tile) { return L <= tile / 4 ? 256 : (L <= tile / 2 ? 512 : 1024); }
 // Longest row: a tile's rows are addressed by 32-bit offsets below kNoChannel.
 constexpr int64_t kMaxRow = int64_t(1) << 20;
 static_assert(kFwdTile * kMaxRow * 4 < int64_t(1) << 31, "a tile's rows end below kNoChannel");

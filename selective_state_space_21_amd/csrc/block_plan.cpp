@@ -37,6 +37,8 @@ GatedPlan plan_gated(int64_t B, int64_t L, int64_t D, int tile, int handover) {
     }
     const char* env = getenv("SSM_GATED_WALKERS");
     if (env && atoi(env) > 0) pl.walkers = atoi(env) < gated::kMaxWalkers ? atoi(env) : gated::kMaxWalkers;
+    const int64_t most = kMaxItems / (gated::kFwdThreads * pl.strips);      // what a launch holds
+    if (pl.walkers > most) pl.walkers = most > 1 ? (int)most : 1;
     if (pl.walkers > pl.tiles) pl.walkers = pl.tiles > 1 ? (int)pl.tiles : 1;
     if (pl.walkers > 1)
         pl.chain_bytes = (size_t)(gated::chain_head(pl.strips) + pl.strips * gated::chain_slots(pl.tiles) * 12);

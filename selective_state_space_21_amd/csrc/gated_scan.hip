@@ -260,30 +260,53 @@ __global__ __launch_bounds__(256) void gated_step(GatedStepArgs p) {
 
 template <typename T>
 hipError_t launch_step(const GatedStepArgs& a, hipStream_t stream) {
-    const int64_t n = a.B * (a.D % 2 == 0 ? a.D / 2 : a.D);
-    const unsigned grid = (unsigned)((n + 255) / 256);
-    if (a.D % 2 == 0) gated_step<T, 2><<<grid, 256, 0, stream>>>(a);
-    else gated_step<T, 1><<<grid, 256, 0, stream>>>(a);
-    return hipGetLastError();
+    const int64_t vecs = a.D % 2 == 0 ? a.D / 2 : a.D;
+    return in_slices(a.B, (kMaxItems - 255) / vecs, [&](int64_t b, int64_t n) {
+        GatedStepArgs s = a;
+        s.state = ahead(a.state, b * a.D);
+        s.x = ahead(a.x, b * a.D, sizeof(T));
+        s.gate_a = ahead(a.gate_a, b * a.D, sizeof(T));
+        s.gate_x = ahead(a.gate_x, b * a.D, sizeof(T));
+        s.y = ahead(a.y, b * a.D, sizeof(T));
+        s.B = n;
+        const unsigned grid = (unsigned)((n * vecs + 255) / 256);
+        if (a.D % 2 == 0) gated_step<T, 2><<<grid, 256, 0, stream>>>(s);
+        else gated_step<T, 1><<<grid, 256, 0, stream>>>(s);
+        return hipGetLastError();
+    });
 }
 
 template <typename T, int V>
 hipError_t launch_fwd_v(const GatedArgs& a, hipStream_t stream) {
-    const unsigned grid = (unsigned)(a.plan.strips * a.plan.walkers);
     if (a.plan.walkers > 1) {
+        const unsigned grid = (unsigned)(a.plan.strips * a.plan.walkers);
         if (!a.cleared) {
             const hipError_t e = launch_chain_clear(a.chain, a.plan.chain_bytes, stream);
             if (e != hipSuccess) return e;
         }
         gated_fwd<T, V, true, 1024><<<grid, 1024, 0, stream>>>(a);
-    } else if (a.L <= gated::kFwdTile / 4) {
-        gated_fwd<T, V, false, 256><<<grid, 256, 0, stream>>>(a);
-    } else if (a.L <= gated::kFwdTile / 2) {
-        gated_fwd<T, V, false, 512><<<grid, 512, 0, stream>>>(a);
-    } else {
-        gated_fwd<T, V, false, 1024><<<grid, 1024, 0, stream>>>(a);
+        return hipGetLastError();
     }
-    return hipGetLastError();
+    // a workgroup to a strip: whole batch rows, as many as a launch holds
+    const int threads = gated::threads(a.L, gated::kFwdTile);
+    return in_slices(a.B, kMaxItems / (threads * a.plan.dblocks), [&](int64_t b, int64_t n) {
+        GatedArgs s = a;
+        s.x = ahead(a.x, b * a.L * a.D, sizeof(T));
+        s.gate_a = ahead(a.gate_a, b * a.L * a.D, sizeof(T));
+        s.gate_x = ahead(a.gate_x, b * a.L * a.D, sizeof(T));
+        s.y = ahead(a.y, b * a.L * a.D, sizeof(T));
+        s.h0 = ahead(a.h0, b * a.D);
+        s.h_last = ahead(a.h_last, b * a.D);
+        s.ckpt = ahead(a.ckpt, b * a.saved * a.D);
+        s.seq_lens = ahead(a.seq_lens, b);
+        s.B = n;
+        s.plan.strips = n * a.plan.dblocks;
+        const unsigned strips = (unsigned)s.plan.strips;
+        if (threads == 256) gated_fwd<T, V, false, 256><<<strips, 256, 0, stream>>>(s);
+        else if (threads == 512) gated_fwd<T, V, false, 512><<<strips, 512, 0, stream>>>(s);
+        else gated_fwd<T, V, false, 1024><<<strips, 1024, 0, stream>>>(s);
+        return hipGetLastError();
+    });
 }
 
 template <typename T>

@@ -384,12 +384,35 @@ __global__ __launch_bounds__(THREADS, 4) void gated_bwd(GatedBwdArgs q) {
 
 template <typename T, int V>
 hipError_t launch_bwd_v(const GatedBwdArgs& a, hipStream_t stream) {
-    const unsigned grid = (unsigned)(a.plan.strips * a.plan.walkers);
-    if (a.plan.walkers > 1) gated_bwd<T, V, true, 1024><<<grid, 1024, 0, stream>>>(a);
-    else if (a.f.L <= gated::kBwdTile / 4) gated_bwd<T, V, false, 256><<<grid, 256, 0, stream>>>(a);
-    else if (a.f.L <= gated::kBwdTile / 2) gated_bwd<T, V, false, 512><<<grid, 512, 0, stream>>>(a);
-    else gated_bwd<T, V, false, 1024><<<grid, 1024, 0, stream>>>(a);
-    return hipGetLastError();
+    if (a.plan.walkers > 1) {
+        gated_bwd<T, V, true, 1024><<<(unsigned)(a.plan.strips * a.plan.walkers), 1024, 0, stream>>>(a);
+        return hipGetLastError();
+    }
+    // a workgroup to a strip: whole batch rows, as many as a launch holds
+    const GatedArgs& f = a.f;
+    const int threads = gated::threads(f.L, gated::kBwdTile);
+    return in_slices(f.B, kMaxItems / (threads * a.plan.dblocks), [&](int64_t b, int64_t n) {
+        GatedBwdArgs s = a;
+        s.f.x = ahead(f.x, b * f.L * f.D, sizeof(T));
+        s.f.gate_a = ahead(f.gate_a, b * f.L * f.D, sizeof(T));
+        s.f.gate_x = ahead(f.gate_x, b * f.L * f.D, sizeof(T));
+        s.f.ckpt = ahead(f.ckpt, b * f.saved * f.D);
+        s.f.seq_lens = ahead(f.seq_lens, b);
+        s.f.B = n;
+        s.dy = ahead(a.dy, b * f.L * f.D, sizeof(T));
+        s.dx = ahead(a.dx, b * f.L * f.D, sizeof(T));
+        s.dgate_a = ahead(a.dgate_a, b * f.L * f.D, sizeof(T));
+        s.dgate_x = ahead(a.dgate_x, b * f.L * f.D, sizeof(T));
+        s.dh_last = ahead(a.dh_last, b * f.D);
+        s.dh0 = ahead(a.dh0, b * f.D);
+        s.part = ahead(a.part, b * a.plan.tiles * 3 * f.D);
+        s.plan.strips = n * a.plan.dblocks;
+        const unsigned strips = (unsigned)s.plan.strips;
+        if (threads == 256) gated_bwd<T, V, false, 256><<<strips, 256, 0, stream>>>(s);
+        else if (threads == 512) gated_bwd<T, V, false, 512><<<strips, 512, 0, stream>>>(s);
+        else gated_bwd<T, V, false, 1024><<<strips, 1024, 0, stream>>>(s);
+        return hipGetLastError();
+    });
 }
 
 template <typename T>

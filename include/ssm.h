@@ -596,6 +596,7 @@ int ssm_layer_norm_fwd(const void* x, const float* residual, const float* weight
  *   dweight = sum over rows of dy * n, dbias = sum over rows of dy : [D] fp32 or NULL
  * Outputs are written, never accumulated into; rows = 0 gives zero sums.  The
  * workspace (256-byte aligned) holds partial sums, added in a fixed order.
+ * Sizes as the forward's, D below 2^32 - 255.
  */
 size_t ssm_layer_norm_bwd_workspace_bytes(int64_t rows, int64_t D);
 

@@ -50,9 +50,15 @@ int norm_check_sizes(int64_t rows, int64_t D, int dtype) {
     if (!is_dtype(dtype)) return SSM_ERR_BAD_DTYPE;
     if (rows < 0 || D < 1) return SSM_ERR_BAD_SHAPE;
     if (mul(rows, D) < 0 || mul(D, 8192) < 0) return SSM_ERR_BAD_SHAPE;
-    if (rows > kMaxGrid) return SSM_ERR_UNSUPPORTED;                // a workgroup per row at most
+    if (rows > kMaxGrid) return SSM_ERR_UNSUPPORTED;
     if ((D + 63) / 64 > kMaxGrid) return SSM_ERR_UNSUPPORTED;
     return SSM_OK;
+}
+
+int norm_bwd_check_sizes(int64_t rows, int64_t D, int dtype) {
+    const int rc = norm_check_sizes(rows, D, dtype);
+    if (rc != SSM_OK) return rc;
+    return D > ssm::kMaxItems - 255 ? SSM_ERR_UNSUPPORTED : SSM_OK;    // the columns, in one launch
 }
 
 int conv_bwd_check_sizes(int64_t B, int64_t L, int64_t D, int64_t K, int dtype) {
@@ -198,7 +204,7 @@ int ssm_layer_norm_fwd(const void* x, const float* residual, const float* weight
 }
 
 size_t ssm_layer_norm_bwd_workspace_bytes(int64_t rows, int64_t D) {
-    if (norm_check_sizes(rows, D, SSM_F32) != SSM_OK) return 0;
+    if (norm_bwd_check_sizes(rows, D, SSM_F32) != SSM_OK) return 0;
     return ssm::norm_bwd_workspace_bytes(rows, D);
 }
 
@@ -207,7 +213,7 @@ int ssm_layer_norm_bwd(const void* x, int x_dtype, const void* dy, const float* 
                        void* dx, float* dresidual, float* dweight, float* dbias, int64_t rows,
                        int64_t D, int dtype, void* workspace, size_t workspace_bytes,
                        void* stream) {
-    const int rc = norm_check_sizes(rows, D, dtype);
+    const int rc = norm_bwd_check_sizes(rows, D, dtype);
     if (rc != SSM_OK) return rc;
     if (!is_dtype(x_dtype)) return SSM_ERR_BAD_DTYPE;
     if (x_dtype != SSM_F32 && x_dtype != dtype) return SSM_ERR_UNSUPPORTED;

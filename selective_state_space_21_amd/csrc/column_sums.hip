@@ -15,10 +15,10 @@ namespace {
 
 constexpr int kCols = 64, kWaves = 16;
 
-__global__ __launch_bounds__(kCols * kWaves) void column_sums(ColumnSums a) {
+__global__ __launch_bounds__(kCols * kWaves) void column_sums(ColumnSums a, int64_t first) {
     __shared__ float s[kWaves][kCols];
     const int lane = threadIdx.x % kCols, wave = threadIdx.x / kCols;
-    const int64_t c = (int64_t)blockIdx.x * kCols + lane;
+    const int64_t c = first + (int64_t)blockIdx.x * kCols + lane;
     const int j = blockIdx.y;
     float sum = 0.0f;
     if (c < a.D) {
@@ -50,9 +50,10 @@ __global__ __launch_bounds__(kCols * kWaves) void column_sums(ColumnSums a) {
 }  // namespace
 
 hipError_t launch_column_sums(const ColumnSums& a, hipStream_t stream) {
-    const dim3 grid((unsigned)((a.D + kCols - 1) / kCols), (unsigned)a.m);
-    column_sums<<<grid, kCols * kWaves, 0, stream>>>(a);
-    return hipGetLastError();
+    return in_slices((a.D + kCols - 1) / kCols, kMaxItems / (kCols * kWaves), [&](int64_t first, int64_t n) {
+        column_sums<<<dim3((unsigned)n, (unsigned)a.m), kCols * kWaves, 0, stream>>>(a, first * kCols);
+        return hipGetLastError();
+    });
 }
 
 }  // namespace ssm

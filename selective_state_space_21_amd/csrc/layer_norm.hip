@@ -375,13 +375,31 @@ __global__ __launch_bounds__(256) void norm_bwd_columns(NormBwdArgs p) {
     p.part[(group * 2 + 1) * p.D + d] = db;
 }
 
+// the rows, as many at once as a launch holds
+template <typename T, typename Launch>
+hipError_t slices(const NormArgs& a, int64_t most, Launch&& launch) {
+    return in_slices(a.rows, most, [&](int64_t row, int64_t n) {
+        NormArgs s = a;
+        s.x = ahead(a.x, row * a.D, sizeof(T));
+        s.residual = ahead(a.residual, row * a.D);
+        s.y = ahead(a.y, row * a.D, sizeof(T));
+        s.residual_out = ahead(a.residual_out, row * a.D);
+        s.mean = ahead(a.mean, row);
+        s.rstd = ahead(a.rstd, row);
+        s.rows = n;
+        launch(s);
+        return hipGetLastError();
+    });
+}
+
 template <bool WHOLE, typename T, bool RES, int VEC, int NV, int TPR>
 hipError_t launch_fwd(const NormArgs& a, hipStream_t stream) {
     constexpr int threads = TPR > 256 ? TPR : 256;
     constexpr int rows = threads / TPR;
-    norm_fwd<WHOLE, T, RES, VEC, NV, TPR>
-        <<<(unsigned)((a.rows + rows - 1) / rows), threads, 0, stream>>>(a);
-    return hipGetLastError();
+    return slices<T>(a, kMaxItems / threads * rows, [&](const NormArgs& s) {
+        norm_fwd<WHOLE, T, RES, VEC, NV, TPR>
+            <<<(unsigned)((s.rows + rows - 1) / rows), threads, 0, stream>>>(s);
+    });
 }
 
 // the thread layout of a row of `nv` vectors
@@ -399,8 +417,9 @@ hipError_t launch_fwd_v(const NormArgs& a, hipStream_t stream) {
     if (nv <= 1024) return launch_fwd<WHOLE, T, RES, VEC, 4, 256>(a, stream);
     if (nv <= 2048) return launch_fwd<WHOLE, T, RES, VEC, 2, 1024>(a, stream);
     if (nv <= 4096) return launch_fwd<WHOLE, T, RES, VEC, 4, 1024>(a, stream);
-    norm_fwd_long<T, RES><<<(unsigned)a.rows, 1024, 0, stream>>>(a);
-    return hipGetLastError();
+    return slices<T>(a, kMaxItems / 1024, [&](const NormArgs& s) {
+        norm_fwd_long<T, RES><<<(unsigned)s.rows, 1024, 0, stream>>>(s);
+    });
 }
 
 template <typename T, int VEC>
@@ -452,7 +471,20 @@ hipError_t launch_bwd_w(const NormBwdArgs& a, hipStream_t stream) {
         if (nv <= 1024) return launch_bwd<WHOLE, X, T, 8, 2, 512>(a, stream);
         if (nv <= 2048) return launch_bwd<WHOLE, X, T, 8, 2, 1024>(a, stream);
     }
-    norm_bwd_long<X, T><<<(unsigned)a.rows, 1024, 0, stream>>>(a);
+    const hipError_t e = in_slices(a.rows, kMaxItems / 1024, [&](int64_t row, int64_t n) {
+        NormBwdArgs s = a;
+        s.x = ahead(a.x, row * a.D, sizeof(X));
+        s.dy = ahead(a.dy, row * a.D, sizeof(T));
+        s.mean = ahead(a.mean, row);
+        s.rstd = ahead(a.rstd, row);
+        s.dresidual_out = ahead(a.dresidual_out, row * a.D);
+        s.dx = ahead(a.dx, row * a.D, sizeof(T));
+        s.dresidual = ahead(a.dresidual, row * a.D);
+        s.rows = n;
+        norm_bwd_long<X, T><<<(unsigned)n, 1024, 0, stream>>>(s);
+        return hipGetLastError();
+    });
+    if (e != hipSuccess) return e;
     norm_bwd_columns<X, T>
         <<<dim3((unsigned)((a.D + 255) / 256), (unsigned)a.groups), 256, 0, stream>>>(a);
     return hipGetLastError();

@@ -26,3 +26,12 @@ def test_walkers_asked_for_fit_a_launch(lib, monkeypatch):
             w = query(B, 100000, 64)
             assert 1 <= w <= 64 and (w == 1 or w * B * 1024 < 1 << 32), (B, w)
     assert lib.ssm_gated_scan_walkers(1, 100000, 64) == 64
+
+
+def test_norm_backward_rows_that_no_launch_takes(lib):
+    def g(rows, D):
+        return lib.ssm_layer_norm_bwd(FAKE, 1, FAKE, FAKE, FAKE, None, None, FAKE, None, None, None, rows, D, 1,
+                                      FAKE, 1 << 62, None)
+    assert g(1, 1 << 32) == U and g(5, (1 << 32) - 255) == U
+    assert lib.ssm_layer_norm_bwd_workspace_bytes(1, 1 << 32) == 0
+    assert lib.ssm_layer_norm_bwd_workspace_bytes(1, (1 << 32) - 256) > 0

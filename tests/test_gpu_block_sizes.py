@@ -70,3 +70,29 @@ def test_step_of_more_items_than_one_launch_takes():
             xs = xs.clone()
             y2 = ssm.gated_state_update(s0, xs, xs, xs, A)
             assert torch.equal(ys, y2) and torch.equal(ss, s0)
+
+
+def test_more_norm_rows_than_one_launch_takes():
+    """2^29 rows of two elements, eight threads a row; the rows against the
+    same rows in calls of their own."""
+    rows, D = (1 << 29) + 37, 2
+    x = randn(rows, D, dtype=BF)
+    w, b = randn(D, seed=1), randn(D, seed=2)
+    r = ssm.layer_norm_fwd(x, w, b, out=torch.full_like(x, 7.0))
+    step = 1 << 27
+    for a in range(0, rows, step):
+        e = ssm.layer_norm_fwd(x[a:a + step], w, b)
+        for k in e:
+            assert torch.equal(e[k], r[k][a:a + step]), (k, a)
+
+
+def test_sums_of_more_columns_than_one_launch_takes():
+    """The parameters' gradients of 2^28 columns, 16 threads a column."""
+    D = (1 << 28) + 5
+    x, dy = randn(1, D, dtype=BF), randn(1, D, dtype=BF, seed=1)
+    mean, rstd = torch.full((1,), 0.25, device="cuda"), torch.full((1,), 0.5, device="cuda")
+    w = torch.ones(D, device="cuda")
+    g = ssm.layer_norm_bwd(x, dy, mean, rstd, weight=w, bias=w)
+    assert torch.equal(g["dbias"], dy[0].float())
+    n = (x[0].float() - 0.25) * 0.5
+    assert torch.equal(g["dweight"], dy[0].float() * n)

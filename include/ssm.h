@@ -472,6 +472,7 @@ int ssm_causal_conv1d_silu(const void* x, const float* weight, const float* bias
  *   bias, dbias : [D] fp32 or NULL (dbias NULL: not computed)
  *   state_in, dstate_out, dstate_in : [B, D, K-1] fp32 or NULL
  *   1 <= K <= 4; D <= 2^21; L >= 0 (L = 0: dweight, dbias zero, dstate_in = dstate_out).
+ *   ceil(L / 256) * ceil(D / 64) below 2^23, and that times B below 2^31.
  * Outputs are written, never accumulated into, and must not overlap inputs.
  * The workspace (256-byte aligned) holds partial sums, added in a fixed
  * order: results are deterministic.

@@ -72,6 +72,8 @@ int conv_bwd_check_sizes(int64_t B, int64_t L, int64_t D, int64_t K, int dtype) 
     const int64_t cells = mul(B, ssm::conv_bwd_blocks(L));
     if (mul(cells, mul(D, 20)) < 0) return SSM_ERR_BAD_SHAPE;       // partial sums
     if (mul(cells, (D + 63) / 64) < 0 || cells * ((D + 63) / 64) > kMaxGrid) return SSM_ERR_UNSUPPORTED;
+    // a batch row, 512 threads to 64 channels of a block, in one launch
+    if (ssm::conv_bwd_blocks(L) * ((D + 63) / 64) > ssm::kMaxItems / 512) return SSM_ERR_UNSUPPORTED;
     return SSM_OK;
 }
 

@@ -228,16 +228,35 @@ __global__ __launch_bounds__(256) void conv1d_bwd_state(ConvBwdArgs p) {
 
 template <typename T, int VEC, int K, bool SILU>
 hipError_t launch_s(const ConvBwdArgs& a, hipStream_t stream) {
+    // whole batch rows, as many at once as a launch holds
+    auto slice = [&](int64_t b, int64_t n) {
+        ConvBwdArgs s = a;
+        s.x = ahead(a.x, b * a.L * a.D, sizeof(T));
+        s.du = ahead(a.du, b * a.L * a.D, sizeof(T));
+        s.dx = ahead(a.dx, b * a.L * a.D, sizeof(T));
+        s.state_in = ahead(a.state_in, b * a.D * (K - 1));
+        s.dstate_out = ahead(a.dstate_out, b * a.D * (K - 1));
+        s.dstate_in = ahead(a.dstate_in, b * a.D * (K - 1));
+        s.part = ahead(a.part, b * a.blocks * (K + 1) * a.D);
+        s.B = n;
+        return s;
+    };
     if (a.blocks > 0) {
-        const int64_t dblocks = (a.D + 64 * VEC - 1) / (64 * VEC);
-        conv1d_bwd_kernel<T, VEC, K, SILU>
-            <<<(unsigned)(dblocks * a.B * a.blocks), kWaves * 64, 0, stream>>>(a);
+        const int64_t groups = (a.D + 64 * VEC - 1) / (64 * VEC) * a.blocks;
+        const hipError_t e = in_slices(a.B, kMaxItems / (kWaves * 64 * groups), [&](int64_t b, int64_t n) {
+            conv1d_bwd_kernel<T, VEC, K, SILU><<<(unsigned)(groups * n), kWaves * 64, 0, stream>>>(slice(b, n));
+            return hipGetLastError();
+        });
+        if (e != hipSuccess) return e;
     }
     if constexpr (K > 1) {
         if (a.dstate_in)
-            conv1d_bwd_state<T, K, SILU><<<(unsigned)((a.B * a.D + 255) / 256), 256, 0, stream>>>(a);
+            return in_slices(a.B, (kMaxItems - 255) / a.D, [&](int64_t b, int64_t n) {
+                conv1d_bwd_state<T, K, SILU><<<(unsigned)((n * a.D + 255) / 256), 256, 0, stream>>>(slice(b, n));
+                return hipGetLastError();
+            });
     }
-    return hipGetLastError();
+    return hipSuccess;
 }
 
 template <typename T, int VEC>

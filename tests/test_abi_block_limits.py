@@ -35,3 +35,12 @@ def test_norm_backward_rows_that_no_launch_takes(lib):
     assert g(1, 1 << 32) == U and g(5, (1 << 32) - 255) == U
     assert lib.ssm_layer_norm_bwd_workspace_bytes(1, 1 << 32) == 0
     assert lib.ssm_layer_norm_bwd_workspace_bytes(1, (1 << 32) - 256) > 0
+
+
+def test_conv_backward_rows_that_no_launch_takes(lib):
+    def g(B, L, D):
+        return lib.ssm_causal_conv1d_silu_bwd(FAKE, FAKE, None, None, 1, FAKE, None, FAKE, FAKE, None, None, B, L,
+                                              D, 4, 1, FAKE, 1 << 62, None)
+    assert g(1, 1 << 31, 1) == U and g(2, (1 << 31) - 255, 64) == U and g(1, 1 << 30, 65) == U
+    assert lib.ssm_causal_conv1d_silu_bwd_workspace_bytes(1, 1 << 31, 1, 4) == 0
+    assert lib.ssm_causal_conv1d_silu_bwd_workspace_bytes(1, (1 << 31) - 256, 1, 4) > 0

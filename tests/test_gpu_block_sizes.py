@@ -96,3 +96,35 @@ def test_sums_of_more_columns_than_one_launch_takes():
     assert torch.equal(g["dbias"], dy[0].float())
     n = (x[0].float() - 0.25) * 0.5
     assert torch.equal(g["dweight"], dy[0].float() * n)
+
+
+@pytest.mark.parametrize("state", [False, True])
+def test_more_conv_rows_than_one_launch_takes(state):
+    """2^23 batch rows of a workgroup of 512 threads each."""
+    B, L, D, K = (1 << 23) + 3, 1, 1, 3
+    x, du = randn(B, L, D), randn(B, L, D, seed=1)
+    w = torch.tensor([[0.5, -0.25, 2.0]], device="cuda")
+    b = torch.tensor([0.1], device="cuda")
+    kw = dict(state=randn(B, D, K - 1, seed=2), dstate_out=randn(B, D, K - 1, seed=3)) if state else {}
+    g = ssm.causal_conv1d_silu_bwd(x, w, du, bias=b, **kw)
+    half = B // 2 // 8 * 8
+    for s in (slice(0, half), slice(half, B)):
+        g2 = ssm.causal_conv1d_silu_bwd(x[s], w, du[s], bias=b, **{k: v[s] for k, v in kw.items()})
+        for k in ("dx",) + (("dstate",) if state else ()):
+            assert torch.equal(g[k][s], g2[k]), k
+    # dx holds w[2] g here and the state's gradient; dbias is the sum of g: a
+    # term passes at most B / 16 + 16 additions
+    if not state:
+        terms = (g["dx"] / 2.0).double()
+        off = abs(float(g["dbias"].double() - terms.sum()))
+        assert off <= (B / 16 + 17) * 2.0 ** -24 * float(terms.abs().sum())
+
+
+def test_states_of_more_items_than_one_launch_takes():
+    """The carried state's gradient without tokens: 2^32 channels, copied."""
+    B, D, K = (1 << 25) + 1, 128, 2
+    assert B * D > 1 << 32
+    st = randn(B, D, K - 1)
+    x = torch.empty(B, 0, D, device="cuda")
+    g = ssm.causal_conv1d_silu_bwd(x, torch.ones(D, K, device="cuda"), x, state=st, dstate_out=st)
+    assert torch.equal(g["dstate"], st) and not g["dweight"].any()

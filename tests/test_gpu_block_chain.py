@@ -7,6 +7,9 @@ import torch
 
 import selective_state_space_21_amd as ssm
 from oracle import block as O
+from oracle.backward import s6_bwd
+
+import _block_bounds as Bd
 
 pytestmark = pytest.mark.gpu
 
@@ -120,3 +123,67 @@ def test_conv_scan_backward_reaches_the_blocks_input():
         # quotient's scale |g| |v|
         scale = float(got[name].double().norm() * v.double().norm())
         assert abs(have - want) <= 1e-2 * scale, (name, have, want)
+
+
+def conv_scan_case():
+    g = torch.Generator().manual_seed(2)
+    B, L, D, N, K = 1, 64, 32, 16, 4
+    r = lambda *s: torch.randn(*s, generator=g)                            # noqa: E731
+    return dict(x=r(B, L, D), w=r(D, K) * 0.5, b=r(D) * 0.1, delta=r(B, L, D),
+                A=-torch.rand(D, N, generator=g) - 0.2, Bm=r(B, L, N), Cm=r(B, L, N), dy=r(B, L, D))
+
+
+def conv_scan_gradients(c):
+    f = ssm.selective_scan_conv_fwd(c["x"], c["w"], c["b"], c["delta"], c["A"], c["Bm"], c["Cm"], return_u=True)
+    du = ssm.selective_scan_bwd(f["u"], c["delta"], c["A"], c["Bm"], c["Cm"], c["dy"])["du"]
+    return ssm.causal_conv1d_silu_bwd(c["x"], c["w"], du, bias=c["b"])
+
+
+def test_conv_scan_gradients_are_the_definitions():
+    """selective_scan_bwd's du into causal_conv1d_silu_bwd against the two
+    definitions differentiated one after the other in fp64."""
+    t = conv_scan_case()
+    x, w, b = t["x"], t["w"], t["b"]
+    L, D = x.shape[1:]
+    K = w.shape[1]
+    got = conv_scan_gradients({k: v.cuda() for k, v in t.items()})
+    full = torch.cat([torch.zeros(1, K - 1, D, dtype=F64), x.to(F64)], 1)
+    s = sum(w[:, k].to(F64) * full[:, k:k + L] for k in range(K)) + b.to(F64)
+    du = s6_bwd(s * torch.sigmoid(s), t["delta"], t["A"], t["Bm"], t["Cm"], t["dy"])["du"]
+    ref = O.causal_conv1d_silu_bwd(x, w, du, bias=b)
+    # the conv's own arithmetic, and du's error of 1e-5 of its largest element
+    # (the scan's bar for fp32 gradients) through the conv, whose SiLU has a
+    # derivative below 1.1 in magnitude
+    err = Bd.conv_bwd(x, w, du, bias=b)
+    d = 1.1e-5 * du.abs().max()
+    err["dx"] = err["dx"] + d * w.abs().to(F64).sum(1)
+    err["dweight"] = err["dweight"] + d * torch.stack([full[:, k:k + L].abs().sum((0, 1)) for k in range(K)], 1)
+    err["dbias"] = err["dbias"] + d * L
+    for k, v in ref.items():
+        Bd.check(got[k], v, err[k], k)
+
+
+def test_conv_scan_gradients_against_differences_along_them():
+    """The forward's difference quotient along the gradient g itself is |g|,
+    and across it zero: at a step of 2^-4 along a unit vector the quotient is
+    off by step^2 / 6 of the third derivative, 2.5e-5 |g| at most in fp64, and
+    by 2^-24 |y| |dy| / step of the fp32 outputs, below 2e-4 |g|."""
+    c = {k: v.cuda() for k, v in conv_scan_case().items()}
+    got = conv_scan_gradients(c)
+    step = 2.0 ** -4
+
+    def quotient(name, v):
+        def at(sign):
+            a = dict(c, **{name: c[name] + sign * step * v})
+            y = ssm.selective_scan_conv_fwd(a["x"], a["w"], a["b"], a["delta"], a["A"], a["Bm"], a["Cm"])["y"]
+            return float((y.double() * c["dy"].double()).sum())
+        return (at(1) - at(-1)) / (2 * step)
+
+    for k, name in (("dx", "x"), ("dweight", "w"), ("dbias", "b")):
+        size = float(got[k].double().norm())
+        v = got[k] / size
+        assert abs(quotient(name, v) - size) <= 1e-3 * size, k
+        across = torch.randn(v.shape, generator=torch.Generator().manual_seed(3)).cuda()
+        across -= (across * v).sum() * v
+        across /= across.norm()
+        assert abs(quotient(name, across)) <= 1e-3 * size, k

@@ -231,7 +231,7 @@ int ssm_layer_norm_bwd(const void* x, int x_dtype, const void* dy, const float* 
     a.x = x; a.dy = dy; a.mean = mean; a.rstd = rstd; a.weight = weight;
     a.dresidual_out = dresidual_out; a.dx = dx; a.dresidual = dresidual; a.dweight = dweight;
     a.dbias = dbias; a.rows = rows; a.D = D; a.x_bf16 = x_dtype == SSM_BF16;
-    a.bf16 = dtype == SSM_BF16; a.groups = ssm::norm_bwd_groups(rows, D);
+    a.bf16 = dtype == SSM_BF16; a.groups = ssm::norm_bwd_groups(rows);
     a.part = static_cast<float*>(workspace);
     return status(ssm::launch_layer_norm_bwd(a, static_cast<hipStream_t>(stream)));
 }

@@ -166,8 +166,8 @@ struct NormBwdArgs {
 };
 
 // Workgroups of a backward call, each with a share of the rows and a row of
-// partial sums: a pure function of the sizes.
-int64_t norm_bwd_groups(int64_t rows, int64_t D);
+// partial sums: a pure function of their number.
+int64_t norm_bwd_groups(int64_t rows);
 size_t norm_bwd_workspace_bytes(int64_t rows, int64_t D);
 hipError_t launch_layer_norm_bwd(const NormBwdArgs& a, hipStream_t stream);
 

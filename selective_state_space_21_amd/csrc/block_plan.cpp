@@ -82,13 +82,12 @@ void gated_bwd_carve(GatedBwdArgs& a, void* ws) {
     if (a.own_ckpt) a.f.ckpt = reinterpret_cast<float*>(p);
 }
 
-int64_t norm_bwd_groups(int64_t rows, int64_t D) {
-    (void)D;
+int64_t norm_bwd_groups(int64_t rows) {
     return rows < kCUs ? rows : kCUs;       // one workgroup per CU
 }
 
 size_t norm_bwd_workspace_bytes(int64_t rows, int64_t D) {
-    return (size_t)al256(2 * norm_bwd_groups(rows, D) * D * 4);
+    return (size_t)al256(2 * norm_bwd_groups(rows) * D * 4);
 }
 
 int64_t conv_bwd_blocks(int64_t L) { return (L + conv::kBlockTokens - 1) / conv::kBlockTokens; }

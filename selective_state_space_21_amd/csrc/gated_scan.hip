@@ -116,12 +116,15 @@ __global__ __launch_bounds__(THREADS, 4) void gated_fwd(GatedArgs p) {
 #pragma unroll
             for (int v = 0; v < V; ++v) gated_token(xv[v], av[v], gv[v], ch[v], a[j][v], h[j][v]);
         }
-        if (t0 + kTile > len) {                  // no token: the state stays (its x was read as zero)
+        if (t0 + kTile > len) {                  // no token: the state stays
 #pragma unroll
             for (int j = 0; j < R; ++j)
 #pragma unroll
                 for (int v = 0; v < V; ++v)
-                    if (t0 + g * R + j >= len) a[j][v] = 1.0f;
+                    if (t0 + g * R + j >= len) {
+                        a[j][v] = 1.0f;
+                        h[j][v] = 0.0f;
+                    }
         }
 #pragma unroll
         for (int v = 0; v < V; ++v) {

@@ -174,3 +174,21 @@ def test_conv_sums_do_not_take_inputs_of_tokens_behind_the_end(L):
             assert torch.equal(got["dweight"][:, :-1], want["dweight"][:, :-1]), (D, K)
             assert not torch.isfinite(got["dweight"][:, -1]).any()
             assert torch.equal(got["dx"], want["dx"]) and torch.equal(got["dbias"], want["dbias"])
+
+
+@pytest.mark.parametrize("dtype", [F, BF])
+@pytest.mark.parametrize("L,walkers", [(20, None), (100, None), (256, None), (1500, "1"), (1500, "4")])
+def test_rows_without_tokens_keep_their_state_whatever_the_parameters(L, walkers, dtype, monkeypatch):
+    if walkers:
+        monkeypatch.setenv("SSM_GATED_WALKERS", walkers)
+    D = 66
+    t, _, dh = make(3, L, D, dtype, seed=L, lens=[0, L, 0])
+    t["bias_a"][3] = t["bias_x"][4] = NAN
+    t["A"][5] = 0.5
+    d = dev(t)
+    y, h, ck = ssm.gated_scan_fwd_ckpt(**d, out=torch.full((3, L, D), 7.0, dtype=dtype, device="cuda"))
+    assert torch.equal(h[[0, 2]], d["h0"][[0, 2]]) and torch.equal(ck[[0, 2], 0], d["h0"][[0, 2]])
+    assert torch.all(y[[0, 2]] == 7.0)
+    assert y[1, :, 3:6].isnan().all() and h[1, 3:6].isnan().all() and int(h.isnan().sum()) == 3
+    g = ssm.gated_scan_bwd(**d, dy=torch.ones_like(y), dh_last=dh.cuda(), ckpt=ck)
+    assert torch.equal(g["dh0"][[0, 2]].cpu(), dh[[0, 2]]) and not g["dx"][[0, 2]].any()

@@ -518,9 +518,10 @@ int ssm_causal_conv1d_silu_bwd(const void* x, const float* weight, const float* 
  * workspace (256-byte aligned, 0 bytes for one walker; the call clears what it
  * needs of it).  Calls that may run at the same time need a workspace each.
  * ssm_gated_scan_walkers and ssm_gated_scan_bwd_walkers return their number
- * for the two directions (0 for invalid sizes), a pure function of the sizes; the environment variable SSM_GATED_WALKERS (1..64)
- * overrides it, for the queries and the calls.  Results do not depend on the
- * number of walkers, bit for bit.
+ * for the two directions (0 for invalid sizes), a pure function of the sizes;
+ * the environment variable SSM_GATED_WALKERS (1..64) overrides it, for the
+ * queries and the calls, as far as one launch holds them.  Results do not
+ * depend on the number of walkers, bit for bit.
  */
 #define SSM_GATED_TILE 128
 

@@ -15,8 +15,13 @@
 // buffer resources that end with the sequence: behind it x and du read as
 // zero, g is zero, and stores are dropped.
 //
-// Measured at B=8 L=2048 D=1536 K=4 bf16 (151 MB): 41.5 us, 3.6 TB/s, and 4.5
-// for the sums' last step; one channel a thread and one token in flight 91.
+// Measured at B=8 L=2048 D=1536 K=4 bf16 (151 MB): 43.4 us for calls back to
+// back, 3.5 TB/s, with the sums' last step (alone, in a kernel trace, 40.8 and
+// 4.5 us); one channel a thread and one token in flight 91.  What follows a
+// run, up to kTail tokens at a time, is walked apart from its whole batches:
+// a check of every token against the end there costs nothing (44.3 us with
+// and without), in the batches 45.5, and a second copy of the batch for runs
+// that end within it 30 registers (8 x 4096 x 2560 without SiLU 111 -> 117).
 // Sixteen tokens in flight 44.8 us for the call against 43.8, the next eight
 // loaded ahead 44.2, runs of 64 tokens 45.0, four wavefronts to a workgroup
 // 43.9.
@@ -36,7 +41,7 @@ namespace {
 constexpr int kWaves = 8;
 constexpr int kRun = 32;                        // tokens per thread
 constexpr int kFlight = 8;
-constexpr int kTail = 4;
+constexpr int kTail = 4;                        // at least K - 1
 constexpr int kBlockTokens = kWaves * kRun;     // a workgroup: 64 * VEC channels of these
 static_assert(kBlockTokens == conv::kBlockTokens && kRun % kFlight == 0, "the planner's blocks");
 

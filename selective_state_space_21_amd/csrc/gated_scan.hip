@@ -15,12 +15,14 @@
 // from the state that enters its run.  Inputs are read once; the next tile's
 // are under way from the moment this one's are folded.
 //
-// Measured: B=1 L=131072 D=2048 fp32 (4.3 GB) 773 us, 5.6 TB/s, above what a
-// copy of as many bytes reaches (5.0); bf16 531 us, 4.0 TB/s; B=8 L=2048 D=1536
-// bf16 (201 MB) 58.5 us, 3.4 TB/s.  In bf16 the arithmetic weighs as much as the
-// bytes: 35 vector instructions an element, six of them transcendental; without
-// it the last case takes 52.9 us (47.0 with one workgroup to a strip).  Tried at
-// the bf16 shapes above (long, short) and not kept: 512 threads and tiles of
+// Measured: B=1 L=131072 D=2048 fp32 (4.3 GB) 771 us, 5.6 TB/s, above what a
+// copy of as many bytes reaches (5.0); bf16 528 us, 4.1 TB/s; B=8 L=2048 D=1536
+// bf16 (201 MB) 58.5 us, 3.4 TB/s, 18 above the copy.  Of those 18 the
+// arithmetic (35 vector instructions an element, six of them transcendental)
+// accounts for 6: without it the call takes 52.9 us; the clearing launch and
+// the hand-over for 6 more: 47.0 without these too, with one workgroup to a
+// strip; the last 7 are the phases of one workgroup a CU between its barriers,
+// on 192 CUs.  Tried at the bf16 shapes above (long, short) and not kept: 512 threads and tiles of
 // 128 tokens, two workgroups to a CU, 547 and 58.7 us; strips of 32 channels,
 // whose bf16 rows are half a cache line, 795 and 75.8; the next tile's loads a
 // whole tile ahead 585 and 63.3; cached instead of nontemporal accesses 61.2 at

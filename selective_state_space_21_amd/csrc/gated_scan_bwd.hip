@@ -16,8 +16,8 @@
 // map needs gate_a and dy alone: it is formed and put up first, and the state
 // before it awaited while the others form the rest.
 //
-// Measured, from saved states: B=1 L=32768 D=2048 fp32 (1.9 GB) 372 us, 5.0
-// TB/s, the copy rate; bf16 286 us, 3.3 TB/s; B=8 L=2048 D=1536 bf16 (352 MB)
+// Measured, from saved states: B=1 L=32768 D=2048 fp32 (1.9 GB) 377 us, 5.0
+// TB/s, the copy rate; bf16 285 us, 3.3 TB/s; B=8 L=2048 D=1536 bf16 (352 MB)
 // 117 us, 3.0 TB/s.  In bf16 the vector instructions bound it: 77 an element,
 // eight transcendental, about 60 us of the 117 on the 192 CUs that its 192
 // strips fill.  128 registers (16 wavefronts a CU) are what a tile may hold;

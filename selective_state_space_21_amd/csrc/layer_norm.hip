@@ -9,12 +9,13 @@
 // A row is read once and kept in registers: mean, then the mean square of the
 // differences from it (two passes over registers, so nothing cancels).  TPR
 // threads share a row (8 lanes for the shortest, a wavefront, a whole
-// workgroup for long rows) and each holds NV vectors of VEC elements, vector i of thread j being vector
-// i * TPR + j of the row.  Rows too long for that are read from memory again
-// for every pass.  Both directions are bound by the bytes they move.
+// workgroup for long rows) and each holds NV vectors of VEC elements, vector i
+// of thread j being vector i * TPR + j of the row.  Rows too long for that are
+// read from memory again for every pass.  Both directions are bound by the
+// bytes they move.
 //
-// Measured with the residual stream, 16384 x 768 bf16: forward (151 MB) 32.0
-// us, 4.7 TB/s; backward (201 MB) 40.9 us, 4.9 TB/s, 4 of them the sums' last
+// Measured with the residual stream, 16384 x 768 bf16: forward (151 MB) 31.8
+// us, 4.8 TB/s; backward (201 MB) 40.7 us, 4.9 TB/s, 4 of them the sums' last
 // step.  33M elements without it: D = 64 to 16384 bf16 27 to 34 us forward, 42
 // to 70 backward (at the copy rate 27 and 40), fp32 45 to 58 and 69 to 93 (54
 // and 81).

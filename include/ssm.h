@@ -9,7 +9,10 @@
  *
  * and the calls around them: the S6 decode step and backward, the causal
  * conv1d + SiLU and its backward, the gated linear recurrence (forward,
- * backward, decode step), and layer norm with the residual stream.
+ * backward, decode step), layer norm with the residual stream, linear attention
+ * with a decay for each head (forward, backward, decode step), the norm of
+ * queries and keys with rotary positions, and the moves between a state pool's
+ * slots.
  *
  * Conventions shared by every entry point
  *   - All tensor arguments are DEVICE pointers owned by the caller, row-major
@@ -607,6 +610,138 @@ int ssm_layer_norm_bwd(const void* x, int x_dtype, const void* dy, const float* 
                        void* dx, float* dresidual, float* dweight, float* dbias, int64_t rows,
                        int64_t D, int dtype, void* workspace, size_t workspace_bytes,
                        void* stream);
+
+/*
+ * -------------------------------------------- linear attention
+ * A matrix-valued state for each head, with a decay for each head or for each
+ * token and head; per batch row b and head h, over tokens t:
+ *
+ *   S_t = exp(log_decay) * S_{t-1} + k_t v_t^T       (Dk x Dv, fp32)
+ *   o_t = scale * q_t^T S_t
+ *
+ *   q, k       : [B, L, G, Dk] dtype; head h reads group h / (H / G)
+ *   v          : [B, L, H, Dv] dtype
+ *                Token t of row b starts at element (b * L + t) * q_row (k_row,
+ *                v_row): tensors may be parts of a wider projection's output.
+ *                The strides are at least a token's elements, at most 2^22, and
+ *                multiples of 16 bytes.
+ *   log_decay  : fp32 [B, L, H], or [H] with by_head.  Not positive in use; a
+ *                positive one grows the state as the formula says.  Below -104
+ *                (minus infinity too) it forgets all: exp is zero in fp32.
+ *   o          : [B, L, H, Dv] dtype
+ *   h0, h_last : [B, H, Dk, Dv] fp32 or NULL (zeros; not wanted)
+ *   seq_lens   : device int32 [B] or NULL: row b has its first seq_lens[b]
+ *                tokens (clamped to [0, L]); the padding is not read, o there is
+ *                left untouched, h_last is the state after the row's last token
+ *   Dk, Dv multiples of 16, at most 256; H a multiple of G, at most 2^14;
+ *   B * H at most 2^21; L at most 2^31.
+ *
+ * Tokens are taken in chunks (64 bf16, 32 fp32) as masked products on the
+ * matrix cores, the fp32 state carried between them: an infinity or NaN in a
+ * token's v may make NaN of the same chunk's earlier tokens' outputs too.
+ * For bf16, scores and state are rounded to bf16 as operands; what enters the
+ * state is not (it keeps 2^-18).  With few heads long sequences are cut into
+ * segments whose states are formed first; ssm_linear_attention_segments (and
+ * _bwd_segments) return their number, a pure function of the sizes; the
+ * environment variable SSM_LINEAR_SEGMENTS (1..256) overrides it for queries
+ * and calls.  The workspace is 256-byte aligned (0 bytes for one segment).
+ */
+int ssm_linear_attention_segments(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv, int dtype);
+int ssm_linear_attention_bwd_segments(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv, int dtype);
+size_t ssm_linear_attention_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv, int dtype);
+
+int ssm_linear_attention_fwd(const void* q, const void* k, const void* v, const float* log_decay, int by_head,
+                             float scale, const float* h0, void* o, float* h_last, const int32_t* seq_lens,
+                             int64_t q_row, int64_t k_row, int64_t v_row, int64_t B, int64_t L, int64_t H, int64_t G,
+                             int64_t Dk, int64_t Dv, int dtype, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/*
+ * Gradients of ssm_linear_attention_fwd for L = sum(d_o * o) + sum(dh_last * h_last).
+ * Inputs as the forward's, plus d_o [B, L, H, Dv] dtype (dense) and dh_last
+ * [B, H, Dk, Dv] fp32 or NULL.  Outputs, all dense and written, never
+ * accumulated into:
+ *   dq, dk     : [B, L, G, Dk] dtype, summed over the heads of a group in fp32
+ *   dv         : [B, L, H, Dv] dtype
+ *   dlog_decay : fp32, the shape of log_decay, or NULL (not computed: faster)
+ *   dh0        : [B, H, Dk, Dv] fp32 or NULL
+ * Behind a row's end the tokens' gradients are zeros.  L = 0: dh0 = dh_last,
+ * dlog_decay of the by_head form zero.  Results are deterministic (no atomics).
+ * B * L * G * Dk below 2^33.
+ */
+size_t ssm_linear_attention_bwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t G, int64_t Dk, int64_t Dv,
+                                                int by_head, int dtype);
+
+int ssm_linear_attention_bwd(const void* q, const void* k, const void* v, const float* log_decay, int by_head,
+                             float scale, const float* h0, const void* d_o, const float* dh_last, void* dq, void* dk,
+                             void* dv, float* dlog_decay, float* dh0, const int32_t* seq_lens, int64_t q_row,
+                             int64_t k_row, int64_t v_row, int64_t B, int64_t L, int64_t H, int64_t G, int64_t Dk,
+                             int64_t Dv, int dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One token of linear attention per sequence against resident states (decode):
+ *   state      : [n_slots, H, Dk, Dv] fp32, read and overwritten in place
+ *   slots      : device int32 [B], row b's state is state[slots[b]]; or NULL:
+ *                state[b] (n_slots >= B).  A row whose slot is outside the pool
+ *                (-1 for a padded row) touches no state, its o is zeros.  Rows
+ *                that name one slot are its tokens in the order of the rows.
+ *   q, k [B, G, Dk], v [B, H, Dv], o [B, H, Dv] dtype, rows of q, k and v
+ *   q_row, k_row, v_row elements apart; log_decay fp32 [B, H], or [H] with by_head
+ * All arithmetic is fp32.
+ */
+int ssm_linear_state_update(float* state, const void* q, const void* k, const void* v, const float* log_decay,
+                            int by_head, float scale, const int32_t* slots, void* o, int64_t q_row, int64_t k_row,
+                            int64_t v_row, int64_t B, int64_t n_slots, int64_t H, int64_t G, int64_t Dk, int64_t Dv,
+                            int dtype, void* stream);
+
+/*
+ * -------------------------------------------- norm of queries and keys, rotated
+ * Per row (token) and head, over the head's width, queries and keys in one pass:
+ *   n = x / sqrt(mean(x^2) + eps) * weight
+ *   the first `rotary` elements of n, as pairs (p, p + rotary / 2), or
+ *   (2p, 2p + 1) if interleaved, turned by the angle positions[row] * inv_freq[p]
+ *   q [rows, q_heads, width], k [rows, k_heads, width] dtype, heads dense, rows
+ *   q_row and k_row elements apart; q_out, k_out dense, 16-byte aligned
+ *   q_weight, k_weight : [width] fp32 or NULL (ones)
+ *   positions          : int32 [rows];  inv_freq : fp32 [rotary / 2], radians a
+ *                        position (both may be NULL with rotary = 0)
+ *   width even, at most 512; rotary even, at most width; up to 2^16 heads (0:
+ *   none of that kind); rows up to 2^24; eps >= 0 and finite.
+ * Angles are reduced in fp64.
+ */
+int ssm_qk_norm_rope_fwd(const void* q, const void* k, const float* q_weight, const float* k_weight,
+                         const int32_t* positions, const float* inv_freq, int interleaved, float eps, void* q_out,
+                         void* k_out, int64_t q_row, int64_t k_row, int64_t rows, int64_t q_heads, int64_t k_heads,
+                         int64_t width, int64_t rotary, int dtype, void* stream);
+
+/*
+ * Its gradients: q, k as the forward's; dq_out, dk_out, the gradients of its
+ * outputs, and dq, dk dense.  dq_weight, dk_weight: [width] fp32 or NULL (not
+ * computed), sums over rows and heads.  Nothing is accumulated into; rows = 0
+ * gives zero sums.  The workspace (256-byte aligned) holds partial sums, added
+ * in a fixed order.
+ */
+size_t ssm_qk_norm_rope_bwd_workspace_bytes(int64_t rows, int64_t width);
+
+int ssm_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const void* dk_out, const float* q_weight,
+                         const float* k_weight, const int32_t* positions, const float* inv_freq, int interleaved,
+                         float eps, void* dq, void* dk, float* dq_weight, float* dk_weight, int64_t q_row,
+                         int64_t k_row, int64_t rows, int64_t q_heads, int64_t k_heads, int64_t width, int64_t rotary,
+                         int dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * -------------------------------------------- slots of a state pool
+ * Copies, forks, reorders, compacts and clears the states of sequences in a
+ * pool [layers, n_slots, slot_bytes] of any kind of state, in place, as one
+ * assignment: for e < n and every layer,
+ *   slot dst[e] <- what slot src[e] held before the call, or zeros if src[e] < 0
+ * src, dst: device int32 [n], n up to 2048.  Slots may be sources and
+ * destinations of the same call in any way (beams that swap parents).  An entry
+ * whose dst is outside the pool, or its src beyond it, does nothing; of entries
+ * with one dst the last counts.
+ */
+int ssm_state_slots_copy(void* pool, const int32_t* src, const int32_t* dst, int64_t layers, int64_t n_slots,
+                         int64_t slot_bytes, int64_t n, void* stream);
 
 #ifdef __cplusplus
 }

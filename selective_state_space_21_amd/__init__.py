@@ -15,8 +15,9 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import _args, _native, recurrent_block
+from . import _args, _native, linear_attention, recurrent_block
 from ._native import SSMError
+from .linear_attention import *  # noqa: F401,F403
 from .recurrent_block import *  # noqa: F401,F403
 
 __all__ = ["selective_scan_fwd", "selective_scan_fwd_noalloc", "selective_scan_conv_fwd",
@@ -25,7 +26,7 @@ __all__ = ["selective_scan_fwd", "selective_scan_fwd_noalloc", "selective_scan_c
            "causal_conv1d_silu", "selective_scan_workspace_bytes",
            "selective_scan_segments", "selective_scan_lanes", "selective_scan_bwd_segments",
            "ssd_chunk_workspace_bytes",
-           "SSMError", *recurrent_block.__all__]
+           "SSMError", *recurrent_block.__all__, *linear_attention.__all__]
 
 _DT = _args.DTYPES
 _F32 = torch.float32

@@ -83,6 +83,17 @@ SIGNATURES = {
     "ssm_layer_norm_fwd": (_i, [_vp] * 4 + [_f] + [_vp] * 4 + [_i64] * 2 + [_i, _vp]),
     "ssm_layer_norm_bwd_workspace_bytes": (_sz, [_i64] * 2),
     "ssm_layer_norm_bwd": (_i, [_vp, _i] + [_vp] * 9 + [_i64] * 2 + [_i, _vp, _sz, _vp]),
+    "ssm_linear_attention_segments": (_i, [_i64] * 5 + [_i]),
+    "ssm_linear_attention_bwd_segments": (_i, [_i64] * 5 + [_i]),
+    "ssm_linear_attention_workspace_bytes": (_sz, [_i64] * 5 + [_i]),
+    "ssm_linear_attention_fwd": (_i, [_vp] * 4 + [_i, _f] + [_vp] * 4 + [_i64] * 9 + [_i, _vp, _sz, _vp]),
+    "ssm_linear_attention_bwd_workspace_bytes": (_sz, [_i64] * 6 + [_i, _i]),
+    "ssm_linear_attention_bwd": (_i, [_vp] * 4 + [_i, _f] + [_vp] * 9 + [_i64] * 9 + [_i, _vp, _sz, _vp]),
+    "ssm_linear_state_update": (_i, [_vp] * 5 + [_i, _f] + [_vp] * 2 + [_i64] * 9 + [_i, _vp]),
+    "ssm_qk_norm_rope_fwd": (_i, [_vp] * 6 + [_i, _f] + [_vp] * 2 + [_i64] * 7 + [_i, _vp]),
+    "ssm_qk_norm_rope_bwd_workspace_bytes": (_sz, [_i64] * 2),
+    "ssm_qk_norm_rope_bwd": (_i, [_vp] * 8 + [_i, _f] + [_vp] * 4 + [_i64] * 7 + [_i, _vp, _sz, _vp]),
+    "ssm_state_slots_copy": (_i, [_vp] * 3 + [_i64] * 4 + [_vp]),
 }
 
 _lock = threading.Lock()

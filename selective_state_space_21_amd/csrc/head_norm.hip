@@ -1,0 +1,329 @@
+// The norm of queries and keys over each head's width with the rotation by
+// position, in one pass, and its gradients.
+//
+//   n = x rsqrt(mean(x^2) + eps) w;  pair p < R / 2 of a head is turned by
+//   position * inv_freq[p]: (a, b) -> (a cos - b sin, b cos + a sin)
+//   backward: d = dy turned back, dw = sum d n^, n^ = x rstd,
+//   dx = rstd (w d - n^ mean(w d n^))
+//
+// Bound by the bytes: each element is read and written once.  A group of lanes
+// has one head of one row; a lane holds whole pairs (elements p and p + R / 2,
+// or 2p and 2p + 1), VEC neighbouring ones to a load, so the rotation needs no
+// exchange and the sum over the width log2(lanes) of them.  A workgroup takes a
+// few rows: their angles are reduced once, in fp64 (a position of 10^6 leaves
+// an fp32 angle 4 bits behind the point), and their sines shared by the heads
+// through LDS.  The backward's workgroups sum their rows' shares of the
+// weights' gradients in registers, and a last launch adds those up in order.
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+
+#include "block_internal.h"
+#include "device_math.h"
+#include "lane_ops.h"
+#include "linear_internal.h"
+
+namespace ssm {
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kThreads = 256;
+constexpr int kAngles = 1024;                                // of a workgroup's rows
+
+// N = 1 or 4 neighbouring elements (4: on a border of four)
+template <typename T, int N> __device__ __forceinline__ void load(const T* p, float (&x)[N]) {
+    if constexpr (N == 1) {
+        x[0] = Elem<T>::load(p, 0);
+    } else if constexpr (sizeof(T) == 4) {
+        const f32x4 v = *reinterpret_cast<const f32x4*>(p);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = v[j];
+    } else {
+        const u32x2 v = *reinterpret_cast<const u32x2*>(p);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            x[2 * j] = __uint_as_float(v[j] << 16);
+            x[2 * j + 1] = __uint_as_float(v[j] & 0xffff0000u);
+        }
+    }
+}
+template <typename T, int N> __device__ __forceinline__ void store(T* p, const float (&x)[N]) {
+    if constexpr (N == 1) {
+        Elem<T>::store(p, 0, x[0]);
+    } else if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<f32x4*>(p) = f32x4{x[0], x[1], x[2], x[3]};
+    } else {
+        u32x2 v;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            v[j] = f32_to_bf16_bits(x[2 * j]) | (uint32_t)f32_to_bf16_bits(x[2 * j + 1]) << 16;
+        *reinterpret_cast<u32x2*>(p) = v;
+    }
+}
+
+// VEC pairs p .. p + VEC - 1 of a head
+template <typename T, int VEC>
+struct Pairs {
+    float a[VEC], b[VEC];
+    __device__ __forceinline__ void read(const T* head, int p, bool halves, int half) {
+        if (halves) {
+            load<T, VEC>(head + p, a);
+            load<T, VEC>(head + p + half, b);
+        } else if constexpr (VEC == 4) {
+            float x[4], y[4];
+            load<T, 4>(head + 2 * p, x);
+            load<T, 4>(head + 2 * p + 4, y);
+            a[0] = x[0]; b[0] = x[1]; a[1] = x[2]; b[1] = x[3];
+            a[2] = y[0]; b[2] = y[1]; a[3] = y[2]; b[3] = y[3];
+        } else {
+            a[0] = Elem<T>::load(head, 2 * p);
+            b[0] = Elem<T>::load(head, 2 * p + 1);
+        }
+    }
+    __device__ __forceinline__ void write(T* head, int p, bool halves, int half) const {
+        if (halves) {
+            store<T, VEC>(head + p, a);
+            store<T, VEC>(head + p + half, b);
+        } else if constexpr (VEC == 4) {
+            const float x[4] = {a[0], b[0], a[1], b[1]}, y[4] = {a[2], b[2], a[3], b[3]};
+            store<T, 4>(head + 2 * p, x);
+            store<T, 4>(head + 2 * p + 4, y);
+        } else {
+            Elem<T>::store(head, 2 * p, a[0]);
+            Elem<T>::store(head, 2 * p + 1, b[0]);
+        }
+    }
+};
+
+__device__ __forceinline__ float group_sum(float x, int lanes) {
+    for (int m = lanes / 2; m >= 1; m /= 2) x += __shfl_xor(x, m);
+    return x;
+}
+
+// Angles of `n` rows from `row0` on: entry r * half + p.
+__device__ __forceinline__ void angles(const HeadNormArgs& a, int64_t row0, int n, int half, float2* at) {
+    for (int e = threadIdx.x; e < n * half; e += kThreads) {
+        const int64_t row = row0 + e / half;
+        const double turns = (double)a.positions[row] * ((double)a.inv_freq[e % half] * 0.15915494309189533577);
+        float s, c;
+        sincospif((float)(2.0 * (turns - rint(turns))), &s, &c);
+        at[e] = float2{c, s};
+    }
+}
+
+// NP: pieces of VEC pairs that a lane holds of a head
+template <typename T, int VEC, int NP>
+__global__ __launch_bounds__(kThreads) void head_norm_fwd(HeadNormArgs a, int lanes, int tokens) {
+    __shared__ float2 angle[kAngles];
+    const int half = a.rotary / 2, pairs = a.width / 2;
+    const int64_t row0 = (int64_t)blockIdx.x * tokens;
+    const int n = a.rows - row0 < tokens ? (int)(a.rows - row0) : tokens;
+    angles(a, row0, n, half, angle);
+    const int groups = kThreads / lanes, grp = threadIdx.x / lanes, lane = threadIdx.x % lanes;
+    const float by = 1.0f / (float)a.width;
+    lds_barrier();
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        const int heads = (int)a.heads[which];
+        const float* w = a.weight[which];
+        Pairs<float, VEC> wt[NP];
+#pragma unroll
+        for (int m = 0; m < NP; ++m) {
+            const int p = (lane + m * lanes) * VEC;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) wt[m].a[j] = wt[m].b[j] = 1.0f;
+            if (w && p < pairs) wt[m].read(w, p, !a.interleaved && p < half, half);
+        }
+        const int items = n * heads;
+#pragma unroll 2
+        for (int item = grp; item < items; item += groups) {
+            const int r = item / heads, h = item % heads;
+            const T* x = static_cast<const T*>(a.x[which]) + (row0 + r) * a.x_row[which] + (int64_t)h * a.width;
+            T* y = static_cast<T*>(a.y[which]) + ((row0 + r) * heads + h) * a.width;
+            Pairs<T, VEC> v[NP];
+            float sum = 0.0f;
+#pragma unroll
+            for (int m = 0; m < NP; ++m) {
+                const int p = (lane + m * lanes) * VEC;
+                if (p < pairs) {
+                    v[m].read(x, p, !a.interleaved && p < half, half);
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) sum = fmaf(v[m].a[j], v[m].a[j], fmaf(v[m].b[j], v[m].b[j], sum));
+                }
+            }
+            const float rstd = 1.0f / sqrtf(fmaf(group_sum(sum, lanes), by, a.eps));
+#pragma unroll
+            for (int m = 0; m < NP; ++m) {
+                const int p = (lane + m * lanes) * VEC;
+                if (p < pairs) {
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) {
+                        const float f = v[m].a[j] * rstd * wt[m].a[j], g = v[m].b[j] * rstd * wt[m].b[j];
+                        float2 cs = float2{1.0f, 0.0f};
+                        if (p < half) cs = angle[r * half + p + j];
+                        v[m].a[j] = f * cs.x - g * cs.y;
+                        v[m].b[j] = g * cs.x + f * cs.y;
+                    }
+                    v[m].write(y, p, !a.interleaved && p < half, half);
+                }
+            }
+        }
+    }
+}
+
+template <typename T, int VEC, int NP>
+__global__ __launch_bounds__(kThreads) void head_norm_bwd(HeadNormArgs a, int lanes, int tokens) {
+    __shared__ float2 angle[kAngles];
+    __shared__ float share[2 * VEC * NP * kThreads];
+    const int half = a.rotary / 2, pairs = a.width / 2;
+    const int groups = kThreads / lanes, grp = threadIdx.x / lanes, lane = threadIdx.x % lanes;
+    const float by = 1.0f / (float)a.width;
+    Pairs<float, VEC> wt[2][NP], sum[2][NP];
+#pragma unroll
+    for (int which = 0; which < 2; ++which)
+#pragma unroll
+        for (int m = 0; m < NP; ++m) {
+            const int p = (lane + m * lanes) * VEC;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                wt[which][m].a[j] = wt[which][m].b[j] = 1.0f;
+                sum[which][m].a[j] = sum[which][m].b[j] = 0.0f;
+            }
+            if (a.weight[which] && p < pairs) wt[which][m].read(a.weight[which], p, !a.interleaved && p < half, half);
+        }
+    for (int64_t row0 = (int64_t)blockIdx.x * tokens; row0 < a.rows; row0 += a.groups * tokens) {
+        const int n = a.rows - row0 < tokens ? (int)(a.rows - row0) : tokens;
+        lds_barrier();                                       // the last rows' angles have been read
+        angles(a, row0, n, half, angle);
+        lds_barrier();
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            const int heads = (int)a.heads[which], items = n * heads;
+            for (int item = grp; item < items; item += groups) {
+                const int r = item / heads, h = item % heads;
+                const T* x = static_cast<const T*>(a.x[which]) + (row0 + r) * a.x_row[which] + (int64_t)h * a.width;
+                const int64_t at = ((row0 + r) * heads + h) * a.width;
+                const T* dy = static_cast<const T*>(a.dy[which]) + at;
+                T* dx = static_cast<T*>(a.dx[which]) + at;
+                Pairs<T, VEC> v[NP], d[NP];
+                float sq = 0.0f, dot = 0.0f;
+#pragma unroll
+                for (int m = 0; m < NP; ++m) {
+                    const int p = (lane + m * lanes) * VEC;
+                    if (p < pairs) {
+                        v[m].read(x, p, !a.interleaved && p < half, half);
+                        d[m].read(dy, p, !a.interleaved && p < half, half);
+#pragma unroll
+                        for (int j = 0; j < VEC; ++j) {
+                            float2 cs = float2{1.0f, 0.0f};
+                            if (p < half) cs = angle[r * half + p + j];
+                            const float f = d[m].a[j] * cs.x + d[m].b[j] * cs.y;
+                            d[m].b[j] = d[m].b[j] * cs.x - d[m].a[j] * cs.y;
+                            d[m].a[j] = f;
+                            sq = fmaf(v[m].a[j], v[m].a[j], fmaf(v[m].b[j], v[m].b[j], sq));
+                            dot = fmaf(d[m].a[j] * wt[which][m].a[j], v[m].a[j],
+                                       fmaf(d[m].b[j] * wt[which][m].b[j], v[m].b[j], dot));
+                        }
+                    }
+                }
+                const float rstd = 1.0f / sqrtf(fmaf(group_sum(sq, lanes), by, a.eps));
+                const float c = group_sum(dot, lanes) * rstd * by;       // mean(w d n^)
+#pragma unroll
+                for (int m = 0; m < NP; ++m) {
+                    const int p = (lane + m * lanes) * VEC;
+                    if (p < pairs) {
+#pragma unroll
+                        for (int j = 0; j < VEC; ++j) {
+                            const float na = v[m].a[j] * rstd, nb = v[m].b[j] * rstd;
+                            sum[which][m].a[j] = fmaf(d[m].a[j], na, sum[which][m].a[j]);
+                            sum[which][m].b[j] = fmaf(d[m].b[j], nb, sum[which][m].b[j]);
+                            v[m].a[j] = rstd * (d[m].a[j] * wt[which][m].a[j] - na * c);
+                            v[m].b[j] = rstd * (d[m].b[j] * wt[which][m].b[j] - nb * c);
+                        }
+                        v[m].write(dx, p, !a.interleaved && p < half, half);
+                    }
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        if (!a.dweight[which]) continue;
+        lds_barrier();
+#pragma unroll
+        for (int m = 0; m < NP; ++m) {
+            const int p = (lane + m * lanes) * VEC;
+            if (p < pairs) sum[which][m].write(share + grp * a.width, p, !a.interleaved && p < half, half);
+        }
+        lds_barrier();
+        for (int c = threadIdx.x; c < a.width; c += kThreads) {
+            float x = share[c];
+            for (int g = 1; g < groups; ++g) x += share[g * a.width + c];
+            a.part[((int64_t)blockIdx.x * 2 + which) * a.width + c] = x;
+        }
+    }
+}
+
+int next_pow2(int n) {
+    int p = 1;
+    while (p < n) p *= 2;
+    return p;
+}
+
+// Rows of a workgroup: enough heads to keep its lanes busy a few times over,
+// fewer while that leaves CUs idle, as many angles as LDS is given.
+int rows_of(const HeadNormArgs& a) {
+    int64_t n = a.rows / 2048;
+    const int half = a.rotary / 2;
+    if (half > 0 && n > kAngles / half) n = kAngles / half;
+    return n < 1 ? 1 : n > 8 ? 8 : (int)n;
+}
+
+template <typename T, int VEC, int NP>
+hipError_t launch(const HeadNormArgs& a, bool backward, int lanes, hipStream_t stream) {
+    const int tokens = rows_of(a);
+    if (backward) {
+        head_norm_bwd<T, VEC, NP><<<dim3((unsigned)a.groups), kThreads, 0, stream>>>(a, lanes, tokens);
+    } else {
+        const int64_t blocks = (a.rows + tokens - 1) / tokens;
+        head_norm_fwd<T, VEC, NP><<<dim3((unsigned)blocks), kThreads, 0, stream>>>(a, lanes, tokens);
+    }
+    return hipGetLastError();
+}
+
+template <typename T> hipError_t launch_type(const HeadNormArgs& a, bool backward, hipStream_t stream) {
+    // four pairs to a load where every piece of four starts on a border of four elements
+    bool four = a.width % 8 == 0 && a.rotary % 8 == 0;
+    const uintptr_t border = 4 * sizeof(T);
+    for (int n = 0; n < 2; ++n) {
+        four = four && a.x_row[n] % 4 == 0 && reinterpret_cast<uintptr_t>(a.x[n]) % border == 0;
+        four = four && reinterpret_cast<uintptr_t>(a.weight[n]) % 16 == 0;
+    }
+    const int pieces = four ? a.width / 8 : a.width / 2;
+    const int lanes = next_pow2(pieces) < 64 ? next_pow2(pieces) : 64;
+    if (four) return launch<T, 4, 1>(a, backward, lanes, stream);
+    if (pieces <= 64) return launch<T, 1, 1>(a, backward, lanes, stream);
+    return launch<T, 1, 4>(a, backward, lanes, stream);
+}
+
+}  // namespace
+
+int64_t head_norm_groups(int64_t rows) { return rows < 1 ? 1 : rows < 1024 ? rows : 1024; }
+
+hipError_t launch_head_norm(const HeadNormArgs& a, hipStream_t stream) {
+    if (a.rows == 0) return hipSuccess;
+    return a.bf16 ? launch_type<uint16_t>(a, false, stream) : launch_type<float>(a, false, stream);
+}
+
+hipError_t launch_head_norm_bwd(const HeadNormArgs& a, hipStream_t stream) {
+    const hipError_t e = a.bf16 ? launch_type<uint16_t>(a, true, stream) : launch_type<float>(a, true, stream);
+    if (e != hipSuccess || (!a.dweight[0] && !a.dweight[1])) return e;
+    ColumnSums c{};
+    c.part = a.part; c.n = a.groups; c.D = a.width; c.m = 2;
+    c.out[0] = a.dweight[0]; c.out[1] = a.dweight[1];
+    return launch_column_sums(c, stream);
+}
+
+}  // namespace ssm

@@ -1,0 +1,276 @@
+// Host planning of linear attention: how sequences are cut, what the
+// workspaces hold, and the order of launches behind the two calls.
+#include <hip/hip_runtime.h>
+
+#include <math.h>
+#include <stdint.h>
+#include <stdlib.h>
+
+#include "block_internal.h"
+#include "linear_internal.h"
+
+namespace ssm {
+namespace {
+
+int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+int64_t tiles_of(int64_t width) { return (width + linear::kColumns - 1) / linear::kColumns; }
+
+// Workgroups that fill the GPU: two on each of its 256 CUs.
+constexpr int64_t kFill = 512;
+// Shortest segment worth a launch of its own for its state.
+constexpr int64_t kMinSegment = 256;
+// Forced segments: what joins them, and their workgroups, go out as one launch.
+constexpr int64_t kMostCut = int64_t(1) << 14;
+
+// `groups` workgroups a segment
+LinearPlan plan(int64_t groups, int64_t L, int chunk) {
+    LinearPlan p{1, up(L > 0 ? L : 1, chunk)};
+    int64_t want = (kFill + groups - 1) / groups;
+    if (const char* e = getenv("SSM_LINEAR_SEGMENTS")) {
+        const long n = strtol(e, nullptr, 10);
+        if (n >= 1 && n <= 256 && groups <= kMostCut) {
+            want = n;
+            if (want > 1) {
+                p.seg_tokens = up((L + want - 1) / want, chunk);
+                if (p.seg_tokens < chunk) p.seg_tokens = chunk;
+                p.segments = L > 0 ? (int)((L + p.seg_tokens - 1) / p.seg_tokens) : 1;
+            }
+            return p;
+        }
+    }
+    if (groups * 2 >= kFill || L < 2 * kMinSegment) return p;
+    if (want > L / kMinSegment) want = L / kMinSegment;
+    p.seg_tokens = up((L + want - 1) / want, chunk);
+    p.segments = (int)((L + p.seg_tokens - 1) / p.seg_tokens);
+    return p;
+}
+
+// Pieces of a workspace, each on a 256-byte border.
+struct Carver {
+    char* base;
+    size_t at = 0;
+    float* take(int64_t floats) {
+        float* p = base ? reinterpret_cast<float*>(base + at) : nullptr;
+        at += (size_t)up(floats * 4, 256);
+        return p;
+    }
+};
+
+struct FwdSpace {
+    float* state = nullptr;
+    float* decay = nullptr;
+    size_t bytes;
+    FwdSpace(char* ws, const LinearPlan& p, int64_t B, int64_t H, int64_t size) {
+        Carver c{ws};
+        if (p.segments > 1) {
+            state = c.take(B * H * p.segments * size);
+            decay = c.take(B * H * p.segments);
+        }
+        bytes = c.at;
+    }
+};
+
+struct BwdSpace {
+    float *S = nullptr, *S_decay = nullptr, *D = nullptr, *D_decay = nullptr;
+    float *S_last, *dot_q, *dot_k, *dq = nullptr, *dk = nullptr, *part = nullptr;
+    int tiles;                   // of dot products: 16 columns each
+    size_t bytes;
+    BwdSpace(char* ws, const LinearPlan& p, int64_t B, int64_t L, int64_t H, int64_t G, int64_t Dk, int64_t Dv,
+             bool by_head) {
+        Carver c{ws};
+        const int64_t size = Dk * Dv;
+        if (p.segments > 1) {
+            S = c.take(B * H * p.segments * size);
+            S_decay = c.take(B * H * p.segments);
+            D = c.take(B * H * p.segments * size);
+            D_decay = c.take(B * H * p.segments);
+        }
+        S_last = c.take(B * H * size);
+        tiles = (int)(tiles_of(Dk) * (linear::kColumns / 16));
+        dot_q = c.take(tiles * B * H * L);
+        dot_k = c.take(tiles * B * H * L);
+        if (H > G) {
+            dq = c.take(B * L * H * Dk);
+            dk = c.take(B * L * H * Dk);
+        }
+        if (by_head) part = c.take(B * p.segments * H);
+        bytes = c.at;
+    }
+};
+
+LinearRun run_of(const LinearArgs& a) {
+    LinearRun r{};
+    r.g = a.g; r.by_head = a.by_head; r.seq_lens = a.seq_lens;
+    r.B = a.B; r.L = a.L; r.H = a.H;
+    r.segments = a.plan.segments; r.seg_tokens = a.plan.seg_tokens;
+    r.bf16 = a.bf16;
+    return r;
+}
+
+// The roles of a tensor: rows of `width`, shared by `per` heads.
+struct Rows {
+    const void* p;
+    int64_t row;
+    int32_t per, width;
+};
+
+LinearJob job_of(const Rows& q, const Rows& k, const Rows& v) {
+    LinearJob j{};
+    j.q = q.p; j.q_row = q.row; j.q_per = q.per;
+    j.k = k.p; j.k_row = k.row; j.k_per = k.per;
+    j.v = v.p; j.v_row = v.row; j.v_per = v.per;
+    j.kd = k.width; j.vd = v.width;
+    return j;
+}
+
+hipError_t join(float* states, const float* decay, const float* first, const LinearArgs& a, bool reversed,
+                hipStream_t stream) {
+    LinearJoin j{states, decay, first, a.B * a.H, a.plan.segments, (int32_t)(a.Dk * a.Dv), reversed ? 1 : 0};
+    return launch_linear_join(j, stream);
+}
+
+int pad(int64_t width) { return width <= 64 ? 64 : width <= 128 ? 128 : 256; }
+
+}  // namespace
+
+LinearPlan plan_linear_fwd(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv, bool bf16) {
+    (void)Dk;
+    return plan(B * H * tiles_of(Dv), L, linear::chunk(bf16));
+}
+
+LinearPlan plan_linear_bwd(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv, bool bf16) {
+    return plan(B * H * (2 * tiles_of(Dk) + tiles_of(Dv)), L, linear::chunk(bf16));
+}
+
+size_t linear_fwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv, bool bf16) {
+    return FwdSpace(nullptr, plan_linear_fwd(B, L, H, Dk, Dv, bf16), B, H, Dk * Dv).bytes;
+}
+
+size_t linear_bwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t G, int64_t Dk, int64_t Dv, bool bf16,
+                                  bool by_head) {
+    return BwdSpace(nullptr, plan_linear_bwd(B, L, H, Dk, Dv, bf16), B, L, H, G, Dk, Dv, by_head).bytes;
+}
+
+hipError_t launch_linear_fwd(const LinearArgs& a, hipStream_t stream) {
+    const FwdSpace ws(static_cast<char*>(a.workspace), a.plan, a.B, a.H, a.Dk * a.Dv);
+    const int32_t per = (int32_t)(a.H / a.G);
+    const Rows q{a.q, a.q_row, per, (int32_t)a.Dk}, k{a.k, a.k_row, per, (int32_t)a.Dk};
+    const Rows v{a.v, a.v_row, 1, (int32_t)a.Dv};
+    LinearRun r = run_of(a);
+    LinearJob j = job_of(q, k, v);
+    j.inner = j.outer = a.scale;
+    j.fresh = 1.0f;
+    j.sk = (int32_t)a.Dv; j.sv = 1;
+    j.in_head = a.Dk * a.Dv;
+    j.out_head = a.Dk * a.Dv;
+    j.state_in = a.h0;
+    r.jobs = 1;
+    hipError_t e;
+    if (a.plan.segments > 1) {
+        r.job[0] = j;
+        r.seg_state[0] = ws.state;
+        r.seg_decay[0] = ws.decay;
+        r.job[0].state_in = nullptr;
+        if ((e = launch_linear_run(r, true, stream)) != hipSuccess) return e;
+        if ((e = join(ws.state, ws.decay, a.h0, a, false, stream)) != hipSuccess) return e;
+        j.state_in = ws.state;
+        j.in_head = a.plan.segments * a.Dk * a.Dv;
+        j.in_seg = a.Dk * a.Dv;
+    }
+    j.out = a.o;
+    j.state_out = a.h_last;
+    r.job[0] = j;
+    return launch_linear_run(r, false, stream);
+}
+
+hipError_t launch_linear_bwd(const LinearBwdArgs& a, hipStream_t stream) {
+    const LinearArgs& f = a.f;
+    const int64_t size = f.Dk * f.Dv;
+    const BwdSpace ws(static_cast<char*>(f.workspace), f.plan, f.B, f.L, f.H, f.G, f.Dk, f.Dv, f.by_head != 0);
+    const int32_t per = (int32_t)(f.H / f.G);
+    const Rows q{f.q, f.q_row, per, (int32_t)f.Dk}, k{f.k, f.k_row, per, (int32_t)f.Dk};
+    const Rows v{f.v, f.v_row, 1, (int32_t)f.Dv}, d{a.d_o, f.H * f.Dv, 1, (int32_t)f.Dv};
+    const bool shared = per > 1, segs = f.plan.segments > 1;
+    const int64_t many = f.plan.segments * size;
+    hipError_t e;
+
+    // the states at the segments' borders: S from the left, D (of scale q do^T) from the right
+    LinearRun r = run_of(f);
+    if (segs) {
+        r.jobs = 2;
+        r.job[0] = job_of(q, k, v);
+        r.job[0].fresh = 1.0f;
+        r.job[1] = job_of(k, q, d);
+        r.job[1].fresh = f.scale;
+        r.job[1].reversed = 1;
+        r.seg_state[0] = ws.S; r.seg_decay[0] = ws.S_decay;
+        r.seg_state[1] = ws.D; r.seg_decay[1] = ws.D_decay;
+        if ((e = launch_linear_run(r, true, stream)) != hipSuccess) return e;
+        if ((e = join(ws.S, ws.S_decay, f.h0, f, false, stream)) != hipSuccess) return e;
+        if ((e = join(ws.D, ws.D_decay, a.dh_last, f, true, stream)) != hipSuccess) return e;
+    }
+
+    LinearJob dq = job_of(d, v, k), dk = job_of(v, d, q), dv = job_of(k, q, d);
+    dq.inner = dq.outer = f.scale; dq.fresh = 1.0f;
+    dk.inner = dv.inner = f.scale; dk.outer = dv.outer = 1.0f; dk.fresh = dv.fresh = f.scale;
+    dk.reversed = dv.reversed = 1;
+    dq.state_in = segs ? ws.S : f.h0;
+    dk.state_in = dv.state_in = segs ? ws.D : a.dh_last;
+    for (LinearJob* j : {&dq, &dk, &dv}) {
+        j->in_head = segs ? many : size;
+        j->in_seg = segs ? size : 0;
+        j->out_head = size;
+        j->zero_tail = f.seq_lens != nullptr;
+    }
+    dq.sk = dk.sk = 1; dq.sv = dk.sv = (int32_t)f.Dv;        // the states transposed
+    dv.sk = (int32_t)f.Dv; dv.sv = 1;
+    dq.out = shared ? ws.dq : a.dq;
+    dk.out = shared ? ws.dk : a.dk;
+    dq.out_f32 = dk.out_f32 = shared;
+    dv.out = a.dv;
+    dv.state_out = a.dh0; dv.decay_out = 1;
+    r = run_of(f);
+    if (a.dg) {
+        r.split = 1;
+        dq.dot_with = f.q; dq.dot_row = f.q_row; dq.dot_per = per; dq.dots = ws.dot_q;
+        dk.dot_with = f.k; dk.dot_row = f.k_row; dk.dot_per = per; dk.dots = ws.dot_k;
+        dq.state_out = ws.S_last;
+    }
+    r.job[0] = dq; r.job[1] = dk; r.job[2] = dv;
+    r.jobs = pad(f.Dk) == pad(f.Dv) ? 3 : 2;
+    if ((e = launch_linear_run(r, false, stream)) != hipSuccess) return e;
+    if (r.jobs == 2) {
+        r.jobs = 1;
+        r.split = 0;                                         // dv is of the inputs' type alone
+        r.job[0] = dv;
+        if ((e = launch_linear_run(r, false, stream)) != hipSuccess) return e;
+    }
+    if (shared) {
+        LinearGroupSum s{ws.dq, a.dq, f.B * f.L, f.H, f.G, (int32_t)f.Dk, f.bf16};
+        if ((e = launch_linear_group_sum(s, stream)) != hipSuccess) return e;
+        s.part = ws.dk; s.out = a.dk;
+        if ((e = launch_linear_group_sum(s, stream)) != hipSuccess) return e;
+    }
+    if (a.dg) {
+        LinearDecayGrad g{};
+        g.dot_q = ws.dot_q; g.dot_k = ws.dot_k;
+        g.q_tiles = g.k_tiles = (int)((f.Dk + 15) / 16);
+        g.S = ws.S; g.S_last = ws.S_last; g.D = ws.D; g.D_last = a.dh_last;
+        g.g = f.g; g.by_head = f.by_head;
+        g.seq_lens = f.seq_lens;
+        g.B = f.B; g.L = f.L; g.H = f.H;
+        g.segments = f.plan.segments; g.size = (int32_t)size; g.seg_tokens = f.plan.seg_tokens;
+        g.dg = f.by_head ? nullptr : a.dg;
+        g.part = f.by_head ? ws.part : nullptr;
+        if ((e = launch_linear_decay_grad(g, stream)) != hipSuccess) return e;
+        if (f.by_head) {
+            ColumnSums c{};
+            c.part = ws.part; c.n = f.B * f.plan.segments; c.D = f.H; c.m = 1;
+            c.out[0] = a.dg;
+            return launch_column_sums(c, stream);
+        }
+    }
+    return hipSuccess;
+}
+
+}  // namespace ssm

@@ -1,0 +1,125 @@
+// One token of linear attention per sequence against resident states:
+// S <- e^g S + k v^T in place, o = scale q^T S.
+//
+// Bound by the state's bytes, read and written once.  A workgroup owns some
+// columns of one head's state; a thread four neighbouring columns of every
+// RG-th row, so a wavefront's loads run along rows.  The first rows are on
+// their way before q, k and the slot table are looked at.  The sums over rows
+// are joined through LDS in a fixed order.
+//
+// Rows of a batch that name the same slot are taken as that sequence's tokens
+// in the order of the rows: the workgroups of the first of them run them all,
+// the others' leave.
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+
+#include "device_math.h"
+#include "lane_ops.h"
+#include "linear_internal.h"
+
+namespace ssm {
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kThreads = 256;
+constexpr int kAhead = 8;                                    // rows in flight per thread
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void linear_step(LinearStepArgs a, int columns, int tiles) {
+    __shared__ float q[linear::kMaxWidth], k[linear::kMaxWidth];
+    __shared__ f32x4 part[kThreads];
+    __shared__ int earlier, next;
+    const int tid = threadIdx.x;
+    const int64_t unit = blockIdx.x / tiles;
+    const int64_t b = unit / a.H;
+    const int h = (int)(unit % a.H);
+    const int col0 = (int)(blockIdx.x % tiles) * columns;
+    const int width = (int)a.Dv - col0 < columns ? (int)a.Dv - col0 : columns;
+    const int quads = width / 4, RG = kThreads / quads;
+    const int rg = tid / quads, c = tid % quads * 4;
+    const bool busy = rg < RG;
+    const int Dk = (int)a.Dk, Dv = (int)a.Dv;
+    const int64_t slot = a.slots ? a.slots[b] : b;
+    if (slot < 0 || slot >= a.n_slots) {
+        if (tid < width) Elem<T>::store(static_cast<T*>(a.o) + (b * a.H + h) * Dv + col0, tid, 0.0f);
+        return;
+    }
+    float* S = a.state + ((slot * a.H + h) * Dk) * Dv + col0 + c;
+    int64_t row = b;
+    while (true) {
+        f32x4 s[kAhead];
+#pragma unroll
+        for (int m = 0; m < kAhead; ++m) {
+            const int r = rg + m * RG;
+            if (busy && r < Dk) s[m] = *reinterpret_cast<const f32x4*>(S + (int64_t)r * Dv);
+        }
+        const int grp = h / (int)(a.H / a.G);
+        if (tid < Dk) {
+            q[tid] = Elem<T>::load(static_cast<const T*>(a.q) + row * a.q_row + (int64_t)grp * Dk, tid) * a.scale;
+            k[tid] = Elem<T>::load(static_cast<const T*>(a.k) + row * a.k_row + (int64_t)grp * Dk, tid);
+        }
+        f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (busy) {
+            const T* p = static_cast<const T*>(a.v) + row * a.v_row + (int64_t)h * Dv + col0 + c;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] = Elem<T>::load(p, r);
+        }
+        const float x = (a.by_head ? a.g[h] : a.g[row * a.H + h]) * kLog2e;
+        const float decay = fast_exp2(x < -150.0f ? -150.0f : x);
+        if (tid == 0) earlier = 0, next = 0x7fffffff;
+        lds_barrier();
+        if (a.slots)
+            for (int64_t n = tid; n < a.B; n += kThreads)
+                if (a.slots[n] == (int)slot) {
+                    if (n < b) earlier = 1;
+                    else if (n > row) atomicMin(&next, (int)n);
+                }
+        lds_barrier();
+        if (earlier) return;
+        f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int r0 = rg; r0 < Dk; r0 += kAhead * RG) {
+#pragma unroll
+            for (int m = 0; m < kAhead; ++m) {
+                const int r = r0 + m * RG;
+                if (busy && r < Dk) {
+                    s[m] = s[m] * decay + k[r] * v;
+                    o += q[r] * s[m];
+                    *reinterpret_cast<f32x4*>(S + (int64_t)r * Dv) = s[m];
+                }
+            }
+#pragma unroll
+            for (int m = 0; m < kAhead; ++m) {
+                const int r = r0 + (kAhead + m) * RG;
+                if (busy && r < Dk) s[m] = *reinterpret_cast<const f32x4*>(S + (int64_t)r * Dv);
+            }
+        }
+        part[tid] = o;
+        lds_barrier();
+        if (tid < quads) {
+            for (int n = 1; n < RG; ++n) o += part[n * quads + tid];
+            T* p = static_cast<T*>(a.o) + (row * a.H + h) * Dv + col0 + c;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) Elem<T>::store(p, r, o[r]);
+        }
+        row = next;
+        if (row == 0x7fffffff) return;
+        lds_barrier();                                       // q, k, part and next are free again
+    }
+}
+
+}  // namespace
+
+hipError_t launch_linear_step(const LinearStepArgs& a, hipStream_t stream) {
+    // columns of a workgroup: all of them, or fewer until the GPU has two workgroups on every CU
+    int columns = (int)a.Dv;
+    while (columns > 16 && a.B * a.H * ((a.Dv + columns - 1) / columns) < 512) columns = (columns / 2 + 15) / 16 * 16;
+    const int tiles = (int)((a.Dv + columns - 1) / columns);
+    const unsigned grid = (unsigned)(a.B * a.H * tiles);
+    if (a.bf16) linear_step<uint16_t><<<grid, kThreads, 0, stream>>>(a, columns, tiles);
+    else linear_step<float><<<grid, kThreads, 0, stream>>>(a, columns, tiles);
+    return hipGetLastError();
+}
+
+}  // namespace ssm

@@ -1,0 +1,330 @@
+"""Linear attention with a decay for each head (forward, gradients, decode
+step), the norm of queries and keys with rotary positions, and the moves of
+states between the slots of a pool.
+
+Python entry points of the C ABI in include/ssm.h, by the rules of the
+package's other wrappers: they check every argument, allocate outputs and
+workspace on the caller's stream, and marshal; the arithmetic runs in the
+library's HIP kernels.  Queries, keys and values may be views into a wider
+projection's output: heads dense within a token, tokens a fixed stride apart.
+"""
+from __future__ import annotations
+
+from typing import Optional, Tuple
+
+import torch
+
+from . import _args, _native
+from .recurrent_block import _on
+
+__all__ = ["linear_attention_fwd", "linear_attention_bwd", "linear_state_update",
+           "linear_attention_segments", "linear_attention_bwd_segments",
+           "linear_attention_workspace_bytes", "linear_attention_bwd_workspace_bytes",
+           "qk_norm_rope_fwd", "qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace_bytes",
+           "state_slots_copy"]
+
+_F32 = torch.float32
+_I32 = torch.int32
+_DT = _args.DTYPES
+_ptr = _args.ptr
+
+
+def _rows(name, t, shape, dtype, device) -> int:
+    """Checks a tensor whose last two axes are dense; returns the elements
+    between its tokens (all axes before those two, in order)."""
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor (got {t.device})")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    heads, width = shape[-2:]
+    if t.is_contiguous():
+        return heads * width
+    stride = t.stride()
+    ok = (width == 1 or stride[-1] == 1) and (heads == 1 or stride[-2] == width)
+    row = span = None
+    for size, step in zip(reversed(shape[:-2]), reversed(stride[:-2])):
+        if size == 1:
+            continue
+        if row is None:
+            row, span = step, step * size
+        else:
+            ok = ok and step == span
+            span *= size
+    if not ok or (row is not None and row < heads * width):
+        raise ValueError(f"{name} must have dense heads and tokens a fixed stride apart (strides {tuple(stride)})")
+    return heads * width if row is None else row
+
+
+def _sizes(q, v, lead, names):
+    dt = _args.act_dtype("q", q)
+    _args.need(v=v)
+    if q.dim() != lead + 2 or v.dim() != lead + 2:
+        raise ValueError(f"q must be [{names}, G, Dk] and v [{names}, H, Dv]")
+    if tuple(q.shape[:lead]) != tuple(v.shape[:lead]):
+        raise ValueError(f"q is for {tuple(q.shape[:lead])} tokens, v for {tuple(v.shape[:lead])}")
+    G, Dk = q.shape[-2:]
+    H, Dv = v.shape[-2:]
+    if G < 1 or H % G:
+        raise ValueError(f"{H} heads do not share {G} groups of keys evenly")
+    return dt, q.device, G, Dk, H, Dv
+
+
+def _decay(log_decay, by_token, H, device):
+    """The decays' shape tells their kind: [H], or one for each token and head."""
+    _args.need(log_decay=log_decay)
+    by_head = log_decay.dim() == 1
+    _args.check_args(device, ("log_decay", log_decay, (H,) if by_head else by_token, _F32))
+    return by_head
+
+
+def _default_scale(scale, Dk) -> float:
+    return Dk ** -0.5 if scale is None else float(scale)
+
+
+def linear_attention_segments(B: int, L: int, H: int, Dk: int, Dv: int, dtype=torch.bfloat16) -> int:
+    """Segments that the forward cuts sequences into at these sizes."""
+    return int(_native.load().ssm_linear_attention_segments(B, L, H, Dk, Dv, _DT[dtype]))
+
+
+def linear_attention_bwd_segments(B: int, L: int, H: int, Dk: int, Dv: int, dtype=torch.bfloat16) -> int:
+    """The same for the backward."""
+    return int(_native.load().ssm_linear_attention_bwd_segments(B, L, H, Dk, Dv, _DT[dtype]))
+
+
+def linear_attention_workspace_bytes(B: int, L: int, H: int, Dk: int, Dv: int, dtype=torch.bfloat16) -> int:
+    return int(_native.load().ssm_linear_attention_workspace_bytes(B, L, H, Dk, Dv, _DT[dtype]))
+
+
+def linear_attention_bwd_workspace_bytes(B: int, L: int, H: int, G: int, Dk: int, Dv: int, by_head: bool = False,
+                                         dtype=torch.bfloat16) -> int:
+    return int(_native.load().ssm_linear_attention_bwd_workspace_bytes(B, L, H, G, Dk, Dv, int(bool(by_head)),
+                                                                       _DT[dtype]))
+
+
+def linear_attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                         scale: Optional[float] = None, h0: Optional[torch.Tensor] = None,
+                         return_last_state: bool = True, out: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None, seq_lens: Optional[torch.Tensor] = None
+                         ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Linear attention with a decay for each head (ssm_linear_attention_fwd):
+    S_t = exp(log_decay) S_{t-1} + k_t v_t^T, o_t = scale q_t^T S_t.
+
+    q, k: [Bt, L, G, Dk]; v: [Bt, L, H, Dv], H a multiple of G; log_decay:
+    fp32, [Bt, L, H] or [H]; scale: 1 / sqrt(Dk) unless given; h0: [Bt, H, Dk,
+    Dv] fp32.  Returns (o [Bt, L, H, Dv], h_last).
+    seq_lens: optional int32 [Bt] -- row b runs its first seq_lens[b] tokens;
+    later positions of o are left untouched.
+    """
+    dt, dev, G, Dk, H, Dv = _sizes(q, v, 2, "B, L")
+    Bt, L = q.shape[:2]
+    _args.need(k=k)
+    rows = [_rows(n, t, s, dt, dev) for n, t, s in
+            (("q", q, (Bt, L, G, Dk)), ("k", k, (Bt, L, G, Dk)), ("v", v, (Bt, L, H, Dv)))]
+    by_head = _decay(log_decay, (Bt, L, H), H, dev)
+    _args.check_args(dev, ("h0", h0, (Bt, H, Dk, Dv), _F32), ("out", out, (Bt, L, H, Dv), dt),
+                     ("seq_lens", seq_lens, (Bt,), _I32))
+    lib = _native.load()
+    need = int(lib.ssm_linear_attention_workspace_bytes(Bt, L, H, Dk, Dv, _DT[dt]))
+    workspace, ws_bytes = _args.workspace(workspace, need, dev)
+    o = out if out is not None else torch.empty((Bt, L, H, Dv), dtype=dt, device=dev)
+    h_last = torch.empty((Bt, H, Dk, Dv), dtype=_F32, device=dev) if return_last_state else None
+    with _on(dev):
+        rc = lib.ssm_linear_attention_fwd(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), int(by_head), _default_scale(scale, Dk), _ptr(h0), _ptr(o),
+            _ptr(h_last), _ptr(seq_lens), *rows, Bt, L, H, G, Dk, Dv, _DT[dt], _ptr(workspace), ws_bytes,
+            _args.stream_handle(dev))
+    _native.check(rc, "ssm_linear_attention_fwd")
+    return o, h_last
+
+
+def linear_attention_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                         do: torch.Tensor, scale: Optional[float] = None, h0: Optional[torch.Tensor] = None,
+                         dh_last: Optional[torch.Tensor] = None, decay_grad: bool = True,
+                         workspace: Optional[torch.Tensor] = None,
+                         seq_lens: Optional[torch.Tensor] = None) -> dict:
+    """Gradients of linear_attention_fwd (ssm_linear_attention_bwd).
+
+    Inputs as linear_attention_fwd plus do [Bt, L, H, Dv] (dtype of q) and
+    dh_last [Bt, H, Dk, Dv] fp32.  Returns a dict with dq, dk, dv (dtype of
+    q), dlog_decay (fp32, the shape of log_decay) unless decay_grad is off
+    (for fixed decays: the call is then faster), and dh0 if h0 was given.
+    With seq_lens the gradients behind a row's end are zeros.
+    """
+    dt, dev, G, Dk, H, Dv = _sizes(q, v, 2, "B, L")
+    Bt, L = q.shape[:2]
+    _args.need(k=k, do=do)
+    rows = [_rows(n, t, s, dt, dev) for n, t, s in
+            (("q", q, (Bt, L, G, Dk)), ("k", k, (Bt, L, G, Dk)), ("v", v, (Bt, L, H, Dv)))]
+    by_head = _decay(log_decay, (Bt, L, H), H, dev)
+    _args.check_args(dev, ("do", do, (Bt, L, H, Dv), dt), ("h0", h0, (Bt, H, Dk, Dv), _F32),
+                     ("dh_last", dh_last, (Bt, H, Dk, Dv), _F32), ("seq_lens", seq_lens, (Bt,), _I32))
+    lib = _native.load()
+    need = int(lib.ssm_linear_attention_bwd_workspace_bytes(Bt, L, H, G, Dk, Dv, int(by_head), _DT[dt]))
+    workspace, ws_bytes = _args.workspace(workspace, need, dev)
+    r = {"dq": torch.empty((Bt, L, G, Dk), dtype=dt, device=dev),
+         "dk": torch.empty((Bt, L, G, Dk), dtype=dt, device=dev),
+         "dv": torch.empty((Bt, L, H, Dv), dtype=dt, device=dev)}
+    if decay_grad:
+        r["dlog_decay"] = torch.empty_like(log_decay)
+    if h0 is not None:
+        r["dh0"] = torch.empty_like(h0)
+    with _on(dev):
+        rc = lib.ssm_linear_attention_bwd(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), int(by_head), _default_scale(scale, Dk), _ptr(h0), _ptr(do),
+            _ptr(dh_last), _ptr(r["dq"]), _ptr(r["dk"]), _ptr(r["dv"]), _ptr(r.get("dlog_decay")),
+            _ptr(r.get("dh0")), _ptr(seq_lens), *rows, Bt, L, H, G, Dk, Dv, _DT[dt], _ptr(workspace), ws_bytes,
+            _args.stream_handle(dev))
+    _native.check(rc, "ssm_linear_attention_bwd")
+    return r
+
+
+def linear_state_update(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                        log_decay: torch.Tensor, scale: Optional[float] = None,
+                        slots: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One decode step of linear attention (ssm_linear_state_update).
+
+    state: [n_slots, H, Dk, Dv] fp32, updated in place; q, k: [Bt, G, Dk]; v:
+    [Bt, H, Dv]; log_decay: fp32, [Bt, H] or [H].  Row b's state is
+    state[slots[b]] (slots: int32 [Bt]; a slot outside the pool, -1 say, marks a
+    padded row: no state is touched and o is zeros; rows of one slot are its
+    tokens in the order of the rows), or state[b] without slots.  Returns o
+    [Bt, H, Dv].
+    """
+    dt, dev, G, Dk, H, Dv = _sizes(q, v, 1, "B")
+    Bt = q.shape[0]
+    _args.need(state=state, k=k)
+    rows = [_rows(n, t, s, dt, dev) for n, t, s in
+            (("q", q, (Bt, G, Dk)), ("k", k, (Bt, G, Dk)), ("v", v, (Bt, H, Dv)))]
+    by_head = _decay(log_decay, (Bt, H), H, dev)
+    if state.dim() != 4 or (slots is None and state.shape[0] < Bt):
+        raise ValueError("state must be [n_slots, H, Dk, Dv], with a slot for each row")
+    n = state.shape[0]
+    _args.check_args(dev, ("state", state, (n, H, Dk, Dv), _F32), ("slots", slots, (Bt,), _I32),
+                     ("out", out, (Bt, H, Dv), dt))
+    o = out if out is not None else torch.empty((Bt, H, Dv), dtype=dt, device=dev)
+    with _on(dev):
+        rc = _native.load().ssm_linear_state_update(
+            _ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), int(by_head), _default_scale(scale, Dk),
+            _ptr(slots), _ptr(o), *rows, Bt, n, H, G, Dk, Dv, _DT[dt], _args.stream_handle(dev))
+    _native.check(rc, "ssm_linear_state_update")
+    return o
+
+
+def _norm_args(q, k, q_weight, k_weight, positions, inv_freq):
+    dt = _args.act_dtype("q", q)
+    _args.need(k=k)
+    if q.dim() < 2 or k.dim() != q.dim():
+        raise ValueError("q must be [..., q_heads, width] and k [..., k_heads, width]")
+    lead, dev, width = tuple(q.shape[:-2]), q.device, q.shape[-1]
+    Hq, Hk = q.shape[-2], k.shape[-2]
+    rows = 1
+    for size in lead:
+        rows *= size
+    strides = [_rows("q", q, lead + (Hq, width), dt, dev), _rows("k", k, lead + (Hk, width), dt, dev)]
+    if inv_freq is not None:
+        _args.need(positions=positions)
+        if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
+            raise ValueError("inv_freq must be [rotary / 2]")
+    half = 0 if inv_freq is None else inv_freq.shape[0]
+    _args.check_args(dev, ("q_weight", q_weight, (width,), _F32), ("k_weight", k_weight, (width,), _F32),
+                     ("positions", positions, lead, _I32), ("inv_freq", inv_freq, (half,), _F32))
+    return dt, dev, lead, rows, strides, Hq, Hk, width, 2 * half
+
+
+def qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tensor] = None,
+                     k_weight: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                     inv_freq: Optional[torch.Tensor] = None, interleaved: bool = False, eps: float = 1e-6,
+                     out_q: Optional[torch.Tensor] = None, out_k: Optional[torch.Tensor] = None
+                     ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """RMS norm of queries and keys over each head's width, then the rotation
+    of its first elements by position (ssm_qk_norm_rope_fwd).
+
+    q: [..., Hq, width], k: [..., Hk, width]; q_weight, k_weight: [width] fp32;
+    positions: int32, the leading shape of q; inv_freq: fp32 [rotary / 2],
+    radians a position (none: no rotation).  Pairs are (p, p + rotary / 2), or
+    (2p, 2p + 1) if interleaved.  Returns dense (q, k).
+    """
+    dt, dev, lead, rows, strides, Hq, Hk, width, rotary = _norm_args(q, k, q_weight, k_weight, positions, inv_freq)
+    _args.check_args(dev, ("out_q", out_q, lead + (Hq, width), dt), ("out_k", out_k, lead + (Hk, width), dt))
+    yq = out_q if out_q is not None else torch.empty(lead + (Hq, width), dtype=dt, device=dev)
+    yk = out_k if out_k is not None else torch.empty(lead + (Hk, width), dtype=dt, device=dev)
+    with _on(dev):
+        rc = _native.load().ssm_qk_norm_rope_fwd(
+            _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(inv_freq),
+            int(bool(interleaved)), float(eps), _ptr(yq), _ptr(yk), *strides, rows, Hq, Hk, width, rotary, _DT[dt],
+            _args.stream_handle(dev))
+    _native.check(rc, "ssm_qk_norm_rope_fwd")
+    return yq, yk
+
+
+def qk_norm_rope_bwd_workspace_bytes(rows: int, width: int) -> int:
+    return int(_native.load().ssm_qk_norm_rope_bwd_workspace_bytes(rows, width))
+
+
+def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, dq_out: torch.Tensor, dk_out: torch.Tensor,
+                     q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                     positions: Optional[torch.Tensor] = None, inv_freq: Optional[torch.Tensor] = None,
+                     interleaved: bool = False, eps: float = 1e-6,
+                     workspace: Optional[torch.Tensor] = None) -> dict:
+    """Gradients of qk_norm_rope_fwd (ssm_qk_norm_rope_bwd).
+
+    Inputs as the forward plus dq_out, dk_out, the gradients of its outputs
+    (dense).  Returns a dict with dense dq, dk, and dq_weight, dk_weight
+    [width] fp32 for the weights that were given.
+    """
+    dt, dev, lead, rows, strides, Hq, Hk, width, rotary = _norm_args(q, k, q_weight, k_weight, positions, inv_freq)
+    _args.need(dq_out=dq_out, dk_out=dk_out)
+    _args.check_args(dev, ("dq_out", dq_out, lead + (Hq, width), dt), ("dk_out", dk_out, lead + (Hk, width), dt))
+    lib = _native.load()
+    workspace, ws_bytes = _args.workspace(
+        workspace, int(lib.ssm_qk_norm_rope_bwd_workspace_bytes(rows, width)), dev)
+    r = {"dq": torch.empty(lead + (Hq, width), dtype=dt, device=dev),
+         "dk": torch.empty(lead + (Hk, width), dtype=dt, device=dev)}
+    if q_weight is not None:
+        r["dq_weight"] = torch.empty_like(q_weight)
+    if k_weight is not None:
+        r["dk_weight"] = torch.empty_like(k_weight)
+    with _on(dev):
+        rc = lib.ssm_qk_norm_rope_bwd(
+            _ptr(q), _ptr(k), _ptr(dq_out), _ptr(dk_out), _ptr(q_weight), _ptr(k_weight), _ptr(positions),
+            _ptr(inv_freq), int(bool(interleaved)), float(eps), _ptr(r["dq"]), _ptr(r["dk"]),
+            _ptr(r.get("dq_weight")), _ptr(r.get("dk_weight")), *strides, rows, Hq, Hk, width, rotary, _DT[dt],
+            _ptr(workspace), ws_bytes, _args.stream_handle(dev))
+    _native.check(rc, "ssm_qk_norm_rope_bwd")
+    return r
+
+
+def state_slots_copy(pool: torch.Tensor, src: torch.Tensor, dst: torch.Tensor, dim: int = 0) -> torch.Tensor:
+    """Copies, forks, reorders, compacts and clears states in a pool, in place
+    (ssm_state_slots_copy): along axis `dim` of the pool, slot dst[e] becomes
+    what slot src[e] was before the call, or zeros where src[e] is negative, as
+    one assignment.
+
+    pool: any dtype, contiguous (a layer axis may stand before the slots with
+    dim = 1); src, dst: int32 [n], n up to 2048.  Entries whose slots are
+    outside the pool do nothing; of entries with one dst the last counts.
+    Returns the pool.
+    """
+    _args.need(pool=pool, src=src, dst=dst)
+    if not -pool.dim() <= dim < pool.dim():
+        raise ValueError(f"pool has no axis {dim}")
+    dim %= pool.dim()
+    if pool.shape[dim] < 1:
+        raise ValueError("pool has no slots")
+    dev = pool.device
+    n = src.shape[0] if src.dim() == 1 else -1
+    _args.check_args(dev, ("pool", pool, pool.shape, pool.dtype), ("src", src, (n,), _I32), ("dst", dst, (n,), _I32))
+    layers, slot = 1, pool.element_size()
+    for size in pool.shape[:dim]:
+        layers *= size
+    for size in pool.shape[dim + 1:]:
+        slot *= size
+    with _on(dev):
+        rc = _native.load().ssm_state_slots_copy(_ptr(pool), _ptr(src), _ptr(dst), layers, pool.shape[dim], slot, n,
+                                                 _args.stream_handle(dev))
+    _native.check(rc, "ssm_state_slots_copy")
+    return pool

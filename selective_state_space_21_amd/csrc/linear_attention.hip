@@ -26,7 +26,7 @@
 // (columns are tokens), so a lane stores four neighbouring elements.  State
 // tile (kk, u) holds key rows 32kk + 8a + 4u + b as its rows 4a + b: lane g
 // then has rows 32kk + 8g + 0..7 of its column in tiles u = 0, 1, which is the
-// A operand of the product with the queries.
+// A operand of the product with the queries as it stands.
 //
 // Rounding: exponent sums are fp64 and kept as two floats, differences are
 // taken of those.  For bf16 the decayed values of the state update are split
@@ -38,6 +38,8 @@
 
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "device_math.h"
 #include "lane_ops.h"
 #include "linear_internal.h"
@@ -46,6 +48,8 @@ namespace ssm {
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef short i16x8 __attribute__((ext_vector_type(8)));
@@ -60,6 +64,11 @@ constexpr uint32_t kNoOffset = 0x80000000u;      // past every resource's end: l
 constexpr uint32_t kRecords = 0x7ffffff0u;
 constexpr float kMinLog2 = -150.0f;              // 2^-150 is zero in fp32
 
+// Two values rounded to bf16 in one register.
+__device__ __forceinline__ uint32_t pair(float a, float b) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+}
+
 // Operands and products of a storage type.
 template <typename T> struct Mat;
 
@@ -70,12 +79,10 @@ template <> struct Mat<uint16_t> {
     }
     // eight neighbouring elements of a row
     static __device__ __forceinline__ Frag along(const uint16_t* p) { return *reinterpret_cast<const Frag*>(p); }
-    // rows row..row+7 of this lane's column: the 16 columns are first + step * a + b for a, b < 4.
-    // A transposing read takes 4 columns of one row from each lane (row r = i / 4, block a = i % 4)
-    // and gives lane i column i of the four rows.
-    static __device__ __forceinline__ Frag down(const uint16_t* tile, int stride, int row, int first, int step, int i) {
-        const uint16_t* p = tile + (row + i / 4) * stride + first + step * (i % 4);
-        const i16x4 x = read4(p), y = read4(p + 4 * stride);
+    // eight rows of a column, four from p on and four from p2 on.  A transposing read takes four columns
+    // of one row from each of 16 lanes (row i / 4, block i % 4) and gives lane i column i of the four rows.
+    static __device__ __forceinline__ Frag down(const uint16_t* p, const uint16_t* p2) {
+        const i16x4 x = read4(p), y = read4(p2);
         i16x8 z;
 #pragma unroll
         for (int j = 0; j < 4; ++j) z[j] = x[j], z[j + 4] = y[j];
@@ -85,8 +92,19 @@ template <> struct Mat<uint16_t> {
         typedef __attribute__((address_space(3))) i16x4 Shared;
         return __builtin_amdgcn_ds_read_tr16_b64_v4i16((Shared*)(uintptr_t)p);
     }
-    static __device__ __forceinline__ f32x8 widen(Frag a) { return __builtin_convertvector(a, f32x8); }
-    static __device__ __forceinline__ Frag high(f32x8 x) { return __builtin_convertvector(x, Frag); }
+    static __device__ __forceinline__ f32x8 widen(Frag a) {
+        const u32x4 u = __builtin_bit_cast(u32x4, a);
+        f32x8 x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            x[2 * j] = __uint_as_float(u[j] << 16);
+            x[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
+        }
+        return x;
+    }
+    static __device__ __forceinline__ Frag high(f32x8 x) {
+        return __builtin_bit_cast(Frag, u32x4{pair(x[0], x[1]), pair(x[2], x[3]), pair(x[4], x[5]), pair(x[6], x[7])});
+    }
 };
 
 template <> struct Mat<float> {
@@ -100,8 +118,7 @@ template <> struct Mat<float> {
         const f32x4 x = *reinterpret_cast<const f32x4*>(p), y = *reinterpret_cast<const f32x4*>(p + 4);
         return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
     }
-    static __device__ __forceinline__ Frag down(const float* tile, int stride, int row, int first, int step, int i) {
-        const float* p = tile + row * stride + first + step * (i / 4) + i % 4;
+    static __device__ __forceinline__ Frag down(const float* p, int stride) {
         Frag z;
 #pragma unroll
         for (int j = 0; j < 8; ++j) z[j] = p[j * stride];
@@ -154,52 +171,111 @@ struct Terms {
     }
 };
 
+// Chunks whose decays are held: as many as wavefronts, which form one each, and the one in use.
+constexpr int kDecays = kWaves + 1;
+
+// Tokens of a chunk.
+template <typename T, int KD> constexpr int kChunk = sizeof(T) == 2 && KD <= 128 ? 64 : 32;
+
+// Key and query rows, read along (eight neighbours, sixteen rows at a time) and
+// down (four rows of four blocks, 16 bytes apart).  bf16 rows have 64 bytes
+// behind them and their 16-byte pieces permuted in fours by the row: sixteen
+// rows' pieces of one place then lie in all the banks, and four rows' blocks
+// too (4.5 and 4.1 clocks a wavefront's read; 8.1 and 8.1 with 16 bytes behind
+// the rows), while the place of the fours stays an offset in the instruction.
+template <typename T, int WIDTH>
+struct KeyRows {
+    static constexpr int kStride = WIDTH + (sizeof(T) == 2 ? 32 : 4);
+    // eight elements from 8 c on
+    static __device__ __forceinline__ int at(int row, int c) {
+        return row * kStride + (sizeof(T) == 2 ? 32 * (c / 4) + 8 * ((c ^ row >> 2) & 3) : 8 * c);
+    }
+    // a 16-byte piece from column `col` on
+    static __device__ __forceinline__ int piece(int row, int col) {
+        return sizeof(T) == 2 ? at(row, col / 8) : row * kStride + col;
+    }
+};
+// Rows of scores, as above with dense rows (there are up to six tiles of them).
+template <typename T, int C>
+struct ScoreRows {
+    static constexpr int kStride = sizeof(T) == 2 ? C : C + 4;
+    static __device__ __forceinline__ int at(int row, int c) {
+        const int f = C == 64 ? (row >> 1 & 1) << 2 | (row >> 2 & 3) : row >> 2 & 3;
+        return row * kStride + 8 * (sizeof(T) == 2 ? c ^ f : c);
+    }
+};
+
 template <typename T, int KD, bool STATES, int TERMS>
 struct Lds {
-    static constexpr int C = linear::chunk(sizeof(T) == 2);
+    static constexpr int C = kChunk<T, KD>;
     static constexpr int E = 16 / sizeof(T);                 // elements of a 16-byte piece
-    static constexpr int kKey = KD + E, kValue = linear::kColumns + E, kScore = C + E;   // row strides
-    alignas(16) T K[C * kKey];
-    alignas(16) T V[C * kValue];
-    alignas(16) T Q[STATES ? E : C * kKey];
-    alignas(16) T P[STATES ? 1 : TERMS][STATES ? E : C * kScore];   // scores, in terms
-    alignas(16) f32x4 other[STATES ? 1 : kWaves * C / 32 * 64];     // outputs' parts that the other half finishes
-    alignas(16) float hi[C];                                 // log2 of the decay since the chunk's start
-    alignas(16) float lo[C];                                 // as two floats
-    alignas(16) float since[C];                              // that decay
-    alignas(16) float until[C];                              // the decay until the chunk's end (times `fresh`)
-    float whole[4];                                          // the chunk's decay
+    using Keys = KeyRows<T, KD>;
+    using Scores = ScoreRows<T, C>;
+    static constexpr int kValue = linear::kColumns + E;      // row stride
+    // two of what the next chunk's scores and decays need while this one's are in use
+    alignas(16) T K[2][C * Keys::kStride];
+    alignas(16) T Q[STATES ? 1 : 2][STATES ? E : C * Keys::kStride];
+    alignas(16) T V[STATES ? 2 : 1][C * kValue];
+    alignas(16) T P[STATES ? 1 : 2][TERMS][STATES ? E : C * Scores::kStride];   // scores, in terms
+    alignas(16) f32x4 other[STATES ? 1 : kWaves * C / 32 * 64];        // outputs' parts that the other half finishes
+    alignas(16) float hi[kDecays][C];                        // log2 of the decay since the chunk's start
+    alignas(16) float lo[kDecays][C];                        // as two floats
+    alignas(16) float until[kDecays][C];                     // the decay until the chunk's end times `fresh`
+    float whole[kDecays];                                    // the chunk's decay
+    double whole_log2[STATES ? kWaves : 1];
 };
 
-// A chunk's rows as 16-byte pieces, spread over the workgroup.
-template <typename T, int WIDTH>
+// A chunk's rows as 16-byte pieces, spread over the workgroup: piece m of a
+// thread holds 16 bytes of local row t.  Rows are addressed from the lowest of
+// the C tokens that a whole chunk spans, and the address moves on by a chunk a
+// fetch: a chunk past the end has no rows and reads nothing.
+template <typename T, int WIDTH, int C>
 struct Rows {
-    static constexpr int C = linear::chunk(sizeof(T) == 2), E = 16 / sizeof(T);
-    static constexpr int PER_ROW = WIDTH / E, N = C * PER_ROW / kThreads;
-    static_assert(C * PER_ROW % kThreads == 0, "whole pieces for every thread");
+    static constexpr int E = 16 / sizeof(T), PER_ROW = WIDTH / E, ALL = C * PER_ROW;
+    static constexpr int N = (ALL + kThreads - 1) / kThreads;
     u32x4 piece[N];
-    // `n` rows from `base` on, `row` elements apart, the first `width` elements of each
-    __device__ __forceinline__ void fetch(const T* base, int64_t row, int n, int width, int tid) {
-        const __amdgpu_buffer_rsrc_t r = make_rsrc(base, kRecords);
+    uint32_t at[N];
+    const char* base;
+    int step;
+    __device__ __forceinline__ static int row_of(int m, int tid) { return (tid + m * kThreads) / PER_ROW; }
+    __device__ __forceinline__ static int col_of(int m, int tid) { return (tid + m * kThreads) % PER_ROW * E; }
+    // from `token0` of the tensor on, `row` elements between tokens, the first `width` of each
+    __device__ __forceinline__ void place(const T* tensor, int64_t token0, int64_t row, int width, bool rev, int tid) {
+        base = reinterpret_cast<const char*>(tensor + token0 * row);
+        step = (rev ? -C : C) * (int)row * (int)sizeof(T);
 #pragma unroll
         for (int m = 0; m < N; ++m) {
-            const int p = tid + m * kThreads, t = p / PER_ROW, c = p % PER_ROW * E;
-            const uint32_t at = t < n && c < width ? (uint32_t)((t * (int)row + c) * (int)sizeof(T)) : kNoOffset;
-            piece[m] = __builtin_amdgcn_raw_buffer_load_b128(r, (int)at, 0, 0);
+            const int t = row_of(m, tid), c = col_of(m, tid);
+            at[m] = t < C && c < width ? (uint32_t)(((rev ? C - 1 - t : t) * (int)row + c) * (int)sizeof(T)) : kNoOffset;
         }
     }
-    __device__ __forceinline__ void stage(T* tile, int stride, int n, bool reversed, int tid) {
+    __device__ __forceinline__ void fetch(int n, int tid) {
+        const __amdgpu_buffer_rsrc_t r = make_rsrc(base, kRecords);
+        base += step;
+#pragma unroll
+        for (int m = 0; m < N; ++m)
+            piece[m] = __builtin_amdgcn_raw_buffer_load_b128(r, (int)(row_of(m, tid) < n ? at[m] : kNoOffset), 0, 0);
+    }
+    // `place` gives a piece's place by its row and column
+    template <typename Place> __device__ __forceinline__ void stage(T* tile, int tid, Place&& place) {
 #pragma unroll
         for (int m = 0; m < N; ++m) {
-            const int p = tid + m * kThreads, t = p / PER_ROW, c = p % PER_ROW * E;
-            const int to = reversed && t < n ? n - 1 - t : t;
-            *reinterpret_cast<u32x4*>(&tile[to * stride + c]) = piece[m];
+            const int t = row_of(m, tid);
+            if (ALL % kThreads == 0 || t < C) *reinterpret_cast<u32x4*>(&tile[place(t, col_of(m, tid))]) = piece[m];
         }
     }
 };
 
-// The half that finishes output tile `it`: 0 1 1 0, so both have as many blocks of keys.
-__device__ __forceinline__ constexpr int half_of(int it) { return (it ^ it >> 1) & 1; }
+// A uniform argument held in a scalar register: read again from the argument
+// block inside the loop, each use would wait for all LDS traffic as well.
+__device__ __forceinline__ int held(int x) {
+    x = __builtin_amdgcn_readfirstlane(x);
+    asm volatile("" : "+s"(x));
+    return x;
+}
+__device__ __forceinline__ float held(float x) { return __int_as_float(held(__float_as_int(x))); }
+// Loads before it are issued before it, whatever uses them comes after.
+__device__ __forceinline__ void issue_point() { __builtin_amdgcn_sched_barrier(0); }
 
 template <typename T, int KD, bool STATES, bool SPLIT>
 __global__ __launch_bounds__(kThreads, 2) void linear_chunks(LinearRun run) {
@@ -207,7 +283,11 @@ __global__ __launch_bounds__(kThreads, 2) void linear_chunks(LinearRun run) {
     using Frag = typename M::Frag;
     constexpr int TERMS = SPLIT && sizeof(T) == 2 ? 3 : 1;   // of the scores and of the state as an operand
     using L = Lds<T, KD, STATES, TERMS>;
+    using Keys = typename L::Keys;
+    using Scores = typename L::Scores;
     constexpr int C = L::C, RT = C / 16, KB = C / 32, KK = KD / 64;   // KK: of this half
+    constexpr bool kDots = SPLIT || sizeof(T) == 4;
+    constexpr int OWN = RT / 2;                              // output tiles that a half finishes
     constexpr int TILES = RT * (RT + 1) / 2;                 // score tiles on and below the diagonal
     __shared__ L s;
 
@@ -224,7 +304,8 @@ __global__ __launch_bounds__(kThreads, 2) void linear_chunks(LinearRun run) {
     const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
     const int group = wave % kGroups, half = wave / kGroups, k0 = half * KK;
     const bool rev = job.reversed;
-    const int kd = job.kd, vd = job.vd;
+    const int kd = held(job.kd), vd = held(job.vd);
+    const float inner = held(job.inner), outer = held(job.outer), fresh = held(job.fresh);
     const int col0 = tile * linear::kColumns;                // the workgroup's columns
     const int col = col0 + 16 * group;                       // the wavefront's
     const bool live = col < vd;
@@ -237,39 +318,133 @@ __global__ __launch_bounds__(kThreads, 2) void linear_chunks(LinearRun run) {
     const int64_t from = seg * run.seg_tokens;
     const int64_t last = from + run.seg_tokens < run.L ? from + run.seg_tokens : run.L;
     const int64_t to = last < len ? last : len;
-    const int64_t chunks = to > from ? (to - from + C - 1) / C : 0;
+    const int tokens = to > from ? (int)(to - from) : 0;
+    const int chunks = (tokens + C - 1) / C;
+    // Local row i of chunk c is token from + c C + i, or to - 1 - c C - i.
+    const int64_t token0 = rev ? to - C : from;              // the lowest that a whole chunk 0 spans
 
-    // rows of token t: base + t * row
-    const T* qb = STATES ? nullptr
-                         : static_cast<const T*>(job.q) + b * run.L * job.q_row + (int64_t)(h / job.q_per) * kd;
-    const T* kb = static_cast<const T*>(job.k) + b * run.L * job.k_row + (int64_t)(h / job.k_per) * kd;
-    const T* vb = static_cast<const T*>(job.v) + b * run.L * job.v_row + (int64_t)(h / job.v_per) * vd + col0;
+    Rows<T, KD, C> qr, kr;
+    Rows<T, linear::kColumns, C> vr;
+    if constexpr (!STATES)
+        qr.place(static_cast<const T*>(job.q) + b * run.L * job.q_row + (int64_t)(h / job.q_per) * kd, token0,
+                 job.q_row, kd, rev, tid);
+    kr.place(static_cast<const T*>(job.k) + b * run.L * job.k_row + (int64_t)(h / job.k_per) * kd, token0, job.k_row,
+             kd, rev, tid);
+    vr.place(static_cast<const T*>(job.v) + b * run.L * job.v_row + (int64_t)(h / job.v_per) * vd + col0, token0,
+             job.v_row, vd - col0, rev, tid);
     const float* gb = run.by_head ? run.g + h : run.g + b * run.L * run.H + h;
-
-    Rows<T, KD> qr, kr;
-    Rows<T, linear::kColumns> vr;
+    // The decays of chunks c .. c + 7, one to a wavefront: loaded well ahead.
     float gr = 0.0f;
-    // tokens lo .. lo + n - 1 make chunk c
-    const auto place = [&](int64_t c, int64_t& lo, int& n) {
-        const int64_t left = (to - from) - c * C;
-        n = left < C ? (int)left : C;
-        lo = rev ? to - c * C - n : from + c * C;
-    };
-    const auto fetch = [&](int64_t c) {
-        int64_t lo;
-        int n;
-        place(c, lo, n);
-        if constexpr (!STATES) qr.fetch(qb + lo * job.q_row, job.q_row, n, kd, tid);
-        kr.fetch(kb + lo * job.k_row, job.k_row, n, kd, tid);
-        vr.fetch(vb + lo * job.v_row, job.v_row, n, vd - col0, tid);
+    const auto fetch_decays = [&](int c) {
+        const int at = (c + wave) * C + lane;                // local
         gr = 0.0f;
-        if (wave == 0 && lane < n) {
-            const int64_t t = rev ? lo + n - lane : lo + lane;       // reversed: the g of the token behind
+        if (lane < C && at < tokens) {
+            const int64_t t = rev ? to - at : from + at;     // reversed: the g of the token behind
             if (t < len) gr = run.by_head ? gb[0] : gb[t * run.H];
         }
     };
-    if (chunks > 0) fetch(0);
+    double seg_decay = 0.0;
+    const auto decays = [&](int c) {
+        const int at = (c + wave) % kDecays;
+        double x = (double)gr * 1.4426950408889634074;
+        if (x < (double)kMinLog2) x = (double)kMinLog2;              // a NaN stays
+        const double sum = wave_sums(x, lane), all = from_lane(sum, 63);
+        if (lane < C) {
+            const float hi = (float)sum;
+            s.hi[at][lane] = hi;
+            s.lo[at][lane] = (float)(sum - (double)hi);
+            s.until[at][lane] = fast_exp2((float)(all - sum)) * fresh;
+        }
+        if (lane == 0) s.whole[at] = fast_exp2((float)all);
+        seg_decay += all;
+    };
+    // A chunk's scores, transposed: a lane has four keys of one query.  The
+    // operands come in groups, each on its way before the first of it is used.
+    constexpr int KS = KD / 32, GS = sizeof(T) == 4 ? 2 : 4;
+    struct Score {
+        int at, slot, query, key;
+        Frag k[GS], q[GS];
+        f32x4 acc, hk, lk;
+        float hq, lq;
+    };
+    const auto tile_load = [&](Score& x, int group) {
+#pragma unroll
+        for (int n = 0; n < GS; ++n) {
+            const int kk = group * GS + n;
+            if (kk < KS) {
+                x.k[n] = M::along(&s.K[x.at][Keys::at(x.key - 4 * g + i, 4 * kk + g)]);
+                x.q[n] = M::along(&s.Q[x.at][Keys::at(x.query, 4 * kk + g)]);
+            }
+        }
+    };
+    const auto tile_products = [&](Score& x, int group) {
+#pragma unroll
+        for (int n = 0; n < GS; ++n)
+            if (group * GS + n < KS) x.acc = M::mma(x.k[n], x.q[n], x.acc);
+    };
+    const auto tile_start = [&](Score& x, int at, int slot, int idx) {
+        const int it = (idx >= 1) + (idx >= 3) + (idx >= 6), jt = idx - it * (it + 1) / 2;
+        x.at = at, x.slot = slot, x.query = 16 * it + i, x.key = 16 * jt + 4 * g;
+        x.acc = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        tile_load(x, 0);
+        x.hq = s.hi[slot][x.query], x.lq = s.lo[slot][x.query];
+        x.hk = *reinterpret_cast<const f32x4*>(&s.hi[slot][x.key]);
+        x.lk = *reinterpret_cast<const f32x4*>(&s.lo[slot][x.key]);
+    };
+    const auto tile_multiply = [&](Score& x) {
+        tile_products(x, 0);
+#pragma unroll
+        for (int group = 1; group * GS < KS; ++group) {
+            tile_load(x, group);
+            issue_point();
+            tile_products(x, group);
+        }
+    };
+    const auto tile_finish = [&](Score& x) {
+        f32x4 acc = x.acc;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const bool seen = x.key + r <= x.query;
+            const float log2 = (x.hq - x.hk[r]) + (x.lq - x.lk[r]);
+            const float e = fast_exp2(seen ? log2 : kMinLog2) * inner;
+            acc[r] = (seen ? acc[r] : 0.0f) * e;
+        }
+#pragma unroll
+        for (int n2 = 0; n2 < TERMS; ++n2) {
+            T* p = &s.P[x.at][n2][Scores::at(x.query, x.key / 8) + x.key % 8];
+            if constexpr (sizeof(T) == 4) {
+                *reinterpret_cast<f32x4*>(p) = acc;
+            } else {
+                const u32x2 y = {pair(acc[0], acc[1]), pair(acc[2], acc[3])};
+                *reinterpret_cast<u32x2*>(p) = y;
+                if (n2 + 1 < TERMS)
+                    acc -= f32x4{__uint_as_float(y[0] << 16), __uint_as_float(y[0] & 0xffff0000u),
+                                 __uint_as_float(y[1] << 16), __uint_as_float(y[1] & 0xffff0000u)};
+            }
+        }
+    };
 
+    const auto key_place = [](int row, int col) { return Keys::piece(row, col); };
+    const auto value_place = [](int row, int col) { return row * L::kValue + col; };
+    // this half's queries for the product with the state, over all tokens, its own tiles first
+    constexpr bool kAhead = !STATES && !SPLIT && KD <= 128;      // read a phase ahead where registers hold them
+    Frag q[STATES ? 1 : KK][2 * OWN];
+    const int even = Keys::at(i, 4 * k0 + g) + 16 * half * Keys::kStride;
+    const int odd = Keys::at(i, 4 * k0 + g) - 16 * half * Keys::kStride;
+    const auto load_queries = [&](const T* tile) {
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+            for (int o = 0; o < 2 * OWN; ++o) {
+                const int it = RT == 2 ? o : o == 0 ? 0 : o == 1 ? 3 : o == 2 ? 1 : 2;     // ^ half
+                q[kk][o] = M::along(&tile[(it & 1 ? odd : even) + 16 * it * Keys::kStride + 32 * kk]);
+            }
+    };
+
+    if constexpr (!STATES) qr.fetch(tokens, tid);
+    kr.fetch(tokens, tid);
+    vr.fetch(tokens, tid);
+    fetch_decays(0);
     f32x4 state[KK][2];
     {
         const float* p = job.state_in ? job.state_in + bh * job.in_head + seg * job.in_seg : nullptr;
@@ -283,154 +458,243 @@ __global__ __launch_bounds__(kThreads, 2) void linear_chunks(LinearRun run) {
                     state[kk][u][r] = p && live && row < kd ? p[(int64_t)row * job.sk + (int64_t)(col + i) * job.sv] : 0.0f;
                 }
     }
-    if constexpr (!STATES) {
-        // the score tiles right of the diagonal that a block of 32 keys reaches are zero throughout
-        for (int e = tid; e < RT / 2 * 256; e += kThreads) {
-            const int at = (32 * (e / 256) + e % 256 / 16) * L::kScore + 32 * (e / 256) + 16 + e % 16;
+    if (chunks > 0) {
+        if constexpr (!STATES) {
+            // the score tiles right of the diagonal that a block of 32 keys reaches are zero throughout
+            for (int e = tid; e < RT / 2 * 256; e += kThreads) {
+                const int col = 32 * (e / 256) + 16 + e % 16;
+                const int at = Scores::at(32 * (e / 256) + e % 256 / 16, col / 8) + col % 8;
 #pragma unroll
-            for (int n = 0; n < TERMS; ++n) s.P[n][at] = T(0);
+                for (int n = 0; n < 2 * TERMS; ++n) s.P[n % 2][n / 2][at] = T(0);
+            }
+            qr.stage(s.Q[0], tid, key_place);
+        } else {
+            vr.stage(s.V[0], tid, value_place);
+        }
+        kr.stage(s.K[0], tid, key_place);
+        decays(0);
+        fetch_decays(kWaves);
+        if constexpr (STATES) vr.fetch(tokens - C, tid);
+        else qr.fetch(tokens - C, tid);
+        kr.fetch(tokens - C, tid);
+        lds_barrier();
+        if constexpr (!STATES) {
+            for (int idx = wave; idx < TILES; idx += kWaves) {
+                Score x;
+                tile_start(x, 0, 0, idx);
+                tile_multiply(x);
+                tile_finish(x);
+            }
+            if constexpr (kAhead) load_queries(s.Q[0]);
+            lds_barrier();
         }
     }
 
-    double seg_decay = 0.0;
-    for (int64_t c = 0; c < chunks; ++c) {
-        int64_t lo;
-        int n;
-        place(c, lo, n);
-        lds_barrier();                                       // the last chunk's rows have been read
-        if constexpr (!STATES) qr.stage(s.Q, L::kKey, n, rev, tid);
-        kr.stage(s.K, L::kKey, n, rev, tid);
-        vr.stage(s.V, L::kValue, n, rev, tid);
-        if (wave == 0) {
-            double x = (double)gr * 1.4426950408889634074;
-            if (x < (double)kMinLog2) x = (double)kMinLog2;          // a NaN stays
-            const double sum = wave_sums(x, lane), all = from_lane(sum, 63);
-            if (lane < C) {
-                const float hi = (float)sum;
-                s.hi[lane] = hi;
-                s.lo[lane] = (float)(sum - (double)hi);
-                s.since[lane] = fast_exp2(hi) * job.outer;
-                s.until[lane] = fast_exp2((float)(all - sum)) * job.fresh;
-            }
-            if (lane == 0) s.whole[0] = fast_exp2((float)all);
-            seg_decay += all;
+    // the outputs' places: row 16 own + i of this half's tiles, four columns from `col` on
+    const bool wide = sizeof(T) == 4 || held(job.out_f32);
+    const int esize = wide ? 4 : 2;
+    int own[OWN];
+    uint32_t out_at[OWN], dot_at[OWN];
+    char* out_base = nullptr;
+    const char* dot_base = nullptr;
+    float* dots = nullptr;
+    int out_step = 0, dot_step = 0;
+    if constexpr (!STATES) {
+#pragma unroll
+        for (int o = 0; o < OWN; ++o) {
+            own[o] = RT == 2 ? half : o == 0 ? half : 3 - half;      // 0 and 3, or 1 and 2: three blocks of keys each
+            const int row = 16 * own[o] + i, t = rev ? C - 1 - row : row;
+            out_at[o] = live ? (uint32_t)((t * (int)run.H * vd + 4 * g) * esize) : kNoOffset;
+            if constexpr (kDots) dot_at[o] = live ? (uint32_t)((t * (int)job.dot_row + 4 * g) * (int)sizeof(T)) : kNoOffset;
         }
-        lds_barrier();
-        if (c + 1 < chunks) fetch(c + 1);
+        out_base = static_cast<char*>(job.out) + (((b * run.L + token0) * run.H + h) * vd + col) * esize;
+        out_step = (rev ? -C : C) * (int)run.H * vd * esize;
+        if (kDots && job.dots) {
+            dot_base = static_cast<const char*>(job.dot_with) +
+                       ((b * run.L + token0) * job.dot_row + (int64_t)(h / job.dot_per) * vd + col) * (int)sizeof(T);
+            dot_step = (rev ? -C : C) * (int)job.dot_row * (int)sizeof(T);
+            dots = job.dots + ((int64_t)(tile * kGroups + group) * run.B * run.H + bh) * run.L + token0;
+        }
+    }
 
-        f32x4 out[RT];
-        if constexpr (!STATES) {
-            // scores, transposed: a lane has four keys of one query
+    int slot = 0, left = tokens, until_decays = kWaves - 1;  // left: tokens from this chunk on
+    const auto step = [&](auto parity, int c) {
+        constexpr int now = decltype(parity)::value, next = now ^ 1;
+        const int next_slot = slot + 1 == kDecays ? 0 : slot + 1;
+        f32x4 out[OWN], theirs[OWN];
+        Frag k[KB][KK][2], p[OWN][KB][TERMS];
+        const auto load_keys = [&] {
 #pragma unroll
-            for (int m = 0; m < (TILES + kWaves - 1) / kWaves; ++m) {
-                const int idx = kWaves - 1 - wave + m * kWaves;
-                if (idx >= TILES) break;
-                const int it = (idx >= 1) + (idx >= 3) + (idx >= 6), jt = idx - it * (it + 1) / 2;
-                f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int b2 = 0; b2 < KB; ++b2)
 #pragma unroll
-                for (int kk = 0; kk < KD / 32; ++kk)
-                    acc = M::mma(M::along(&s.K[(16 * jt + i) * L::kKey + 32 * kk + 8 * g]),
-                                 M::along(&s.Q[(16 * it + i) * L::kKey + 32 * kk + 8 * g]), acc);
-                const int query = 16 * it + i, key = 16 * jt + 4 * g;
-                const float hq = s.hi[query], lq = s.lo[query];
-                const f32x4 hk = *reinterpret_cast<const f32x4*>(&s.hi[key]);
-                const f32x4 lk = *reinterpret_cast<const f32x4*>(&s.lo[key]);
+                for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float e = fast_exp2((hq - hk[r]) + (lq - lk[r])) * job.inner;
-                    acc[r] = key + r <= query ? acc[r] * e : 0.0f;
-                }
-#pragma unroll
-                for (int n2 = 0; n2 < TERMS; ++n2) {
-                    T* p = &s.P[n2][query * L::kScore + key];
-                    if constexpr (sizeof(T) == 4) {
-                        *reinterpret_cast<f32x4*>(p) = acc;
-                    } else {
-                        const bf16x4 x = __builtin_convertvector(acc, bf16x4);
-                        *reinterpret_cast<bf16x4*>(p) = x;
-                        acc -= __builtin_convertvector(x, f32x4);
+                    for (int w = 0; w < 2; ++w) {
+                        const T* tile = s.K[now];
+                        const int row = 32 * b2 + 8 * g, c8 = 4 * (k0 + kk);
+                        if constexpr (sizeof(T) == 2)
+                            k[b2][kk][w] = M::down(&tile[Keys::at(row + i / 4, c8 + i % 4) + 4 * w],
+                                                   &tile[Keys::at(row + 4 + i / 4, c8 + i % 4) + 4 * w]);
+                        else
+                            k[b2][kk][w] = M::down(&tile[Keys::at(row, c8 + i / 4) + 4 * w + i % 4], Keys::kStride);
                     }
-                }
-            }
-            // the entering state's part
+        };
+        if constexpr (!STATES) {
+            // the entering state's part of the outputs, over this half's key rows
+            if constexpr (kAhead) load_keys();
+            else load_queries(s.Q[now]);
+            issue_point();
+            vr.stage(s.V[0], tid, value_place);
+            qr.stage(s.Q[next], tid, key_place);
+            kr.stage(s.K[next], tid, key_place);
+            qr.fetch(left - 2 * C, tid);
+            kr.fetch(left - 2 * C, tid);
+            vr.fetch(left - C, tid);
 #pragma unroll
-            for (int it = 0; it < RT; ++it) out[it] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int o = 0; o < OWN; ++o) out[o] = theirs[o] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk) {
                 const Terms<T, TERMS> x(__builtin_shufflevector(state[kk][0], state[kk][1], 0, 1, 2, 3, 4, 5, 6, 7));
 #pragma unroll
-                for (int it = 0; it < RT; ++it) {
-                    const Frag q = M::along(&s.Q[(16 * it + i) * L::kKey + 32 * (k0 + kk) + 8 * g]);
+                for (int n2 = 0; n2 < TERMS; ++n2)
 #pragma unroll
-                    for (int n2 = 0; n2 < TERMS; ++n2) out[it] = M::mma(x.term[n2], q, out[it]);
-                }
+                    for (int o = 0; o < OWN; ++o) {
+                        out[o] = M::mma(x.term[n2], q[kk][o], out[o]);
+                        theirs[o] = M::mma(x.term[n2], q[kk][OWN + o], theirs[o]);
+                    }
             }
-#pragma unroll
-            for (int it = 0; it < RT; ++it)
-                if (half_of(it) != half) s.other[(wave * (RT / 2) + it / 2) * 64 + lane] = out[it];
-            lds_barrier();                                   // the scores and the other half's parts are there
+        } else {
+            vr.stage(s.V[next], tid, value_place);
+            kr.stage(s.K[next], tid, key_place);
+            kr.fetch(left - 2 * C, tid);
+            vr.fetch(left - 2 * C, tid);
         }
-
-        const float whole = s.whole[0];
-#pragma unroll
-        for (int kk = 0; kk < KK; ++kk) state[kk][0] *= whole, state[kk][1] *= whole;
-        Frag v[KB];
-#pragma unroll
-        for (int b2 = 0; b2 < KB; ++b2) v[b2] = M::down(s.V, L::kValue, 32 * b2 + 8 * g, 16 * group, 4, i);
-#pragma unroll
-        for (int b2 = 0; b2 < KB; ++b2) {
-            const f32x4 u0 = *reinterpret_cast<const f32x4*>(&s.until[32 * b2 + 8 * g]);
-            const f32x4 u1 = *reinterpret_cast<const f32x4*>(&s.until[32 * b2 + 8 * g + 4]);
-            const Terms<T, 3> w(M::widen(v[b2]) * __builtin_shufflevector(u0, u1, 0, 1, 2, 3, 4, 5, 6, 7));
-#pragma unroll
-            for (int kk = 0; kk < KK; ++kk)
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const Frag k = M::down(s.K, L::kKey, 32 * b2 + 8 * g, 32 * (k0 + kk) + 4 * u, 8, i);
-#pragma unroll
-                    for (int n2 = 0; n2 < Terms<T, 3>::kN; ++n2) state[kk][u] = M::mma(k, w.term[n2], state[kk][u]);
-                }
+        if (until_decays == 0) {                             // the next chunk is the first whose decays are not there
+            decays(c + 1);
+            fetch_decays(c + 1 + kWaves);
+            until_decays = kWaves;
         }
-
+        --until_decays;
         if constexpr (!STATES) {
 #pragma unroll
-            for (int it = 0; it < RT; ++it) {
-                if (half_of(it) != half) continue;
-                // wavefront-uniform, and the indices are constants
-                f32x4 x = out[it] + s.other[((wave ^ kGroups) * (RT / 2) + it / 2) * 64 + lane];
-                const int row = 16 * it + i;
-                x *= s.since[row];
+            for (int o = 0; o < OWN; ++o) s.other[(wave * OWN + o) * 64 + lane] = theirs[o];
+            lds_barrier();   // the parts of the other half, this chunk's values, the next one's keys and queries are there
+        }
+
+        // the next chunk's scores; the other operands are on their way meanwhile
+        Score x;
+        const bool scores = !STATES && (TILES >= kWaves || wave < TILES);
+        const T* V = s.V[STATES ? now : 0];
+        Frag v[KB];
+        f32x4 u[KB][2], theirs_for[OWN];
+        float since[OWN];
+        if (scores) tile_start(x, next, next_slot, wave);
+        issue_point();
+        if (scores) tile_multiply(x);
 #pragma unroll
-                for (int b2 = 0; b2 <= it / 2; ++b2) {
+        for (int b2 = 0; b2 < KB; ++b2) {
+            const T* at = &V[(32 * b2 + 8 * g) * L::kValue + 16 * group];
+            if constexpr (sizeof(T) == 2)
+                v[b2] = M::down(at + i / 4 * L::kValue + 4 * (i % 4), at + (4 + i / 4) * L::kValue + 4 * (i % 4));
+            else
+                v[b2] = M::down(at + i, L::kValue);
+            u[b2][0] = *reinterpret_cast<const f32x4*>(&s.until[slot][32 * b2 + 8 * g]);
+            u[b2][1] = *reinterpret_cast<const f32x4*>(&s.until[slot][32 * b2 + 8 * g + 4]);
+        }
+        const float decay = s.whole[slot];
+        if constexpr (!kAhead) load_keys();
+        if constexpr (!STATES) {
 #pragma unroll
-                    for (int n2 = 0; n2 < TERMS; ++n2)
-                        x = M::mma(v[b2], M::along(&s.P[n2][row * L::kScore + 32 * b2 + 8 * g]), x);
-                }
-                if (!live) continue;
-                const int64_t t = rev ? lo + n - 1 - row : lo + row;
-                const int64_t at = b * run.L + t;            // of the token
-                if (row < n) {
-                    const int64_t to2 = (at * run.H + h) * vd + col + 4 * g;
-                    if (sizeof(T) == 4 || job.out_f32)
-                        *reinterpret_cast<f32x4*>(static_cast<float*>(job.out) + to2) = x;
-                    else
-                        *reinterpret_cast<bf16x4*>(static_cast<uint16_t*>(job.out) + to2) = __builtin_convertvector(x, bf16x4);
-                }
-                if (job.dots) {
-                    float sum = 0.0f;
-                    if (row < n) {
-                        const T* y = static_cast<const T*>(job.dot_with) + at * job.dot_row +
-                                     (int64_t)(h / job.dot_per) * vd + col + 4 * g;
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) sum = fmaf(x[r], Elem<T>::load(y, r), sum);
-                    }
-                    sum += __shfl_xor(sum, 16);
-                    sum += __shfl_xor(sum, 32);
-                    if (g == 0 && row < n)
-                        job.dots[((int64_t)(tile * kGroups + group) * run.B * run.H + bh) * run.L + t] = sum;
-                }
+            for (int o = 0; o < OWN; ++o) {
+                theirs_for[o] = s.other[((wave ^ kGroups) * OWN + o) * 64 + lane];
+                since[o] = s.hi[slot][16 * own[o] + i];
             }
         }
+        issue_point();
+        if (scores) tile_finish(x);
+        if (!STATES && TILES > kWaves && wave + kWaves < TILES) {
+            tile_start(x, next, next_slot, wave + kWaves);
+            tile_multiply(x);
+            tile_finish(x);
+        }
+        if constexpr (!STATES) {
+#pragma unroll
+            for (int o = 0; o < OWN; ++o)
+#pragma unroll
+                for (int b2 = 0; b2 <= o; ++b2)
+#pragma unroll
+                    for (int n2 = 0; n2 < TERMS; ++n2)
+                        p[o][b2][n2] = M::along(&s.P[now][n2][Scores::at(16 * own[o] + i, 4 * b2 + g)]);
+            if constexpr (kAhead) load_queries(s.Q[next]);
+            issue_point();
+        }
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) state[kk][0] *= decay, state[kk][1] *= decay;
+#pragma unroll
+        for (int b2 = 0; b2 < KB; ++b2) {
+            const Terms<T, 3> w(M::widen(v[b2]) * __builtin_shufflevector(u[b2][0], u[b2][1], 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+            for (int n2 = 0; n2 < Terms<T, 3>::kN; ++n2)
+#pragma unroll
+                for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+                    for (int w2 = 0; w2 < 2; ++w2) state[kk][w2] = M::mma(k[b2][kk][w2], w.term[n2], state[kk][w2]);
+        }
+        if constexpr (!STATES) {
+            const __amdgpu_buffer_rsrc_t to_out = make_rsrc(out_base, kRecords);
+            out_base += out_step;
+#pragma unroll
+            for (int o = 0; o < OWN; ++o) out[o] = (out[o] + theirs_for[o]) * (fast_exp2(since[o]) * outer);
+#pragma unroll
+            for (int b2 = 0; b2 < KB; ++b2)
+#pragma unroll
+                for (int n2 = 0; n2 < TERMS; ++n2)
+#pragma unroll
+                    for (int o = b2; o < OWN; ++o) out[o] = M::mma(v[b2], p[o][b2][n2], out[o]);
+#pragma unroll
+            for (int o = 0; o < OWN; ++o) {
+                const int row = 16 * own[o] + i;
+                const f32x4 y = out[o];
+                const int at = (int)(row < left ? out_at[o] : kNoOffset);
+                if (wide)
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y), to_out, at, 0, 0);
+                else
+                    __builtin_amdgcn_raw_buffer_store_b64(u32x2{pair(y[0], y[1]), pair(y[2], y[3])}, to_out, at, 0, 0);
+            }
+            if (kDots && dots) {
+                const __amdgpu_buffer_rsrc_t with = make_rsrc(dot_base, kRecords);
+                dot_base += dot_step;
+#pragma unroll
+                for (int o = 0; o < OWN; ++o) {
+                    const int row = 16 * own[o] + i;
+                    const int at = (int)(row < left ? dot_at[o] : kNoOffset);
+                    f32x4 y;
+                    if constexpr (sizeof(T) == 4) {
+                        y = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(with, at, 0, 0));
+                    } else {
+                        const u32x2 z = __builtin_amdgcn_raw_buffer_load_b64(with, at, 0, 0);
+                        y = f32x4{__uint_as_float(z[0] << 16), __uint_as_float(z[0] & 0xffff0000u),
+                                  __uint_as_float(z[1] << 16), __uint_as_float(z[1] & 0xffff0000u)};
+                    }
+                    float sum = fmaf(out[o][3], y[3], fmaf(out[o][2], y[2], fmaf(out[o][1], y[1], out[o][0] * y[0])));
+                    sum += __shfl_xor(sum, 16);
+                    sum += __shfl_xor(sum, 32);
+                    if (g == 0 && row < left && live) dots[rev ? C - 1 - row : row] = sum;
+                }
+                dots += rev ? -C : C;
+            }
+        }
+        lds_barrier();                                       // the next chunk's scores are there; this one's rows are free
+        slot = next_slot;
+        left -= C;
+    };
+    for (int c = 0; c < chunks; c += 2) {
+        step(std::integral_constant<int, 0>{}, c);
+        if (c + 1 < chunks) step(std::integral_constant<int, 1>{}, c + 1);
+    }
+    if constexpr (STATES) {                                  // each wavefront has summed the chunks that it formed
+        if (lane == 0) s.whole_log2[wave] = seg_decay;
+        lds_barrier();
     }
 
     if constexpr (!STATES) {
@@ -450,7 +714,11 @@ __global__ __launch_bounds__(kThreads, 2) void linear_chunks(LinearRun run) {
     float by = 1.0f;
     if constexpr (STATES) {
         p = run.seg_state[blockIdx.y] + unit * kd * vd;
-        if (tile == 0 && tid == 0) run.seg_decay[blockIdx.y][unit] = (float)seg_decay;
+        if (tile == 0 && tid == 0) {
+            double all = 0.0;
+            for (int w = 0; w < kWaves; ++w) all += s.whole_log2[w];
+            run.seg_decay[blockIdx.y][unit] = (float)all;
+        }
     } else if (job.state_out && seg == (rev ? 0 : run.segments - 1)) {
         p = job.state_out + bh * job.out_head;
         if (job.decay_out && len > 0) {

@@ -17,8 +17,7 @@ namespace linear {
 constexpr int kMaxWidth = 256;                          // of a key or value row
 constexpr int64_t kMaxRow = int64_t(1) << 22;           // elements between tokens: 64 of them within 32-bit byte offsets
 constexpr int kColumns = 64;                            // columns of the state per workgroup
-// tokens of a chunk: what a workgroup's products and its LDS rows span
-constexpr int chunk(bool bf16) { return bf16 ? 64 : 32; }
+constexpr int kSegment = 64;                            // segments are multiples of the longest chunk
 }  // namespace linear
 
 // One run of the recurrence S <- e^g S + k v^T, o = q^T S over [B, L] rows of
@@ -56,7 +55,7 @@ struct LinearRun {
     const int32_t* seq_lens;
     int64_t B, L, H;
     int32_t segments;
-    int64_t seg_tokens;          // a multiple of the chunk
+    int64_t seg_tokens;          // a multiple of kSegment
     int32_t bf16;
     int32_t split;               // products with operands split in two bf16 halves each
     float* seg_state[2];         // states-only runs: [B, H, segments][kd][vd] per job

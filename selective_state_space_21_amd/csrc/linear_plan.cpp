@@ -23,16 +23,16 @@ constexpr int64_t kMinSegment = 256;
 constexpr int64_t kMostCut = int64_t(1) << 14;
 
 // `groups` workgroups a segment
-LinearPlan plan(int64_t groups, int64_t L, int chunk) {
-    LinearPlan p{1, up(L > 0 ? L : 1, chunk)};
+LinearPlan plan(int64_t groups, int64_t L) {
+    LinearPlan p{1, up(L > 0 ? L : 1, linear::kSegment)};
     int64_t want = (kFill + groups - 1) / groups;
     if (const char* e = getenv("SSM_LINEAR_SEGMENTS")) {
         const long n = strtol(e, nullptr, 10);
         if (n >= 1 && n <= 256 && groups <= kMostCut) {
             want = n;
             if (want > 1) {
-                p.seg_tokens = up((L + want - 1) / want, chunk);
-                if (p.seg_tokens < chunk) p.seg_tokens = chunk;
+                p.seg_tokens = up((L + want - 1) / want, linear::kSegment);
+                if (p.seg_tokens < linear::kSegment) p.seg_tokens = linear::kSegment;
                 p.segments = L > 0 ? (int)((L + p.seg_tokens - 1) / p.seg_tokens) : 1;
             }
             return p;
@@ -40,7 +40,7 @@ LinearPlan plan(int64_t groups, int64_t L, int chunk) {
     }
     if (groups * 2 >= kFill || L < 2 * kMinSegment) return p;
     if (want > L / kMinSegment) want = L / kMinSegment;
-    p.seg_tokens = up((L + want - 1) / want, chunk);
+    p.seg_tokens = up((L + want - 1) / want, linear::kSegment);
     p.segments = (int)((L + p.seg_tokens - 1) / p.seg_tokens);
     return p;
 }
@@ -135,11 +135,11 @@ int pad(int64_t width) { return width <= 64 ? 64 : width <= 128 ? 128 : 256; }
 
 LinearPlan plan_linear_fwd(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv, bool bf16) {
     (void)Dk;
-    return plan(B * H * tiles_of(Dv), L, linear::chunk(bf16));
+    return plan(B * H * tiles_of(Dv), L);
 }
 
 LinearPlan plan_linear_bwd(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv, bool bf16) {
-    return plan(B * H * (2 * tiles_of(Dk) + tiles_of(Dv)), L, linear::chunk(bf16));
+    return plan(B * H * (2 * tiles_of(Dk) + tiles_of(Dv)), L);
 }
 
 size_t linear_fwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv, bool bf16) {

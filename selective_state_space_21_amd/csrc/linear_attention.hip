@@ -59,7 +59,7 @@ typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 512, kWaves = 8;
-constexpr int kGroups = linear::kColumns / 16;    // column groups: a wavefront of each half of the key rows
+constexpr int kGroups = linear::kColumns / 16;    // each team has a wavefront to 16 columns
 constexpr uint32_t kNoOffset = 0x80000000u;      // past every resource's end: loads give zeros
 constexpr uint32_t kRecords = 0x7ffffff0u;
 constexpr float kMinLog2 = -150.0f;              // 2^-150 is zero in fp32
@@ -215,9 +215,11 @@ struct Lds {
     // two of what the next chunk's scores and decays need while this one's are in use
     alignas(16) T K[2][C * Keys::kStride];
     alignas(16) T Q[STATES ? 1 : 2][STATES ? E : C * Keys::kStride];
-    alignas(16) T V[STATES ? 2 : 1][C * kValue];
+    // values too where LDS holds them: they are then ready a phase earlier
+    static constexpr bool kEarly = STATES || (sizeof(T) == 2 ? KD == 64 || TERMS == 1 : KD <= 128);
+    alignas(16) T V[kEarly ? 2 : 1][C * kValue];
     alignas(16) T P[STATES ? 1 : 2][TERMS][STATES ? E : C * Scores::kStride];   // scores, in terms
-    alignas(16) f32x4 other[STATES ? 1 : kWaves * C / 32 * 64];        // outputs' parts that the other half finishes
+    alignas(16) f32x4 through[STATES ? 1 : kGroups * C / 16 * 64];     // the state's part of the outputs
     alignas(16) float hi[kDecays][C];                        // log2 of the decay since the chunk's start
     alignas(16) float lo[kDecays][C];                        // as two floats
     alignas(16) float until[kDecays][C];                     // the decay until the chunk's end times `fresh`
@@ -277,6 +279,13 @@ __device__ __forceinline__ float held(float x) { return __int_as_float(held(__fl
 // Loads before it are issued before it, whatever uses them comes after.
 __device__ __forceinline__ void issue_point() { __builtin_amdgcn_sched_barrier(0); }
 
+// One team keeps the state (products with the queries, then the update), the
+// other everything that does not touch it (staging, scores, outputs): a SIMD
+// has a wavefront of each, so the one's matrix products run beside the other's
+// exponentials, and nothing is formed twice.  Two barriers a chunk:
+//   A  state: queries x state -> LDS            other: the last chunk's outputs to memory
+//      both: stage the next chunk, fetch the one behind it
+//   B  state: update                            other: the next chunk's scores, this one's outputs
 template <typename T, int KD, bool STATES, bool SPLIT>
 __global__ __launch_bounds__(kThreads, 2) void linear_chunks(LinearRun run) {
     using M = Mat<T>;
@@ -285,9 +294,8 @@ __global__ __launch_bounds__(kThreads, 2) void linear_chunks(LinearRun run) {
     using L = Lds<T, KD, STATES, TERMS>;
     using Keys = typename L::Keys;
     using Scores = typename L::Scores;
-    constexpr int C = L::C, RT = C / 16, KB = C / 32, KK = KD / 64;   // KK: of this half
+    constexpr int C = L::C, RT = C / 16, KB = C / 32, KK = KD / 32;
     constexpr bool kDots = SPLIT || sizeof(T) == 4;
-    constexpr int OWN = RT / 2;                              // output tiles that a half finishes
     constexpr int TILES = RT * (RT + 1) / 2;                 // score tiles on and below the diagonal
     __shared__ L s;
 
@@ -300,9 +308,10 @@ __global__ __launch_bounds__(kThreads, 2) void linear_chunks(LinearRun run) {
     const int seg = (int)(unit % run.segments);
     const int64_t bh = unit / run.segments, b = bh / run.H;
     const int h = (int)(bh % run.H);
-    const int tid = threadIdx.x, lane = tid % 64, i = lane % 16, g = lane / 16;
-    const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
-    const int group = wave % kGroups, half = wave / kGroups, k0 = half * KK;
+    const int lane = threadIdx.x % 64, i = lane % 16, g = lane / 16;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int group = wave % kGroups, tid = threadIdx.x;
+    const bool keeps = wave < kGroups;                       // the state's team
     const bool rev = job.reversed;
     const int kd = held(job.kd), vd = held(job.vd);
     const float inner = held(job.inner), outer = held(job.outer), fresh = held(job.fresh);
@@ -322,17 +331,8 @@ __global__ __launch_bounds__(kThreads, 2) void linear_chunks(LinearRun run) {
     const int chunks = (tokens + C - 1) / C;
     // Local row i of chunk c is token from + c C + i, or to - 1 - c C - i.
     const int64_t token0 = rev ? to - C : from;              // the lowest that a whole chunk 0 spans
-
-    Rows<T, KD, C> qr, kr;
-    Rows<T, linear::kColumns, C> vr;
-    if constexpr (!STATES)
-        qr.place(static_cast<const T*>(job.q) + b * run.L * job.q_row + (int64_t)(h / job.q_per) * kd, token0,
-                 job.q_row, kd, rev, tid);
-    kr.place(static_cast<const T*>(job.k) + b * run.L * job.k_row + (int64_t)(h / job.k_per) * kd, token0, job.k_row,
-             kd, rev, tid);
-    vr.place(static_cast<const T*>(job.v) + b * run.L * job.v_row + (int64_t)(h / job.v_per) * vd + col0, token0,
-             job.v_row, vd - col0, rev, tid);
     const float* gb = run.by_head ? run.g + h : run.g + b * run.L * run.H + h;
+
     // The decays of chunks c .. c + 7, one to a wavefront: loaded well ahead.
     float gr = 0.0f;
     const auto fetch_decays = [&](int c) {
@@ -358,49 +358,86 @@ __global__ __launch_bounds__(kThreads, 2) void linear_chunks(LinearRun run) {
         if (lane == 0) s.whole[at] = fast_exp2((float)all);
         seg_decay += all;
     };
-    // A chunk's scores, transposed: a lane has four keys of one query.  The
-    // operands come in groups, each on its way before the first of it is used.
-    constexpr int KS = KD / 32, GS = sizeof(T) == 4 ? 2 : 4;
+    fetch_decays(0);
+    int slot = 0, until_decays = kWaves - 1;
+    // at the end of a chunk's first half: the next chunk may be the first whose decays are not there
+    const auto more_decays = [&](int c) {
+        if (until_decays == 0) {
+            decays(c + 1);
+            fetch_decays(c + 1 + kWaves);
+            until_decays = kWaves;
+        }
+        --until_decays;
+    };
+    const auto next_of = [](int n) { return n + 1 == kDecays ? 0 : n + 1; };
+
+    Rows<T, KD, C> qr, kr;
+    Rows<T, linear::kColumns, C> vr;
+    if constexpr (!STATES)
+        qr.place(static_cast<const T*>(job.q) + b * run.L * job.q_row + (int64_t)(h / job.q_per) * kd, token0,
+                 job.q_row, kd, rev, tid);
+    kr.place(static_cast<const T*>(job.k) + b * run.L * job.k_row + (int64_t)(h / job.k_per) * kd, token0,
+             job.k_row, kd, rev, tid);
+    vr.place(static_cast<const T*>(job.v) + b * run.L * job.v_row + (int64_t)(h / job.v_per) * vd + col0, token0,
+             job.v_row, vd - col0, rev, tid);
+    const auto key_place = [](int row, int col) { return Keys::piece(row, col); };
+    const auto value_place = [](int row, int col) { return row * L::kValue + col; };
+    int left = tokens;                                       // from this chunk on
+    const auto stage = [&](int next) {                       // the next chunk; its values, or this one's where LDS holds one chunk's
+        vr.stage(s.V[L::kEarly ? next : 0], tid, value_place);
+        if constexpr (!STATES) qr.stage(s.Q[next], tid, key_place);
+        kr.stage(s.K[next], tid, key_place);
+    };
+    const auto fetch = [&] {
+        if constexpr (!STATES) qr.fetch(left - 2 * C, tid);
+        kr.fetch(left - 2 * C, tid);
+        vr.fetch(left - (L::kEarly ? 2 : 1) * C, tid);
+    };
+    if constexpr (!STATES) qr.fetch(tokens, tid);
+    kr.fetch(tokens, tid);
+    vr.fetch(tokens, tid);
+
+    // A chunk's scores, transposed: a lane has four keys of one query.  The operands come in groups,
+    // each on its way before the first of it is used.
+    constexpr int GS = sizeof(T) == 4 ? 2 : 4;
     struct Score {
-        int at, slot, query, key;
+        int query, key;
         Frag k[GS], q[GS];
         f32x4 acc, hk, lk;
         float hq, lq;
     };
-    const auto tile_load = [&](Score& x, int group) {
+    const auto load = [&](Score& x, const T* K, const T* Q, int group) {
 #pragma unroll
         for (int n = 0; n < GS; ++n) {
             const int kk = group * GS + n;
-            if (kk < KS) {
-                x.k[n] = M::along(&s.K[x.at][Keys::at(x.key - 4 * g + i, 4 * kk + g)]);
-                x.q[n] = M::along(&s.Q[x.at][Keys::at(x.query, 4 * kk + g)]);
+            if (kk < KK) {
+                x.k[n] = M::along(&K[Keys::at(x.key - 4 * g + i, 4 * kk + g)]);
+                x.q[n] = M::along(&Q[Keys::at(x.query, 4 * kk + g)]);
             }
         }
     };
-    const auto tile_products = [&](Score& x, int group) {
-#pragma unroll
-        for (int n = 0; n < GS; ++n)
-            if (group * GS + n < KS) x.acc = M::mma(x.k[n], x.q[n], x.acc);
-    };
-    const auto tile_start = [&](Score& x, int at, int slot, int idx) {
+    const auto start = [&](Score& x, int at, int slot, int idx) {
         const int it = (idx >= 1) + (idx >= 3) + (idx >= 6), jt = idx - it * (it + 1) / 2;
-        x.at = at, x.slot = slot, x.query = 16 * it + i, x.key = 16 * jt + 4 * g;
-        x.acc = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        tile_load(x, 0);
+        x.query = 16 * it + i, x.key = 16 * jt + 4 * g;
+        load(x, s.K[at], s.Q[STATES ? 0 : at], 0);
         x.hq = s.hi[slot][x.query], x.lq = s.lo[slot][x.query];
         x.hk = *reinterpret_cast<const f32x4*>(&s.hi[slot][x.key]);
         x.lk = *reinterpret_cast<const f32x4*>(&s.lo[slot][x.key]);
     };
-    const auto tile_multiply = [&](Score& x) {
-        tile_products(x, 0);
+    const auto multiply = [&](Score& x, int at) {
+        x.acc = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int group = 1; group * GS < KS; ++group) {
-            tile_load(x, group);
-            issue_point();
-            tile_products(x, group);
+        for (int group = 0; group * GS < KK; ++group) {
+            if (group > 0) {
+                load(x, s.K[at], s.Q[STATES ? 0 : at], group);
+                issue_point();
+            }
+#pragma unroll
+            for (int n = 0; n < GS; ++n)
+                if (group * GS + n < KK) x.acc = M::mma(x.k[n], x.q[n], x.acc);
         }
     };
-    const auto tile_finish = [&](Score& x) {
+    const auto finish = [&](Score& x, int at) {
         f32x4 acc = x.acc;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -410,127 +447,80 @@ __global__ __launch_bounds__(kThreads, 2) void linear_chunks(LinearRun run) {
             acc[r] = (seen ? acc[r] : 0.0f) * e;
         }
 #pragma unroll
-        for (int n2 = 0; n2 < TERMS; ++n2) {
-            T* p = &s.P[x.at][n2][Scores::at(x.query, x.key / 8) + x.key % 8];
+        for (int n = 0; n < TERMS; ++n) {
+            T* p = &s.P[STATES ? 0 : at][n][Scores::at(x.query, x.key / 8) + x.key % 8];
             if constexpr (sizeof(T) == 4) {
                 *reinterpret_cast<f32x4*>(p) = acc;
             } else {
                 const u32x2 y = {pair(acc[0], acc[1]), pair(acc[2], acc[3])};
                 *reinterpret_cast<u32x2*>(p) = y;
-                if (n2 + 1 < TERMS)
+                if (n + 1 < TERMS)
                     acc -= f32x4{__uint_as_float(y[0] << 16), __uint_as_float(y[0] & 0xffff0000u),
                                  __uint_as_float(y[1] << 16), __uint_as_float(y[1] & 0xffff0000u)};
             }
         }
     };
-
-    const auto key_place = [](int row, int col) { return Keys::piece(row, col); };
-    const auto value_place = [](int row, int col) { return row * L::kValue + col; };
-    // this half's queries for the product with the state, over all tokens, its own tiles first
-    constexpr bool kAhead = !STATES && !SPLIT && KD <= 128;      // read a phase ahead where registers hold them
-    Frag q[STATES ? 1 : KK][2 * OWN];
-    const int even = Keys::at(i, 4 * k0 + g) + 16 * half * Keys::kStride;
-    const int odd = Keys::at(i, 4 * k0 + g) - 16 * half * Keys::kStride;
-    const auto load_queries = [&](const T* tile) {
-#pragma unroll
-        for (int kk = 0; kk < KK; ++kk)
-#pragma unroll
-            for (int o = 0; o < 2 * OWN; ++o) {
-                const int it = RT == 2 ? o : o == 0 ? 0 : o == 1 ? 3 : o == 2 ? 1 : 2;     // ^ half
-                q[kk][o] = M::along(&tile[(it & 1 ? odd : even) + 16 * it * Keys::kStride + 32 * kk]);
-            }
-    };
-
-    if constexpr (!STATES) qr.fetch(tokens, tid);
-    kr.fetch(tokens, tid);
-    vr.fetch(tokens, tid);
-    fetch_decays(0);
-    f32x4 state[KK][2];
-    {
-        const float* p = job.state_in ? job.state_in + bh * job.in_head + seg * job.in_seg : nullptr;
-#pragma unroll
-        for (int kk = 0; kk < KK; ++kk)
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = 32 * (k0 + kk) + 8 * g + 4 * u + r;
-                    state[kk][u][r] = p && live && row < kd ? p[(int64_t)row * job.sk + (int64_t)(col + i) * job.sv] : 0.0f;
-                }
-    }
-    if (chunks > 0) {
+    // the first chunk's rows and decays, and the fetch of the second's
+    const auto prologue = [&] {
         if constexpr (!STATES) {
             // the score tiles right of the diagonal that a block of 32 keys reaches are zero throughout
             for (int e = tid; e < RT / 2 * 256; e += kThreads) {
-                const int col = 32 * (e / 256) + 16 + e % 16;
-                const int at = Scores::at(32 * (e / 256) + e % 256 / 16, col / 8) + col % 8;
+                const int c = 32 * (e / 256) + 16 + e % 16;
+                const int at = Scores::at(32 * (e / 256) + e % 256 / 16, c / 8) + c % 8;
 #pragma unroll
                 for (int n = 0; n < 2 * TERMS; ++n) s.P[n % 2][n / 2][at] = T(0);
             }
             qr.stage(s.Q[0], tid, key_place);
-        } else {
-            vr.stage(s.V[0], tid, value_place);
+            qr.fetch(tokens - C, tid);
         }
         kr.stage(s.K[0], tid, key_place);
+        kr.fetch(tokens - C, tid);
+        if constexpr (L::kEarly) {
+            vr.stage(s.V[0], tid, value_place);
+            vr.fetch(tokens - C, tid);
+        }
         decays(0);
         fetch_decays(kWaves);
-        if constexpr (STATES) vr.fetch(tokens - C, tid);
-        else qr.fetch(tokens - C, tid);
-        kr.fetch(tokens - C, tid);
         lds_barrier();
-        if constexpr (!STATES) {
-            for (int idx = wave; idx < TILES; idx += kWaves) {
-                Score x;
-                tile_start(x, 0, 0, idx);
-                tile_multiply(x);
-                tile_finish(x);
-            }
-            if constexpr (kAhead) load_queries(s.Q[0]);
-            lds_barrier();
-        }
-    }
+    };
 
-    // the outputs' places: row 16 own + i of this half's tiles, four columns from `col` on
-    const bool wide = sizeof(T) == 4 || held(job.out_f32);
-    const int esize = wide ? 4 : 2;
-    int own[OWN];
-    uint32_t out_at[OWN], dot_at[OWN];
-    char* out_base = nullptr;
-    const char* dot_base = nullptr;
-    float* dots = nullptr;
-    int out_step = 0, dot_step = 0;
-    if constexpr (!STATES) {
+    if (keeps) {
+        f32x4 state[KK][2];
+        {
+            const float* p = job.state_in ? job.state_in + bh * job.in_head + seg * job.in_seg : nullptr;
 #pragma unroll
-        for (int o = 0; o < OWN; ++o) {
-            own[o] = RT == 2 ? half : o == 0 ? half : 3 - half;      // 0 and 3, or 1 and 2: three blocks of keys each
-            const int row = 16 * own[o] + i, t = rev ? C - 1 - row : row;
-            out_at[o] = live ? (uint32_t)((t * (int)run.H * vd + 4 * g) * esize) : kNoOffset;
-            if constexpr (kDots) dot_at[o] = live ? (uint32_t)((t * (int)job.dot_row + 4 * g) * (int)sizeof(T)) : kNoOffset;
+            for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int row = 32 * kk + 8 * g + 4 * u + r;
+                        state[kk][u][r] =
+                            p && live && row < kd ? p[(int64_t)row * job.sk + (int64_t)(col + i) * job.sv] : 0.0f;
+                    }
         }
-        out_base = static_cast<char*>(job.out) + (((b * run.L + token0) * run.H + h) * vd + col) * esize;
-        out_step = (rev ? -C : C) * (int)run.H * vd * esize;
-        if (kDots && job.dots) {
-            dot_base = static_cast<const char*>(job.dot_with) +
-                       ((b * run.L + token0) * job.dot_row + (int64_t)(h / job.dot_per) * vd + col) * (int)sizeof(T);
-            dot_step = (rev ? -C : C) * (int)job.dot_row * (int)sizeof(T);
-            dots = job.dots + ((int64_t)(tile * kGroups + group) * run.B * run.H + bh) * run.L + token0;
-        }
-    }
-
-    int slot = 0, left = tokens, until_decays = kWaves - 1;  // left: tokens from this chunk on
-    const auto step = [&](auto parity, int c) {
-        constexpr int now = decltype(parity)::value, next = now ^ 1;
-        const int next_slot = slot + 1 == kDecays ? 0 : slot + 1;
-        f32x4 out[OWN], theirs[OWN];
-        Frag k[KB][KK][2], p[OWN][KB][TERMS];
-        const auto load_keys = [&] {
+        // operands in groups of up to 64 registers; the queries' are free when the keys' are read
+        constexpr int REGS = sizeof(T) == 2 ? 4 : 8;
+        constexpr int QREGS = KD == 256 ? 32 : 64;
+        constexpr int GQ = KK * RT * REGS <= QREGS ? KK : QREGS / (RT * REGS);
+        constexpr int KREGS = KD == 256 ? 16 : 32;
+        constexpr int GK = KK * 2 * KB * REGS <= KREGS ? KK : KREGS / (2 * KB * REGS);
+        Frag q[STATES ? 1 : GQ][RT], k[KB][GK][2];
+        const int along = Keys::at(i, g);
+        const auto load_queries = [&](const T* tile, int k0) {
+#pragma unroll
+            for (int kk = 0; kk < GQ; ++kk)
+#pragma unroll
+                for (int it = 0; it < RT; ++it)
+                    if (!STATES) q[kk][it] = M::along(&tile[along + 16 * it * Keys::kStride + 32 * (k0 + kk)]);
+        };
+        const auto load_keys = [&](const T* tile, int k0) {
 #pragma unroll
             for (int b2 = 0; b2 < KB; ++b2)
 #pragma unroll
-                for (int kk = 0; kk < KK; ++kk)
+                for (int kk = 0; kk < GK; ++kk)
 #pragma unroll
                     for (int w = 0; w < 2; ++w) {
-                        const T* tile = s.K[now];
                         const int row = 32 * b2 + 8 * g, c8 = 4 * (k0 + kk);
                         if constexpr (sizeof(T) == 2)
                             k[b2][kk][w] = M::down(&tile[Keys::at(row + i / 4, c8 + i % 4) + 4 * w],
@@ -539,204 +529,311 @@ __global__ __launch_bounds__(kThreads, 2) void linear_chunks(LinearRun run) {
                             k[b2][kk][w] = M::down(&tile[Keys::at(row, c8 + i / 4) + 4 * w + i % 4], Keys::kStride);
                     }
         };
-        if constexpr (!STATES) {
-            // the entering state's part of the outputs, over this half's key rows
-            if constexpr (kAhead) load_keys();
-            else load_queries(s.Q[now]);
-            issue_point();
-            vr.stage(s.V[0], tid, value_place);
-            qr.stage(s.Q[next], tid, key_place);
-            kr.stage(s.K[next], tid, key_place);
-            qr.fetch(left - 2 * C, tid);
-            kr.fetch(left - 2 * C, tid);
-            vr.fetch(left - C, tid);
+        if (chunks > 0) prologue();
+        const auto step = [&](auto parity, int c) {
+            constexpr int now = decltype(parity)::value, next = now ^ 1;
+            const T* V = s.V[L::kEarly ? now : 0];
+            Frag v[KB];
+            f32x4 u[KB][2];
+            const auto load_values = [&] {
 #pragma unroll
-            for (int o = 0; o < OWN; ++o) out[o] = theirs[o] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                for (int b2 = 0; b2 < KB; ++b2) {
+                    const T* at = &V[(32 * b2 + 8 * g) * L::kValue + 16 * group];
+                    if constexpr (sizeof(T) == 2)
+                        v[b2] = M::down(at + i / 4 * L::kValue + 4 * (i % 4), at + (4 + i / 4) * L::kValue + 4 * (i % 4));
+                    else
+                        v[b2] = M::down(at + i, L::kValue);
+                    u[b2][0] = *reinterpret_cast<const f32x4*>(&s.until[slot][32 * b2 + 8 * g]);
+                    u[b2][1] = *reinterpret_cast<const f32x4*>(&s.until[slot][32 * b2 + 8 * g + 4]);
+                }
+            };
+            Frag w[KB][Terms<T, 3>::kN];                     // the values, decayed to the chunk's end
+            const auto decay_values = [&] {
 #pragma unroll
-            for (int kk = 0; kk < KK; ++kk) {
-                const Terms<T, TERMS> x(__builtin_shufflevector(state[kk][0], state[kk][1], 0, 1, 2, 3, 4, 5, 6, 7));
+                for (int b2 = 0; b2 < KB; ++b2) {
+                    const Terms<T, 3> x(M::widen(v[b2]) * __builtin_shufflevector(u[b2][0], u[b2][1], 0, 1, 2, 3, 4, 5, 6, 7));
 #pragma unroll
-                for (int n2 = 0; n2 < TERMS; ++n2)
-#pragma unroll
-                    for (int o = 0; o < OWN; ++o) {
-                        out[o] = M::mma(x.term[n2], q[kk][o], out[o]);
-                        theirs[o] = M::mma(x.term[n2], q[kk][OWN + o], theirs[o]);
-                    }
+                    for (int n = 0; n < Terms<T, 3>::kN; ++n) w[b2][n] = x.term[n];
+                }
+            };
+            if constexpr (!STATES) {
+                load_queries(s.Q[now], 0);
+                if constexpr (L::kEarly) load_values();
+                issue_point();
             }
-        } else {
-            vr.stage(s.V[next], tid, value_place);
-            kr.stage(s.K[next], tid, key_place);
-            kr.fetch(left - 2 * C, tid);
-            vr.fetch(left - 2 * C, tid);
-        }
-        if (until_decays == 0) {                             // the next chunk is the first whose decays are not there
-            decays(c + 1);
-            fetch_decays(c + 1 + kWaves);
-            until_decays = kWaves;
-        }
-        --until_decays;
-        if constexpr (!STATES) {
+            stage(next);
+            fetch();
+            if constexpr (!STATES) {
+                f32x4 out[RT];
 #pragma unroll
-            for (int o = 0; o < OWN; ++o) s.other[(wave * OWN + o) * 64 + lane] = theirs[o];
-            lds_barrier();   // the parts of the other half, this chunk's values, the next one's keys and queries are there
+                for (int it = 0; it < RT; ++it) out[it] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int k0 = 0; k0 < KK; k0 += GQ) {
+                    if (k0 > 0) {
+                        load_queries(s.Q[now], k0);
+                        issue_point();
+                    }
+#pragma unroll
+                    for (int kk = 0; kk < GQ; ++kk) {
+                        const Terms<T, TERMS> x(__builtin_shufflevector(state[k0 + kk][0], state[k0 + kk][1],
+                                                                        0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+                        for (int n = 0; n < TERMS; ++n)
+#pragma unroll
+                            for (int it = 0; it < RT; ++it) out[it] = M::mma(x.term[n], q[kk][it], out[it]);
+                    }
+                }
+                load_keys(s.K[now], 0);
+                issue_point();
+                if constexpr (L::kEarly) decay_values();
+#pragma unroll
+                for (int it = 0; it < RT; ++it) s.through[(group * RT + it) * 64 + lane] = out[it];
+            }
+            more_decays(c);
+            if constexpr (!STATES) lds_barrier();
+
+            if constexpr (STATES || !L::kEarly) load_values();
+            const float decay = s.whole[slot];
+            if constexpr (STATES) load_keys(s.K[now], 0);
+            issue_point();
+            if constexpr (STATES || !L::kEarly) decay_values();
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk) state[kk][0] *= decay, state[kk][1] *= decay;
+#pragma unroll
+            for (int k0 = 0; k0 < KK; k0 += GK) {
+                if (k0 > 0) {
+                    load_keys(s.K[now], k0);
+                    issue_point();
+                }
+#pragma unroll
+                for (int b2 = 0; b2 < KB; ++b2)
+#pragma unroll
+                    for (int n = 0; n < Terms<T, 3>::kN; ++n)
+#pragma unroll
+                        for (int kk = 0; kk < GK; ++kk)
+#pragma unroll
+                            for (int x = 0; x < 2; ++x)
+                                state[k0 + kk][x] = M::mma(k[b2][kk][x], w[b2][n], state[k0 + kk][x]);
+            }
+            if (!STATES && TILES > 2 * kGroups && 2 * kGroups + group < TILES) {
+                Score x;
+                start(x, next, next_of(slot), 2 * kGroups + group);
+                issue_point();
+                multiply(x, next);
+                finish(x, next);
+            }
+            lds_barrier();
+            slot = next_of(slot);
+            left -= C;
+        };
+        for (int c = 0; c < chunks; c += 2) {
+            step(std::integral_constant<int, 0>{}, c);
+            if (c + 1 < chunks) step(std::integral_constant<int, 1>{}, c + 1);
         }
 
-        // the next chunk's scores; the other operands are on their way meanwhile
-        Score x;
-        const bool scores = !STATES && (TILES >= kWaves || wave < TILES);
-        const T* V = s.V[STATES ? now : 0];
-        Frag v[KB];
-        f32x4 u[KB][2], theirs_for[OWN];
-        float since[OWN];
-        if (scores) tile_start(x, next, next_slot, wave);
-        issue_point();
-        if (scores) tile_multiply(x);
-#pragma unroll
-        for (int b2 = 0; b2 < KB; ++b2) {
-            const T* at = &V[(32 * b2 + 8 * g) * L::kValue + 16 * group];
-            if constexpr (sizeof(T) == 2)
-                v[b2] = M::down(at + i / 4 * L::kValue + 4 * (i % 4), at + (4 + i / 4) * L::kValue + 4 * (i % 4));
-            else
-                v[b2] = M::down(at + i, L::kValue);
-            u[b2][0] = *reinterpret_cast<const f32x4*>(&s.until[slot][32 * b2 + 8 * g]);
-            u[b2][1] = *reinterpret_cast<const f32x4*>(&s.until[slot][32 * b2 + 8 * g + 4]);
-        }
-        const float decay = s.whole[slot];
-        if constexpr (!kAhead) load_keys();
-        if constexpr (!STATES) {
-#pragma unroll
-            for (int o = 0; o < OWN; ++o) {
-                theirs_for[o] = s.other[((wave ^ kGroups) * OWN + o) * 64 + lane];
-                since[o] = s.hi[slot][16 * own[o] + i];
+        float* p = nullptr;
+        float by = 1.0f;
+        if constexpr (STATES) {
+            p = run.seg_state[blockIdx.y] + unit * kd * vd;
+        } else if (job.state_out && seg == (rev ? 0 : run.segments - 1)) {
+            p = job.state_out + bh * job.out_head;
+            if (job.decay_out && len > 0) {
+                const float x = gb[0] * kLog2e;
+                by = fast_exp2(x < kMinLog2 ? kMinLog2 : x);
             }
         }
-        issue_point();
-        if (scores) tile_finish(x);
-        if (!STATES && TILES > kWaves && wave + kWaves < TILES) {
-            tile_start(x, next, next_slot, wave + kWaves);
-            tile_multiply(x);
-            tile_finish(x);
+        if (p && live) {
+            const int64_t sk = STATES ? vd : job.sk, sv = STATES ? 1 : job.sv;
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int row = 32 * kk + 8 * g + 4 * u + r;
+                        if (row < kd) p[row * sk + (col + i) * sv] = state[kk][u][r] * by;
+                    }
         }
-        if constexpr (!STATES) {
+    } else {
+        // this wavefront's tiles of a chunk: group, group + 4, all on their way together (the state's team
+        // takes what is left; of the first chunk this one does)
+        const auto scores = [&](auto most, int at, int slot) {
+            constexpr int MOST = decltype(most)::value;
+            Score x[MOST];
 #pragma unroll
-            for (int o = 0; o < OWN; ++o)
-#pragma unroll
-                for (int b2 = 0; b2 <= o; ++b2)
-#pragma unroll
-                    for (int n2 = 0; n2 < TERMS; ++n2)
-                        p[o][b2][n2] = M::along(&s.P[now][n2][Scores::at(16 * own[o] + i, 4 * b2 + g)]);
-            if constexpr (kAhead) load_queries(s.Q[next]);
+            for (int m = 0; m < MOST; ++m)
+                if (group + kGroups * m < TILES) start(x[m], at, slot, group + kGroups * m);
             issue_point();
-        }
 #pragma unroll
-        for (int kk = 0; kk < KK; ++kk) state[kk][0] *= decay, state[kk][1] *= decay;
+            for (int m = 0; m < MOST; ++m)
+                if (group + kGroups * m < TILES) multiply(x[m], at);
 #pragma unroll
-        for (int b2 = 0; b2 < KB; ++b2) {
-            const Terms<T, 3> w(M::widen(v[b2]) * __builtin_shufflevector(u[b2][0], u[b2][1], 0, 1, 2, 3, 4, 5, 6, 7));
-#pragma unroll
-            for (int n2 = 0; n2 < Terms<T, 3>::kN; ++n2)
-#pragma unroll
-                for (int kk = 0; kk < KK; ++kk)
-#pragma unroll
-                    for (int w2 = 0; w2 < 2; ++w2) state[kk][w2] = M::mma(k[b2][kk][w2], w.term[n2], state[kk][w2]);
-        }
+            for (int m = 0; m < MOST; ++m)
+                if (group + kGroups * m < TILES) finish(x[m], at);
+        };
+
+        // the outputs' places: row 16 it + i, four columns from `col` on
+        const bool wide = sizeof(T) == 4 || held(job.out_f32);
+        const int esize = wide ? 4 : 2;
+        uint32_t out_at[RT], dot_at[RT];
+        char* out_base = nullptr;
+        const char* dot_base = nullptr;
+        float* dots = nullptr;
+        int out_step = 0, dot_step = 0;
         if constexpr (!STATES) {
+#pragma unroll
+            for (int it = 0; it < RT; ++it) {
+                const int row = 16 * it + i, t = rev ? C - 1 - row : row;
+                out_at[it] = live ? (uint32_t)((t * (int)run.H * vd + 4 * g) * esize) : kNoOffset;
+                if constexpr (kDots)
+                    dot_at[it] = live ? (uint32_t)((t * (int)job.dot_row + 4 * g) * (int)sizeof(T)) : kNoOffset;
+            }
+            out_base = static_cast<char*>(job.out) + (((b * run.L + token0) * run.H + h) * vd + col) * esize;
+            out_step = (rev ? -C : C) * (int)run.H * vd * esize;
+            if (kDots && job.dots) {
+                dot_base = static_cast<const char*>(job.dot_with) +
+                           ((b * run.L + token0) * job.dot_row + (int64_t)(h / job.dot_per) * vd + col) * (int)sizeof(T);
+                dot_step = (rev ? -C : C) * (int)job.dot_row * (int)sizeof(T);
+                dots = job.dots + ((int64_t)(tile * kGroups + group) * run.B * run.H + bh) * run.L + token0;
+            }
+        }
+
+        using Two = std::integral_constant<int, (TILES < 2 * kGroups ? TILES + kGroups - 1 : 2 * kGroups) / kGroups>;
+        if (chunks > 0) {
+            prologue();
+            if constexpr (!STATES) scores(std::integral_constant<int, (TILES + kGroups - 1) / kGroups>{}, 0, 0);
+        }
+        // A chunk's outputs are stored after the next one's rows are staged, and before the fetch behind
+        // those: loads and stores are waited for in order, and the staging waits for the loads.
+        f32x4 out[RT];
+        float dot[RT];
+        const auto store = [&](int rows) {
             const __amdgpu_buffer_rsrc_t to_out = make_rsrc(out_base, kRecords);
             out_base += out_step;
 #pragma unroll
-            for (int o = 0; o < OWN; ++o) out[o] = (out[o] + theirs_for[o]) * (fast_exp2(since[o]) * outer);
-#pragma unroll
-            for (int b2 = 0; b2 < KB; ++b2)
-#pragma unroll
-                for (int n2 = 0; n2 < TERMS; ++n2)
-#pragma unroll
-                    for (int o = b2; o < OWN; ++o) out[o] = M::mma(v[b2], p[o][b2][n2], out[o]);
-#pragma unroll
-            for (int o = 0; o < OWN; ++o) {
-                const int row = 16 * own[o] + i;
-                const f32x4 y = out[o];
-                const int at = (int)(row < left ? out_at[o] : kNoOffset);
+            for (int it = 0; it < RT; ++it) {
+                const f32x4 y = out[it];
+                const int at = (int)(16 * it + i < rows ? out_at[it] : kNoOffset);
                 if (wide)
                     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y), to_out, at, 0, 0);
                 else
                     __builtin_amdgcn_raw_buffer_store_b64(u32x2{pair(y[0], y[1]), pair(y[2], y[3])}, to_out, at, 0, 0);
             }
             if (kDots && dots) {
-                const __amdgpu_buffer_rsrc_t with = make_rsrc(dot_base, kRecords);
-                dot_base += dot_step;
 #pragma unroll
-                for (int o = 0; o < OWN; ++o) {
-                    const int row = 16 * own[o] + i;
-                    const int at = (int)(row < left ? dot_at[o] : kNoOffset);
-                    f32x4 y;
-                    if constexpr (sizeof(T) == 4) {
-                        y = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(with, at, 0, 0));
-                    } else {
-                        const u32x2 z = __builtin_amdgcn_raw_buffer_load_b64(with, at, 0, 0);
-                        y = f32x4{__uint_as_float(z[0] << 16), __uint_as_float(z[0] & 0xffff0000u),
-                                  __uint_as_float(z[1] << 16), __uint_as_float(z[1] & 0xffff0000u)};
-                    }
-                    float sum = fmaf(out[o][3], y[3], fmaf(out[o][2], y[2], fmaf(out[o][1], y[1], out[o][0] * y[0])));
-                    sum += __shfl_xor(sum, 16);
-                    sum += __shfl_xor(sum, 32);
-                    if (g == 0 && row < left && live) dots[rev ? C - 1 - row : row] = sum;
+                for (int it = 0; it < RT; ++it) {
+                    const int row = 16 * it + i;
+                    if (g == 0 && row < rows && live) dots[rev ? C - 1 - row : row] = dot[it];
                 }
                 dots += rev ? -C : C;
             }
-        }
-        lds_barrier();                                       // the next chunk's scores are there; this one's rows are free
-        slot = next_slot;
-        left -= C;
-    };
-    for (int c = 0; c < chunks; c += 2) {
-        step(std::integral_constant<int, 0>{}, c);
-        if (c + 1 < chunks) step(std::integral_constant<int, 1>{}, c + 1);
-    }
-    if constexpr (STATES) {                                  // each wavefront has summed the chunks that it formed
-        if (lane == 0) s.whole_log2[wave] = seg_decay;
-        lds_barrier();
-    }
+        };
+        const auto step = [&](auto parity, int c) {
+            constexpr int now = decltype(parity)::value, next = now ^ 1;
+            if constexpr (STATES) {
+                stage(next);
+                fetch();
+                more_decays(c);
+            } else {
+                stage(next);
+                issue_point();
+                if (c > 0) store(left + C);
+                u32x4 with[RT];                              // what the outputs' dot products are taken with
+                if (kDots && dots) {
+                    const __amdgpu_buffer_rsrc_t r = make_rsrc(dot_base, kRecords);
+                    dot_base += dot_step;
+#pragma unroll
+                    for (int it = 0; it < RT; ++it) {
+                        const int at = (int)(16 * it + i < left ? dot_at[it] : kNoOffset);
+                        if constexpr (sizeof(T) == 4) {
+                            with[it] = __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0);
+                        } else {
+                            const u32x2 z = __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, 0);
+                            with[it] = u32x4{z[0], z[1], 0, 0};
+                        }
+                    }
+                }
+                issue_point();
+                fetch();
+                more_decays(c);
+                lds_barrier();   // the state's part, this chunk's values and scores, the next one's rows are there
 
-    if constexpr (!STATES) {
-        if (job.zero_tail) {
+                scores(Two{}, next, next_of(slot));
+                Frag v[KB], p[RT][KB][TERMS];
+                float since[RT];
+#pragma unroll
+                for (int it = 0; it < RT; ++it) {
+                    out[it] = s.through[(group * RT + it) * 64 + lane];
+                    since[it] = s.hi[slot][16 * it + i];
+                }
+#pragma unroll
+                for (int b2 = 0; b2 < KB; ++b2) {
+                    const T* at = &s.V[L::kEarly ? now : 0][(32 * b2 + 8 * g) * L::kValue + 16 * group];
+                    if constexpr (sizeof(T) == 2)
+                        v[b2] = M::down(at + i / 4 * L::kValue + 4 * (i % 4), at + (4 + i / 4) * L::kValue + 4 * (i % 4));
+                    else
+                        v[b2] = M::down(at + i, L::kValue);
+#pragma unroll
+                    for (int it = 2 * b2; it < RT; ++it)
+#pragma unroll
+                        for (int n = 0; n < TERMS; ++n)
+                            p[it][b2][n] = M::along(&s.P[now][n][Scores::at(16 * it + i, 4 * b2 + g)]);
+                }
+                issue_point();
+#pragma unroll
+                for (int it = 0; it < RT; ++it) out[it] *= fast_exp2(since[it]) * outer;
+#pragma unroll
+                for (int b2 = 0; b2 < KB; ++b2)
+#pragma unroll
+                    for (int n = 0; n < TERMS; ++n)
+#pragma unroll
+                        for (int it = 2 * b2; it < RT; ++it) out[it] = M::mma(v[b2], p[it][b2][n], out[it]);
+                if (kDots && dots) {
+#pragma unroll
+                    for (int it = 0; it < RT; ++it) {
+                        const u32x4 z = with[it];
+                        f32x4 y;
+                        if constexpr (sizeof(T) == 4)
+                            y = __builtin_bit_cast(f32x4, z);
+                        else
+                            y = f32x4{__uint_as_float(z[0] << 16), __uint_as_float(z[0] & 0xffff0000u),
+                                      __uint_as_float(z[1] << 16), __uint_as_float(z[1] & 0xffff0000u)};
+                        float sum = fmaf(out[it][3], y[3], fmaf(out[it][2], y[2], fmaf(out[it][1], y[1], out[it][0] * y[0])));
+                        sum += __shfl_xor(sum, 16);
+                        sum += __shfl_xor(sum, 32);
+                        dot[it] = sum;
+                    }
+                }
+            }
+            lds_barrier();                                   // the next chunk's scores are there; this one's rows are free
+            slot = next_of(slot);
+            left -= C;
+        };
+        for (int c = 0; c < chunks; c += 2) {
+            step(std::integral_constant<int, 0>{}, c);
+            if (c + 1 < chunks) step(std::integral_constant<int, 1>{}, c + 1);
+        }
+        if (!STATES && chunks > 0) store(left + C);
+        if (!STATES && job.zero_tail) {
             const int width = vd - col0 < linear::kColumns ? vd - col0 : linear::kColumns;
             const int64_t first = from > len ? from : len;
-            for (int64_t t = first + wave; t < last; t += kWaves) {
+            for (int64_t t = first + group; t < last; t += kGroups) {
                 const int64_t at = ((b * run.L + t) * run.H + h) * vd + col0 + lane;
                 if (lane < width) {
-                    if (sizeof(T) == 4 || job.out_f32) static_cast<float*>(job.out)[at] = 0.0f;
+                    if (wide) static_cast<float*>(job.out)[at] = 0.0f;
                     else static_cast<uint16_t*>(job.out)[at] = 0;
                 }
             }
         }
     }
-    float* p = nullptr;
-    float by = 1.0f;
-    if constexpr (STATES) {
-        p = run.seg_state[blockIdx.y] + unit * kd * vd;
-        if (tile == 0 && tid == 0) {
+    if constexpr (STATES) {                                  // each wavefront has summed the chunks that it formed
+        if (lane == 0) s.whole_log2[wave] = seg_decay;
+        lds_barrier();
+        if (tile == 0 && threadIdx.x == 0) {
             double all = 0.0;
             for (int w = 0; w < kWaves; ++w) all += s.whole_log2[w];
             run.seg_decay[blockIdx.y][unit] = (float)all;
         }
-    } else if (job.state_out && seg == (rev ? 0 : run.segments - 1)) {
-        p = job.state_out + bh * job.out_head;
-        if (job.decay_out && len > 0) {
-            const float x = gb[0] * kLog2e;
-            by = fast_exp2(x < kMinLog2 ? kMinLog2 : x);
-        }
-    }
-    if (p && live) {
-        const int64_t sk = STATES ? vd : job.sk, sv = STATES ? 1 : job.sv;
-#pragma unroll
-        for (int kk = 0; kk < KK; ++kk)
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = 32 * (k0 + kk) + 8 * g + 4 * u + r;
-                    if (row < kd) p[row * sk + (col + i) * sv] = state[kk][u][r] * by;
-                }
     }
 }
 

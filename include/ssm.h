@@ -634,7 +634,7 @@ int ssm_layer_norm_bwd(const void* x, int x_dtype, const void* dy, const float* 
  *                tokens (clamped to [0, L]); the padding is not read, o there is
  *                left untouched, h_last is the state after the row's last token
  *   Dk, Dv multiples of 16, at most 256; H a multiple of G, at most 2^14;
- *   B * H at most 2^21; L at most 2^31.
+ *   B * H at most 2^21; L at most 2^30.
  *
  * Tokens are taken in chunks (64 bf16, 32 fp32) as masked products on the
  * matrix cores, the fp32 state carried between them: an infinity or NaN in a

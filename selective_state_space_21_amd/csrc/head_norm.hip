@@ -310,8 +310,6 @@ template <typename T> hipError_t launch_type(const HeadNormArgs& a, bool backwar
 
 }  // namespace
 
-int64_t head_norm_groups(int64_t rows) { return rows < 1 ? 1 : rows < 1024 ? rows : 1024; }
-
 hipError_t launch_head_norm(const HeadNormArgs& a, hipStream_t stream) {
     if (a.rows == 0) return hipSuccess;
     return a.bf16 ? launch_type<uint16_t>(a, false, stream) : launch_type<float>(a, false, stream);

@@ -561,8 +561,10 @@ __global__ __launch_bounds__(kThreads, 2) void linear_chunks(LinearRun run) {
                 if constexpr (L::kEarly) load_values();
                 issue_point();
             }
-            stage(next);
-            fetch();
+            if constexpr (STATES) {
+                stage(next);
+                fetch();
+            }
             if constexpr (!STATES) {
                 f32x4 out[RT];
 #pragma unroll
@@ -585,9 +587,11 @@ __global__ __launch_bounds__(kThreads, 2) void linear_chunks(LinearRun run) {
                 }
                 load_keys(s.K[now], 0);
                 issue_point();
-                if constexpr (L::kEarly) decay_values();
+                stage(next);
+                fetch();
 #pragma unroll
                 for (int it = 0; it < RT; ++it) s.through[(group * RT + it) * 64 + lane] = out[it];
+                if constexpr (L::kEarly) decay_values();
             }
             more_decays(c);
             if constexpr (!STATES) lds_barrier();
@@ -598,22 +602,29 @@ __global__ __launch_bounds__(kThreads, 2) void linear_chunks(LinearRun run) {
             issue_point();
             if constexpr (STATES || !L::kEarly) decay_values();
 #pragma unroll
-            for (int kk = 0; kk < KK; ++kk) state[kk][0] *= decay, state[kk][1] *= decay;
-#pragma unroll
             for (int k0 = 0; k0 < KK; k0 += GK) {
                 if (k0 > 0) {
                     load_keys(s.K[now], k0);
                     issue_point();
                 }
+                // the chunk's terms are summed by themselves: one rounding at the state's size, not one a product
+                f32x4 add[GK][2];
+#pragma unroll
+                for (int kk = 0; kk < GK; ++kk) add[kk][0] = add[kk][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int b2 = 0; b2 < KB; ++b2)
 #pragma unroll
-                    for (int n = 0; n < Terms<T, 3>::kN; ++n)
+                    for (int n = Terms<T, 3>::kN - 1; n >= 0; --n)
 #pragma unroll
                         for (int kk = 0; kk < GK; ++kk)
 #pragma unroll
-                            for (int x = 0; x < 2; ++x)
-                                state[k0 + kk][x] = M::mma(k[b2][kk][x], w[b2][n], state[k0 + kk][x]);
+                            for (int x = 0; x < 2; ++x) add[kk][x] = M::mma(k[b2][kk][x], w[b2][n], add[kk][x]);
+#pragma unroll
+                for (int kk = 0; kk < GK; ++kk)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) state[k0 + kk][x][r] = fmaf(state[k0 + kk][x][r], decay, add[kk][x][r]);
             }
             if (!STATES && TILES > 2 * kGroups && 2 * kGroups + group < TILES) {
                 Score x;
@@ -1009,6 +1020,7 @@ hipError_t launch_linear_decay_grad(const LinearDecayGrad& d, hipStream_t stream
 
 hipError_t launch_linear_group_sum(const LinearGroupSum& s, hipStream_t stream) {
     const int64_t n = s.rows * s.G * (s.width / 4);
+    if (n == 0) return hipSuccess;
     linear_group_sum<<<dim3((unsigned)((n + 255) / 256)), 256, 0, stream>>>(s);
     return hipGetLastError();
 }

@@ -67,8 +67,8 @@ struct LinearPlan {
     int segments;
     int64_t seg_tokens;
 };
-LinearPlan plan_linear_fwd(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv, bool bf16);
-LinearPlan plan_linear_bwd(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv, bool bf16);
+LinearPlan plan_linear_fwd(int64_t B, int64_t L, int64_t H, int64_t Dv);
+LinearPlan plan_linear_bwd(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv);
 
 struct LinearArgs {
     const void* q;
@@ -99,9 +99,8 @@ struct LinearBwdArgs {
     float* dh0;
 };
 
-size_t linear_fwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv, bool bf16);
-size_t linear_bwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t G, int64_t Dk, int64_t Dv, bool bf16,
-                                  bool by_head);
+size_t linear_fwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv);
+size_t linear_bwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t G, int64_t Dk, int64_t Dv, bool by_head);
 hipError_t launch_linear_fwd(const LinearArgs& a, hipStream_t stream);
 hipError_t launch_linear_bwd(const LinearBwdArgs& a, hipStream_t stream);
 
@@ -202,8 +201,15 @@ struct SlotsArgs {
     int64_t layers, slots, slot_bytes, n;
 };
 constexpr int64_t kMaxMoves = 2048;
-// one launch takes the call's ranges
-bool slots_copy_fits(const SlotsArgs& a);
+constexpr int kSlotsHeld = 16;   // units that a thread holds
+// How a call is cut: a workgroup's range as wide as its registers hold for all
+// entries, at most a unit a thread.
+struct SlotsCut {
+    int unit, threads, W;        // bytes; a workgroup's; units of a range, a power of two
+    int64_t ranges;              // of a slot
+};
+SlotsCut slots_cut(const SlotsArgs& a);
+bool slots_copy_fits(const SlotsArgs& a);   // one launch takes the ranges
 hipError_t launch_slots_copy(const SlotsArgs& a, hipStream_t stream);
 
 }  // namespace ssm

@@ -1,5 +1,6 @@
-// Host planning of linear attention: how sequences are cut, what the
-// workspaces hold, and the order of launches behind the two calls.
+// Host planning of linear attention (how sequences are cut, what the workspaces
+// hold, and the order of launches behind the two calls), of the head norm's
+// backward and of the moves between slots.
 #include <hip/hip_runtime.h>
 
 #include <math.h>
@@ -15,34 +16,44 @@ namespace {
 int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 int64_t tiles_of(int64_t width) { return (width + linear::kColumns - 1) / linear::kColumns; }
 
-// Workgroups that fill the GPU: two on each of its 256 CUs.
-constexpr int64_t kFill = 512;
-// Shortest segment worth a launch of its own for its state.
-constexpr int64_t kMinSegment = 256;
+// Workgroups that run at once: their LDS leaves room for one on a CU.
+constexpr int64_t kAtOnce = 256;
 // Forced segments: what joins them, and their workgroups, go out as one launch.
 constexpr int64_t kMostCut = int64_t(1) << 14;
 
-// `groups` workgroups a segment
-LinearPlan plan(int64_t groups, int64_t L) {
-    LinearPlan p{1, up(L > 0 ? L : 1, linear::kSegment)};
-    int64_t want = (kFill + groups - 1) / groups;
+// Where sequences are cut.  `units` workgroups a segment make the outputs,
+// `states` make the segments' states first, in rounds of kAtOnce.  In tokens
+// of a workgroup's time (30-45 ns each): a round lasts its segment's length, a
+// round of states 0.3 of it, what a cut costs in launches about 300, the
+// joining of a segment's states about 20.  Measured, forward B=1 L=8192 H=16
+// 128x128 bf16: 286 us whole, 123 in 4, 80 in 8 (one round), 106 in 12, 96 in
+// 16; backward 573, 298, 263, 292, 299; forward B=1 L=512 H=8 64x64: 20 us
+// whole, 24 in 4.  A cut has to save 5%.
+LinearPlan plan(int64_t units, int64_t states, int64_t L) {
+    LinearPlan best{1, up(L > 0 ? L : 1, linear::kSegment)};
+    const auto cut = [L](int64_t n) {
+        LinearPlan p;
+        p.seg_tokens = up((L + n - 1) / n, linear::kSegment);
+        p.segments = (int)((L + p.seg_tokens - 1) / p.seg_tokens);
+        return p;
+    };
+    if (units > kMostCut || L <= linear::kSegment) return best;
     if (const char* e = getenv("SSM_LINEAR_SEGMENTS")) {
         const long n = strtol(e, nullptr, 10);
-        if (n >= 1 && n <= 256 && groups <= kMostCut) {
-            want = n;
-            if (want > 1) {
-                p.seg_tokens = up((L + want - 1) / want, linear::kSegment);
-                if (p.seg_tokens < linear::kSegment) p.seg_tokens = linear::kSegment;
-                p.segments = L > 0 ? (int)((L + p.seg_tokens - 1) / p.seg_tokens) : 1;
-            }
-            return p;
+        if (n >= 1 && n <= 256) return n > 1 ? cut(n) : best;
+    }
+    const auto rounds = [](int64_t n) { return (double)((n + kAtOnce - 1) / kAtOnce); };
+    double least = 0.95 * rounds(units) * (double)L;
+    for (int64_t n = 2; n <= 256 && n * linear::kSegment <= L; ++n) {
+        const LinearPlan p = cut(n);
+        const double cost = (rounds(units * p.segments) + 0.3 * rounds(states * p.segments)) * (double)p.seg_tokens +
+                            300.0 + 20.0 * p.segments;
+        if (cost < least) {
+            least = cost;
+            best = p;
         }
     }
-    if (groups * 2 >= kFill || L < 2 * kMinSegment) return p;
-    if (want > L / kMinSegment) want = L / kMinSegment;
-    p.seg_tokens = up((L + want - 1) / want, linear::kSegment);
-    p.segments = (int)((L + p.seg_tokens - 1) / p.seg_tokens);
-    return p;
+    return best;
 }
 
 // Pieces of a workspace, each on a 256-byte border.
@@ -133,22 +144,21 @@ int pad(int64_t width) { return width <= 64 ? 64 : width <= 128 ? 128 : 256; }
 
 }  // namespace
 
-LinearPlan plan_linear_fwd(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv, bool bf16) {
-    (void)Dk;
-    return plan(B * H * tiles_of(Dv), L);
+LinearPlan plan_linear_fwd(int64_t B, int64_t L, int64_t H, int64_t Dv) {
+    return plan(B * H * tiles_of(Dv), B * H * tiles_of(Dv), L);
 }
 
-LinearPlan plan_linear_bwd(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv, bool bf16) {
-    return plan(B * H * (2 * tiles_of(Dk) + tiles_of(Dv)), L);
+LinearPlan plan_linear_bwd(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv) {
+    return plan(B * H * (2 * tiles_of(Dk) + tiles_of(Dv)), 2 * B * H * tiles_of(Dv), L);
 }
 
-size_t linear_fwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv, bool bf16) {
-    return FwdSpace(nullptr, plan_linear_fwd(B, L, H, Dk, Dv, bf16), B, H, Dk * Dv).bytes;
+size_t linear_fwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv) {
+    return FwdSpace(nullptr, plan_linear_fwd(B, L, H, Dv), B, H, Dk * Dv).bytes;
 }
 
-size_t linear_bwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t G, int64_t Dk, int64_t Dv, bool bf16,
+size_t linear_bwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t G, int64_t Dk, int64_t Dv,
                                   bool by_head) {
-    return BwdSpace(nullptr, plan_linear_bwd(B, L, H, Dk, Dv, bf16), B, L, H, G, Dk, Dv, by_head).bytes;
+    return BwdSpace(nullptr, plan_linear_bwd(B, L, H, Dk, Dv), B, L, H, G, Dk, Dv, by_head).bytes;
 }
 
 hipError_t launch_linear_fwd(const LinearArgs& a, hipStream_t stream) {
@@ -236,12 +246,13 @@ hipError_t launch_linear_bwd(const LinearBwdArgs& a, hipStream_t stream) {
         dk.dot_with = f.k; dk.dot_row = f.k_row; dk.dot_per = per; dk.dots = ws.dot_k;
         dq.state_out = ws.S_last;
     }
+    // dv is of the inputs' type alone: it needs no split operands, nor a launch with those that do
     r.job[0] = dq; r.job[1] = dk; r.job[2] = dv;
-    r.jobs = pad(f.Dk) == pad(f.Dv) ? 3 : 2;
+    r.jobs = !r.split && pad(f.Dk) == pad(f.Dv) ? 3 : 2;
     if ((e = launch_linear_run(r, false, stream)) != hipSuccess) return e;
     if (r.jobs == 2) {
         r.jobs = 1;
-        r.split = 0;                                         // dv is of the inputs' type alone
+        r.split = 0;
         r.job[0] = dv;
         if ((e = launch_linear_run(r, false, stream)) != hipSuccess) return e;
     }
@@ -271,6 +282,24 @@ hipError_t launch_linear_bwd(const LinearBwdArgs& a, hipStream_t stream) {
         }
     }
     return hipSuccess;
+}
+
+int64_t head_norm_groups(int64_t rows) { return rows < 1 ? 1 : rows < 1024 ? rows : 1024; }
+
+SlotsCut slots_cut(const SlotsArgs& a) {
+    const uint64_t at = reinterpret_cast<uintptr_t>(a.pool) | (uint64_t)a.slot_bytes;
+    SlotsCut c;
+    c.unit = at % 16 == 0 ? 16 : at % 4 == 0 ? 4 : 1;
+    c.threads = a.n <= 1024 ? 256 : 1024;
+    c.W = c.threads;
+    while ((int64_t)c.W * a.n > (int64_t)kSlotsHeld * c.threads) c.W /= 2;
+    c.ranges = (a.slot_bytes / c.unit + c.W - 1) / c.W;
+    return c;
+}
+
+bool slots_copy_fits(const SlotsArgs& a) {
+    const SlotsCut c = slots_cut(a);
+    return c.ranges <= kMaxItems / c.threads / a.layers;
 }
 
 }  // namespace ssm

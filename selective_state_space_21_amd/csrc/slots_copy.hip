@@ -21,7 +21,7 @@ namespace {
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kHeld = 16;                                    // units that a thread holds
+constexpr int kHeld = kSlotsHeld;                            // units that a thread holds
 
 __host__ __device__ constexpr int table_size(int n) {
     int size = 64;
@@ -84,25 +84,7 @@ __global__ __launch_bounds__(1024) void slots_copy(SlotsArgs a, int W, int64_t r
         if (target[m] >= 0) base[target[m]] = held[m];
 }
 
-// How a call is cut: a workgroup's range as wide as its registers hold for all
-// entries, at most a unit a thread.
-struct Cut {
-    int unit, threads, W;
-    int64_t ranges;
-};
-
-Cut cut_of(const SlotsArgs& a) {
-    const uint64_t at = reinterpret_cast<uintptr_t>(a.pool) | (uint64_t)a.slot_bytes;
-    Cut c;
-    c.unit = at % 16 == 0 ? 16 : at % 4 == 0 ? 4 : 1;
-    c.threads = a.n <= 1024 ? 256 : 1024;
-    c.W = c.threads;
-    while ((int64_t)c.W * a.n > (int64_t)kHeld * c.threads) c.W /= 2;
-    c.ranges = (a.slot_bytes / c.unit + c.W - 1) / c.W;
-    return c;
-}
-
-template <typename U> hipError_t launch_unit(const SlotsArgs& a, const Cut& c, hipStream_t stream) {
+template <typename U> hipError_t launch_unit(const SlotsArgs& a, const SlotsCut& c, hipStream_t stream) {
     const int size = table_size((int)a.n);
     const size_t lds = (size_t)(2 * a.n + 2 * size) * 4;
     slots_copy<U><<<dim3((unsigned)(c.ranges * a.layers)), c.threads, lds, stream>>>(a, c.W, c.ranges, size);
@@ -111,13 +93,8 @@ template <typename U> hipError_t launch_unit(const SlotsArgs& a, const Cut& c, h
 
 }  // namespace
 
-bool slots_copy_fits(const SlotsArgs& a) {
-    const Cut c = cut_of(a);
-    return c.ranges <= kMaxItems / c.threads / a.layers;
-}
-
 hipError_t launch_slots_copy(const SlotsArgs& a, hipStream_t stream) {
-    const Cut c = cut_of(a);
+    const SlotsCut c = slots_cut(a);
     if (c.unit == 16) return launch_unit<u32x4>(a, c, stream);
     if (c.unit == 4) return launch_unit<uint32_t>(a, c, stream);
     return launch_unit<uint8_t>(a, c, stream);

@@ -29,13 +29,10 @@ _DT = _args.DTYPES
 _ptr = _args.ptr
 
 
-def _rows(name, t, shape, dtype, device) -> int:
-    """Checks a tensor whose last two axes are dense; returns the elements
-    between its tokens (all axes before those two, in order)."""
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+def _row(name, t, shape, device) -> int:
+    """Checks the device and the layout of a tensor whose last two axes are
+    dense; returns the elements between its tokens (all axes before those
+    two, in order)."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor (got {t.device})")
     if t.device != device:
@@ -59,9 +56,28 @@ def _rows(name, t, shape, dtype, device) -> int:
     return heads * width if row is None else row
 
 
+def _check(device, parts, *specs):
+    """Types, shapes and dtypes of every argument first, then devices and
+    layout, as _args.check_args; `parts` may be parts of wider rows.  Returns
+    their elements between tokens."""
+    for name, t, shape, dtype in (*parts, *specs):
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+    rows = [_row(name, t, shape, device) for name, t, shape, _ in parts]
+    _args.check_args(device, *specs)
+    return rows
+
+
 def _sizes(q, v, lead, names):
     dt = _args.act_dtype("q", q)
-    _args.need(v=v)
+    if not isinstance(v, torch.Tensor):
+        raise TypeError("v must be a torch.Tensor")
     if q.dim() != lead + 2 or v.dim() != lead + 2:
         raise ValueError(f"q must be [{names}, G, Dk] and v [{names}, H, Dv]")
     if tuple(q.shape[:lead]) != tuple(v.shape[:lead]):
@@ -73,12 +89,10 @@ def _sizes(q, v, lead, names):
     return dt, q.device, G, Dk, H, Dv
 
 
-def _decay(log_decay, by_token, H, device):
+def _by_head(log_decay) -> bool:
     """The decays' shape tells their kind: [H], or one for each token and head."""
     _args.need(log_decay=log_decay)
-    by_head = log_decay.dim() == 1
-    _args.check_args(device, ("log_decay", log_decay, (H,) if by_head else by_token, _F32))
-    return by_head
+    return isinstance(log_decay, torch.Tensor) and log_decay.dim() == 1
 
 
 def _default_scale(scale, Dk) -> float:
@@ -122,11 +136,10 @@ def linear_attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_
     dt, dev, G, Dk, H, Dv = _sizes(q, v, 2, "B, L")
     Bt, L = q.shape[:2]
     _args.need(k=k)
-    rows = [_rows(n, t, s, dt, dev) for n, t, s in
-            (("q", q, (Bt, L, G, Dk)), ("k", k, (Bt, L, G, Dk)), ("v", v, (Bt, L, H, Dv)))]
-    by_head = _decay(log_decay, (Bt, L, H), H, dev)
-    _args.check_args(dev, ("h0", h0, (Bt, H, Dk, Dv), _F32), ("out", out, (Bt, L, H, Dv), dt),
-                     ("seq_lens", seq_lens, (Bt,), _I32))
+    by_head = _by_head(log_decay)
+    rows = _check(dev, (("q", q, (Bt, L, G, Dk), dt), ("k", k, (Bt, L, G, Dk), dt), ("v", v, (Bt, L, H, Dv), dt)),
+                  ("log_decay", log_decay, (H,) if by_head else (Bt, L, H), _F32), ("h0", h0, (Bt, H, Dk, Dv), _F32),
+                  ("out", out, (Bt, L, H, Dv), dt), ("seq_lens", seq_lens, (Bt,), _I32))
     lib = _native.load()
     need = int(lib.ssm_linear_attention_workspace_bytes(Bt, L, H, Dk, Dv, _DT[dt]))
     workspace, ws_bytes = _args.workspace(workspace, need, dev)
@@ -157,11 +170,11 @@ def linear_attention_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_
     dt, dev, G, Dk, H, Dv = _sizes(q, v, 2, "B, L")
     Bt, L = q.shape[:2]
     _args.need(k=k, do=do)
-    rows = [_rows(n, t, s, dt, dev) for n, t, s in
-            (("q", q, (Bt, L, G, Dk)), ("k", k, (Bt, L, G, Dk)), ("v", v, (Bt, L, H, Dv)))]
-    by_head = _decay(log_decay, (Bt, L, H), H, dev)
-    _args.check_args(dev, ("do", do, (Bt, L, H, Dv), dt), ("h0", h0, (Bt, H, Dk, Dv), _F32),
-                     ("dh_last", dh_last, (Bt, H, Dk, Dv), _F32), ("seq_lens", seq_lens, (Bt,), _I32))
+    by_head = _by_head(log_decay)
+    rows = _check(dev, (("q", q, (Bt, L, G, Dk), dt), ("k", k, (Bt, L, G, Dk), dt), ("v", v, (Bt, L, H, Dv), dt)),
+                  ("log_decay", log_decay, (H,) if by_head else (Bt, L, H), _F32), ("do", do, (Bt, L, H, Dv), dt),
+                  ("h0", h0, (Bt, H, Dk, Dv), _F32), ("dh_last", dh_last, (Bt, H, Dk, Dv), _F32),
+                  ("seq_lens", seq_lens, (Bt,), _I32))
     lib = _native.load()
     need = int(lib.ssm_linear_attention_bwd_workspace_bytes(Bt, L, H, G, Dk, Dv, int(by_head), _DT[dt]))
     workspace, ws_bytes = _args.workspace(workspace, need, dev)
@@ -197,14 +210,15 @@ def linear_state_update(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v
     dt, dev, G, Dk, H, Dv = _sizes(q, v, 1, "B")
     Bt = q.shape[0]
     _args.need(state=state, k=k)
-    rows = [_rows(n, t, s, dt, dev) for n, t, s in
-            (("q", q, (Bt, G, Dk)), ("k", k, (Bt, G, Dk)), ("v", v, (Bt, H, Dv)))]
-    by_head = _decay(log_decay, (Bt, H), H, dev)
+    if not isinstance(state, torch.Tensor):
+        raise TypeError("state must be a torch.Tensor")
+    by_head = _by_head(log_decay)
     if state.dim() != 4 or (slots is None and state.shape[0] < Bt):
         raise ValueError("state must be [n_slots, H, Dk, Dv], with a slot for each row")
     n = state.shape[0]
-    _args.check_args(dev, ("state", state, (n, H, Dk, Dv), _F32), ("slots", slots, (Bt,), _I32),
-                     ("out", out, (Bt, H, Dv), dt))
+    rows = _check(dev, (("q", q, (Bt, G, Dk), dt), ("k", k, (Bt, G, Dk), dt), ("v", v, (Bt, H, Dv), dt)),
+                  ("log_decay", log_decay, (H,) if by_head else (Bt, H), _F32), ("state", state, (n, H, Dk, Dv), _F32),
+                  ("slots", slots, (Bt,), _I32), ("out", out, (Bt, H, Dv), dt))
     o = out if out is not None else torch.empty((Bt, H, Dv), dtype=dt, device=dev)
     with _on(dev):
         rc = _native.load().ssm_linear_state_update(
@@ -214,7 +228,8 @@ def linear_state_update(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v
     return o
 
 
-def _norm_args(q, k, q_weight, k_weight, positions, inv_freq):
+def _norm_args(q, k, q_weight, k_weight, positions, inv_freq, *more):
+    """more: (name, tensor, 0 for queries or 1 for keys), dense tensors of their shapes."""
     dt = _args.act_dtype("q", q)
     _args.need(k=k)
     if q.dim() < 2 or k.dim() != q.dim():
@@ -224,14 +239,16 @@ def _norm_args(q, k, q_weight, k_weight, positions, inv_freq):
     rows = 1
     for size in lead:
         rows *= size
-    strides = [_rows("q", q, lead + (Hq, width), dt, dev), _rows("k", k, lead + (Hk, width), dt, dev)]
+    half = 0
     if inv_freq is not None:
         _args.need(positions=positions)
         if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
             raise ValueError("inv_freq must be [rotary / 2]")
-    half = 0 if inv_freq is None else inv_freq.shape[0]
-    _args.check_args(dev, ("q_weight", q_weight, (width,), _F32), ("k_weight", k_weight, (width,), _F32),
-                     ("positions", positions, lead, _I32), ("inv_freq", inv_freq, (half,), _F32))
+        half = inv_freq.shape[0]
+    shapes = (lead + (Hq, width), lead + (Hk, width))
+    strides = _check(dev, (("q", q, shapes[0], dt), ("k", k, shapes[1], dt)), ("q_weight", q_weight, (width,), _F32),
+                     ("k_weight", k_weight, (width,), _F32), ("positions", positions, lead, _I32),
+                     ("inv_freq", inv_freq, (half,), _F32), *((n, t, shapes[which], dt) for n, t, which in more))
     return dt, dev, lead, rows, strides, Hq, Hk, width, 2 * half
 
 
@@ -248,8 +265,8 @@ def qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.
     radians a position (none: no rotation).  Pairs are (p, p + rotary / 2), or
     (2p, 2p + 1) if interleaved.  Returns dense (q, k).
     """
-    dt, dev, lead, rows, strides, Hq, Hk, width, rotary = _norm_args(q, k, q_weight, k_weight, positions, inv_freq)
-    _args.check_args(dev, ("out_q", out_q, lead + (Hq, width), dt), ("out_k", out_k, lead + (Hk, width), dt))
+    dt, dev, lead, rows, strides, Hq, Hk, width, rotary = _norm_args(
+        q, k, q_weight, k_weight, positions, inv_freq, ("out_q", out_q, 0), ("out_k", out_k, 1))
     yq = out_q if out_q is not None else torch.empty(lead + (Hq, width), dtype=dt, device=dev)
     yk = out_k if out_k is not None else torch.empty(lead + (Hk, width), dtype=dt, device=dev)
     with _on(dev):
@@ -276,9 +293,9 @@ def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, dq_out: torch.Tensor, dk_
     (dense).  Returns a dict with dense dq, dk, and dq_weight, dk_weight
     [width] fp32 for the weights that were given.
     """
-    dt, dev, lead, rows, strides, Hq, Hk, width, rotary = _norm_args(q, k, q_weight, k_weight, positions, inv_freq)
     _args.need(dq_out=dq_out, dk_out=dk_out)
-    _args.check_args(dev, ("dq_out", dq_out, lead + (Hq, width), dt), ("dk_out", dk_out, lead + (Hk, width), dt))
+    dt, dev, lead, rows, strides, Hq, Hk, width, rotary = _norm_args(
+        q, k, q_weight, k_weight, positions, inv_freq, ("dq_out", dq_out, 0), ("dk_out", dk_out, 1))
     lib = _native.load()
     workspace, ws_bytes = _args.workspace(
         workspace, int(lib.ssm_qk_norm_rope_bwd_workspace_bytes(rows, width)), dev)
@@ -310,6 +327,8 @@ def state_slots_copy(pool: torch.Tensor, src: torch.Tensor, dst: torch.Tensor, d
     Returns the pool.
     """
     _args.need(pool=pool, src=src, dst=dst)
+    if not all(isinstance(t, torch.Tensor) for t in (pool, src, dst)):
+        raise TypeError("pool, src and dst must be torch.Tensors")
     if not -pool.dim() <= dim < pool.dim():
         raise ValueError(f"pool has no axis {dim}")
     dim %= pool.dim()

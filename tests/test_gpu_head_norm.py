@@ -1,0 +1,178 @@
+"""The norm of queries and keys with rotary positions on the GPU against the
+fp64 definition.  Allowances: a sum over the width passes width / 2 roundings
+of the squares' size, halved by the square root; the pair's rotation, the
+normalisation, and sine and cosine of a reduced angle add fewer than 24, all
+counted at 2^-23 of the pair's size; a bf16 output is off by half a step."""
+import pytest
+import torch
+
+import selective_state_space_21_amd as ssm
+from oracle import linear as O
+
+import _linear_bounds as Bd
+
+pytestmark = pytest.mark.gpu
+
+BF, F = torch.bfloat16, torch.float32
+
+
+def make(rows, Hq, Hk, width, rotary, dtype, seed=0, weights=True, far=False):
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g)                            # noqa: E731
+    t = dict(q=(2 * r(rows, Hq, width)).to(dtype), k=(0.1 * r(rows, Hk, width)).to(dtype),
+             q_weight=1 + 0.2 * r(width) if weights else None, k_weight=1 + 0.2 * r(width) if weights else None,
+             positions=torch.randint(-1000, 1000000 if far else 1000, (rows,), generator=g, dtype=torch.int32),
+             inv_freq=10000.0 ** (-torch.arange(rotary // 2) * 2.0 / rotary) if rotary else None)
+    if not rotary:
+        t["positions"] = None
+    return t, r(rows, Hq, width).to(dtype), r(rows, Hk, width).to(dtype)
+
+
+def dev(t):
+    return {k: (v.cuda() if isinstance(v, torch.Tensor) else v) for k, v in t.items()}
+
+
+def pair_sizes(x, t, interleaved):
+    """|a| + |b| of the pair that an element is turned in, |x| of the others."""
+    x = x.double().abs()
+    half = 0 if t["inv_freq"] is None else t["inv_freq"].shape[0]
+    if half == 0:
+        return x
+    out = x.clone()
+    first = torch.arange(half) * 2 if interleaved else torch.arange(half)
+    second = first + (1 if interleaved else half)
+    out[..., first] = out[..., second] = x[..., first] + x[..., second]
+    return out
+
+
+def check_all(t, dq, dk, interleaved, got=None, grads=None, eps=1e-6):
+    d = dev(t)
+    if got is None:
+        got = ssm.qk_norm_rope_fwd(**d, interleaved=interleaved, eps=eps)
+        grads = ssm.qk_norm_rope_bwd(d["q"], d["k"], dq.cuda(), dk.cuda(), d["q_weight"], d["k_weight"], d["positions"],
+                                     d["inv_freq"], interleaved=interleaved, eps=eps)
+    width = t["q"].shape[-1]
+    n = (width // 2 + 24) * Bd.U
+    half = Bd.HALF if t["q"].dtype == BF else 0.0
+    want = O.qk_norm_rope(**t, interleaved=interleaved, eps=eps)
+    plain = O.qk_norm_rope(t["q"], t["k"], t["q_weight"], t["k_weight"], eps=eps)
+    for name, x, y, p in zip("qk", got, want, plain):
+        Bd.check(name, x, y, n * pair_sizes(p, t, interleaved) + half * y.abs() + 1e-37)
+    want = O.qk_norm_rope_bwd(t["q"], t["k"], dq, dk, t["q_weight"], t["k_weight"], t["positions"], t["inv_freq"],
+                              interleaved=interleaved, eps=eps)
+    assert set(grads) == set(want)
+    for name, x, d0, w in (("q", t["q"], dq, t["q_weight"]), ("k", t["k"], dk, t["k_weight"])):
+        x = x.double()
+        r = 1 / torch.sqrt((x * x).mean(-1, keepdim=True) + eps)
+        size = pair_sizes(d0, t, interleaved)
+        nd = (x * r).abs()
+        wd = size * (1.0 if w is None else w.double().abs())
+        allow = n * r * (wd + nd * (wd * nd).mean(-1, keepdim=True))
+        Bd.check("d" + name, grads["d" + name], want["d" + name], 2 * allow + half * want["d" + name].abs() + 1e-37)
+        if w is not None:
+            terms = size * nd
+            count = terms.shape[0] * terms.shape[1] + width + 64
+            key = "d" + name + "_weight"
+            Bd.check(key, grads[key], want[key], count * Bd.U * terms.sum((0, 1)) + 1e-37)
+
+
+SHAPES = [
+    # rows, query heads, key heads, width, rotary
+    (1, 1, 1, 2, 2), (3, 2, 1, 6, 4), (5, 3, 2, 10, 10), (7, 4, 4, 16, 0), (33, 5, 1, 64, 64), (2, 8, 8, 80, 80),
+    (9, 3, 3, 96, 48), (70, 8, 2, 128, 128), (1, 32, 8, 128, 32), (4, 2, 2, 130, 64), (3, 1, 1, 250, 250), (6, 2, 1, 256, 64),
+    (5, 2, 2, 510, 512 - 6), (3, 3, 1, 512, 512), (2100, 2, 1, 32, 32), (9000, 1, 1, 8, 8),
+]
+
+
+@pytest.mark.parametrize("dtype", [F, BF])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_forward_and_backward(shape, dtype):
+    for interleaved, weights, far in ((False, True, False), (True, False, True)):
+        check_all(*make(*shape, dtype, seed=sum(shape), weights=weights, far=far), interleaved)
+
+
+@pytest.mark.parametrize("dtype", [F, BF])
+@pytest.mark.parametrize("offset", [0, 1, 4])
+def test_parts_of_a_projection(dtype, offset):
+    """Heads taken out of a wider row, on any border: the dense copies' bits where the loads are the same."""
+    rows, Hq, Hk, width = 50, 3, 2, 64
+    t, dq, dk = make(rows, Hq, Hk, width, 64, dtype)
+    wide = torch.zeros(rows, (Hq + Hk) * width + 16, dtype=dtype)
+    q = wide[:, offset:offset + Hq * width].unflatten(1, (Hq, width))
+    k = wide[:, offset + Hq * width:offset + (Hq + Hk) * width].unflatten(1, (Hk, width))
+    q.copy_(t["q"])
+    k.copy_(t["k"])
+    w = wide.cuda()
+    q, k = (w[:, a:a + n * width].unflatten(1, (n, width)) for a, n in ((offset, Hq), (offset + Hq * width, Hk)))
+    d = dev(t)
+    got = ssm.qk_norm_rope_fwd(q, k, d["q_weight"], d["k_weight"], d["positions"], d["inv_freq"])
+    grads = ssm.qk_norm_rope_bwd(q, k, dq.cuda(), dk.cuda(), d["q_weight"], d["k_weight"], d["positions"], d["inv_freq"])
+    check_all(t, dq, dk, False, got, grads)
+
+
+def test_leading_axes_and_single_kinds():
+    t, dq, dk = make(24, 3, 2, 32, 32, F)
+    d = dev(t)
+    want = ssm.qk_norm_rope_fwd(**d)
+    shaped = {**d, "q": d["q"].view(2, 3, 4, 3, 32), "k": d["k"].view(2, 3, 4, 2, 32), "positions": d["positions"].view(2, 3, 4)}
+    got = ssm.qk_norm_rope_fwd(**shaped)
+    assert got[0].shape == (2, 3, 4, 3, 32) and torch.equal(got[0].flatten(0, 2), want[0])
+    assert torch.equal(got[1].flatten(0, 2), want[1])
+    none = d["k"][:, :0]
+    y, z = ssm.qk_norm_rope_fwd(d["q"], none, d["q_weight"], None, d["positions"], d["inv_freq"])
+    assert torch.equal(y, want[0]) and z.shape == (24, 0, 32)
+    r = ssm.qk_norm_rope_bwd(d["q"], none, dq.cuda(), none, d["q_weight"], d["k_weight"], d["positions"], d["inv_freq"])
+    full = ssm.qk_norm_rope_bwd(d["q"], d["k"], dq.cuda(), dk.cuda(), d["q_weight"], d["k_weight"], d["positions"],
+                                d["inv_freq"])
+    assert torch.equal(r["dq"], full["dq"]) and torch.equal(r["dq_weight"], full["dq_weight"])
+    assert not r["dk_weight"].any()
+
+
+def test_no_rows_and_zero_rows():
+    z = torch.empty(0, 2, 16, dtype=BF, device="cuda")
+    w = torch.ones(16, device="cuda")
+    y, _ = ssm.qk_norm_rope_fwd(z, z, w, w)
+    r = ssm.qk_norm_rope_bwd(z, z, z, z, w, w)
+    torch.cuda.synchronize()
+    assert y.shape == (0, 2, 16) and not r["dq_weight"].any() and not r["dk_weight"].any()
+    x = torch.zeros(3, 2, 16, device="cuda")                      # a head of zeros stays zero
+    y, _ = ssm.qk_norm_rope_fwd(x, x, w, w)
+    r = ssm.qk_norm_rope_bwd(x, x, x + 1, x + 1, w, w)
+    assert not y.any() and torch.isfinite(r["dq"]).all()
+
+
+def test_captured_and_replayed():
+    t, dq, dk = make(300, 4, 2, 64, 64, BF)
+    d = dev(t)
+    dq, dk = dq.cuda(), dk.cuda()
+
+    def work():
+        return [*ssm.qk_norm_rope_fwd(**d), *ssm.qk_norm_rope_bwd(d["q"], d["k"], dq, dk, d["q_weight"], d["k_weight"],
+                                                                  d["positions"], d["inv_freq"]).values()]
+    work()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = work()
+    for n in range(3):
+        d["q"].copy_(torch.randn(d["q"].shape, generator=torch.Generator().manual_seed(n)).to(BF))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [x.clone() for x in out]
+        assert all(torch.equal(a, b) for a, b in zip(got, work())), n
+
+
+def test_offsets_past_32_bits():
+    rows, heads, width = 70000, 256, 128
+    q = torch.randn(rows, heads, width, dtype=BF, device="cuda")
+    assert q.numel() > 2 ** 31
+    pos = torch.arange(rows, dtype=torch.int32, device="cuda")
+    freq = 10000.0 ** (-torch.arange(64, device="cuda") * 2.0 / 128)
+    w = torch.rand(width, device="cuda") + 0.5
+    y, _ = ssm.qk_norm_rope_fwd(q, q[:, :1].contiguous(), w, w, pos, freq)
+    a, _ = ssm.qk_norm_rope_fwd(q[-50:], q[-50:, :1].contiguous(), w, w, pos[-50:].contiguous(), freq)
+    assert torch.equal(y[-50:], a)
+    r = ssm.qk_norm_rope_bwd(q, q[:, :1].contiguous(), q, q[:, :1].contiguous(), w, w, pos, freq)
+    b = ssm.qk_norm_rope_bwd(q[-50:], q[-50:, :1].contiguous(), q[-50:], q[-50:, :1].contiguous(), w, w,
+                             pos[-50:].contiguous(), freq)
+    assert torch.equal(r["dq"][-50:], b["dq"])

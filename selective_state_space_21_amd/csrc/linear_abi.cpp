@@ -66,17 +66,17 @@ extern "C" {
 
 int ssm_linear_attention_segments(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv, int dtype) {
     if (linear_check_sizes(B, L, H, H, Dk, Dv, dtype) != SSM_OK) return 0;
-    return ssm::plan_linear_fwd(B, L, H, Dv).segments;
+    return ssm::plan_linear_fwd(B, L, H, Dk, Dv, dtype == SSM_BF16).segments;
 }
 
 int ssm_linear_attention_bwd_segments(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv, int dtype) {
     if (linear_check_sizes(B, L, H, H, Dk, Dv, dtype) != SSM_OK) return 0;
-    return ssm::plan_linear_bwd(B, L, H, Dk, Dv).segments;
+    return ssm::plan_linear_bwd(B, L, H, Dk, Dv, dtype == SSM_BF16).segments;
 }
 
 size_t ssm_linear_attention_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv, int dtype) {
     if (linear_check_sizes(B, L, H, H, Dk, Dv, dtype) != SSM_OK) return 0;
-    return ssm::linear_fwd_workspace_bytes(B, L, H, Dk, Dv);
+    return ssm::linear_fwd_workspace_bytes(B, L, H, Dk, Dv, dtype == SSM_BF16);
 }
 
 int ssm_linear_attention_fwd(const void* q, const void* k, const void* v, const float* log_decay, int by_head,
@@ -94,12 +94,12 @@ int ssm_linear_attention_fwd(const void* q, const void* k, const void* v, const 
     if (!all_aligned({log_decay, h0, h_last, seq_lens}, 4)) return SSM_ERR_MISALIGNED;
     ssm::LinearArgs a{};
     a.bf16 = dtype == SSM_BF16;
-    const size_t need = ssm::linear_fwd_workspace_bytes(B, L, H, Dk, Dv);
+    const size_t need = ssm::linear_fwd_workspace_bytes(B, L, H, Dk, Dv, a.bf16);
     if (need) {
         if (!workspace || workspace_bytes < need) return SSM_ERR_WORKSPACE;
         if (!aligned(workspace, 256)) return SSM_ERR_MISALIGNED;
     }
-    a.plan = ssm::plan_linear_fwd(B, L, H, Dv);
+    a.plan = ssm::plan_linear_fwd(B, L, H, Dk, Dv, a.bf16);
     a.q = q; a.k = k; a.v = v; a.g = log_decay; a.by_head = by_head != 0; a.scale = scale;
     a.h0 = h0; a.o = o; a.h_last = h_last; a.seq_lens = seq_lens;
     a.q_row = q_row; a.k_row = k_row; a.v_row = v_row;
@@ -111,7 +111,7 @@ int ssm_linear_attention_fwd(const void* q, const void* k, const void* v, const 
 size_t ssm_linear_attention_bwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t G, int64_t Dk, int64_t Dv,
                                                 int by_head, int dtype) {
     if (linear_check_sizes(B, L, H, G, Dk, Dv, dtype) != SSM_OK) return 0;
-    return ssm::linear_bwd_workspace_bytes(B, L, H, G, Dk, Dv, by_head != 0);
+    return ssm::linear_bwd_workspace_bytes(B, L, H, G, Dk, Dv, dtype == SSM_BF16, by_head != 0);
 }
 
 int ssm_linear_attention_bwd(const void* q, const void* k, const void* v, const float* log_decay, int by_head,
@@ -130,10 +130,10 @@ int ssm_linear_attention_bwd(const void* q, const void* k, const void* v, const 
     if (!all_aligned({log_decay, h0, dh_last, dlog_decay, dh0, seq_lens}, 4)) return SSM_ERR_MISALIGNED;
     ssm::LinearBwdArgs a{};
     a.f.bf16 = dtype == SSM_BF16;
-    const size_t need = ssm::linear_bwd_workspace_bytes(B, L, H, G, Dk, Dv, by_head != 0);
+    const size_t need = ssm::linear_bwd_workspace_bytes(B, L, H, G, Dk, Dv, a.f.bf16, by_head != 0);
     if (!workspace || workspace_bytes < need) return SSM_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return SSM_ERR_MISALIGNED;
-    a.f.plan = ssm::plan_linear_bwd(B, L, H, Dk, Dv);
+    a.f.plan = ssm::plan_linear_bwd(B, L, H, Dk, Dv, a.f.bf16);
     a.f.q = q; a.f.k = k; a.f.v = v; a.f.g = log_decay; a.f.by_head = by_head != 0; a.f.scale = scale;
     a.f.h0 = h0; a.f.seq_lens = seq_lens;
     a.f.q_row = q_row; a.f.k_row = k_row; a.f.v_row = v_row;

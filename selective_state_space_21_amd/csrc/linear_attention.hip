@@ -287,7 +287,7 @@ __device__ __forceinline__ void issue_point() { __builtin_amdgcn_sched_barrier(0
 //      both: stage the next chunk, fetch the one behind it
 //   B  state: update                            other: the next chunk's scores, this one's outputs
 template <typename T, int KD, bool STATES, bool SPLIT>
-__global__ __launch_bounds__(kThreads, 2) void linear_chunks(LinearRun run) {
+__global__ __launch_bounds__(kThreads, sizeof(T) == 4 && KD == 64 ? 4 : 2) void linear_chunks(LinearRun run) {
     using M = Mat<T>;
     using Frag = typename M::Frag;
     constexpr int TERMS = SPLIT && sizeof(T) == 2 ? 3 : 1;   // of the scores and of the state as an operand
@@ -306,6 +306,7 @@ __global__ __launch_bounds__(kThreads, 2) void linear_chunks(LinearRun run) {
     const int tile = (int)(id % ctiles);
     if (unit >= run.B * run.H * run.segments) return;
     const int seg = (int)(unit % run.segments);
+    if (STATES && seg == (job.reversed ? 0 : run.segments - 1)) return;    // no segment takes its state
     const int64_t bh = unit / run.segments, b = bh / run.H;
     const int h = (int)(bh % run.H);
     const int lane = threadIdx.x % 64, i = lane % 16, g = lane / 16;
@@ -585,12 +586,12 @@ __global__ __launch_bounds__(kThreads, 2) void linear_chunks(LinearRun run) {
                             for (int it = 0; it < RT; ++it) out[it] = M::mma(x.term[n], q[kk][it], out[it]);
                     }
                 }
+#pragma unroll
+                for (int it = 0; it < RT; ++it) s.through[(group * RT + it) * 64 + lane] = out[it];
                 load_keys(s.K[now], 0);
                 issue_point();
                 stage(next);
                 fetch();
-#pragma unroll
-                for (int it = 0; it < RT; ++it) s.through[(group * RT + it) * 64 + lane] = out[it];
                 if constexpr (L::kEarly) decay_values();
             }
             more_decays(c);
@@ -668,20 +669,8 @@ __global__ __launch_bounds__(kThreads, 2) void linear_chunks(LinearRun run) {
     } else {
         // this wavefront's tiles of a chunk: group, group + 4, all on their way together (the state's team
         // takes what is left; of the first chunk this one does)
-        const auto scores = [&](auto most, int at, int slot) {
-            constexpr int MOST = decltype(most)::value;
-            Score x[MOST];
-#pragma unroll
-            for (int m = 0; m < MOST; ++m)
-                if (group + kGroups * m < TILES) start(x[m], at, slot, group + kGroups * m);
-            issue_point();
-#pragma unroll
-            for (int m = 0; m < MOST; ++m)
-                if (group + kGroups * m < TILES) multiply(x[m], at);
-#pragma unroll
-            for (int m = 0; m < MOST; ++m)
-                if (group + kGroups * m < TILES) finish(x[m], at);
-        };
+        constexpr int MOST = (TILES + kGroups - 1) / kGroups, MINE = MOST < 2 ? MOST : 2;
+        const auto has = [&](int m) { return TILES >= kGroups * (m + 1) || group + kGroups * m < TILES; };
 
         // the outputs' places: row 16 it + i, four columns from `col` on
         const bool wide = sizeof(T) == 4 || held(job.out_f32);
@@ -709,10 +698,17 @@ __global__ __launch_bounds__(kThreads, 2) void linear_chunks(LinearRun run) {
             }
         }
 
-        using Two = std::integral_constant<int, (TILES < 2 * kGroups ? TILES + kGroups - 1 : 2 * kGroups) / kGroups>;
         if (chunks > 0) {
             prologue();
-            if constexpr (!STATES) scores(std::integral_constant<int, (TILES + kGroups - 1) / kGroups>{}, 0, 0);
+            if constexpr (!STATES)
+#pragma unroll
+                for (int m = 0; m < MOST; ++m)
+                    if (has(m)) {
+                        Score x;
+                        start(x, 0, 0, group + kGroups * m);
+                        multiply(x, 0);
+                        finish(x, 0);
+                    }
         }
         // A chunk's outputs are stored after the next one's rows are staged, and before the fetch behind
         // those: loads and stores are waited for in order, and the staging waits for the loads.
@@ -769,7 +765,14 @@ __global__ __launch_bounds__(kThreads, 2) void linear_chunks(LinearRun run) {
                 more_decays(c);
                 lds_barrier();   // the state's part, this chunk's values and scores, the next one's rows are there
 
-                scores(Two{}, next, next_of(slot));
+                Score x[MINE];
+#pragma unroll
+                for (int m = 0; m < MINE; ++m)
+                    if (has(m)) start(x[m], next, next_of(slot), group + kGroups * m);
+                issue_point();
+#pragma unroll
+                for (int m = 0; m < MINE; ++m)
+                    if (has(m)) multiply(x[m], next);
                 Frag v[KB], p[RT][KB][TERMS];
                 float since[RT];
 #pragma unroll
@@ -791,6 +794,9 @@ __global__ __launch_bounds__(kThreads, 2) void linear_chunks(LinearRun run) {
                             p[it][b2][n] = M::along(&s.P[now][n][Scores::at(16 * it + i, 4 * b2 + g)]);
                 }
                 issue_point();
+#pragma unroll
+                for (int m = 0; m < MINE; ++m)
+                    if (has(m)) finish(x[m], next);
 #pragma unroll
                 for (int it = 0; it < RT; ++it) out[it] *= fast_exp2(since[it]) * outer;
 #pragma unroll
@@ -881,7 +887,7 @@ __global__ __launch_bounds__(256) void linear_join(LinearJoin j) {
         float decay[8];
 #pragma unroll
         for (int m = 0; m < 8; ++m)
-            if (n0 + m < j.segments) {
+            if (n0 + m < j.segments - 1) {                   // the last one's state enters none, and is not there
                 const int64_t s = head * j.segments + (j.reversed ? j.segments - 1 - n0 - m : n0 + m);
                 own[m] = *reinterpret_cast<const f32x4*>(j.seg_state + s * j.size + e);
                 decay[m] = j.seg_decay[s];
@@ -891,7 +897,7 @@ __global__ __launch_bounds__(256) void linear_join(LinearJoin j) {
             if (n0 + m < j.segments) {
                 const int64_t s = head * j.segments + (j.reversed ? j.segments - 1 - n0 - m : n0 + m);
                 *reinterpret_cast<f32x4*>(j.seg_state + s * j.size + e) = carry;
-                carry = carry * fast_exp2(decay[m]) + own[m];
+                if (n0 + m < j.segments - 1) carry = carry * fast_exp2(decay[m]) + own[m];
             }
     }
 }

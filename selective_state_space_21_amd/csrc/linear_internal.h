@@ -67,8 +67,8 @@ struct LinearPlan {
     int segments;
     int64_t seg_tokens;
 };
-LinearPlan plan_linear_fwd(int64_t B, int64_t L, int64_t H, int64_t Dv);
-LinearPlan plan_linear_bwd(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv);
+LinearPlan plan_linear_fwd(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv, bool bf16);
+LinearPlan plan_linear_bwd(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv, bool bf16);
 
 struct LinearArgs {
     const void* q;
@@ -99,8 +99,9 @@ struct LinearBwdArgs {
     float* dh0;
 };
 
-size_t linear_fwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv);
-size_t linear_bwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t G, int64_t Dk, int64_t Dv, bool by_head);
+size_t linear_fwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv, bool bf16);
+size_t linear_bwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t G, int64_t Dk, int64_t Dv, bool bf16,
+                                  bool by_head);
 hipError_t launch_linear_fwd(const LinearArgs& a, hipStream_t stream);
 hipError_t launch_linear_bwd(const LinearBwdArgs& a, hipStream_t stream);
 

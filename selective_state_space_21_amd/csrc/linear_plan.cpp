@@ -16,20 +16,21 @@ namespace {
 int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 int64_t tiles_of(int64_t width) { return (width + linear::kColumns - 1) / linear::kColumns; }
 
-// Workgroups that run at once: their LDS leaves room for one on a CU.
-constexpr int64_t kAtOnce = 256;
+// Workgroups that run at once: LDS and registers leave room for one on a CU,
+// or two where fp32 keys of up to 64 elements are contracted.
+int64_t at_once(bool bf16, int64_t keys) { return !bf16 && keys <= 64 ? 512 : 256; }
 // Forced segments: what joins them, and their workgroups, go out as one launch.
 constexpr int64_t kMostCut = int64_t(1) << 14;
 
 // Where sequences are cut.  `units` workgroups a segment make the outputs,
-// `states` make the segments' states first, in rounds of kAtOnce.  In tokens
+// `states` make the segments' states first, in rounds of those that run at once.  In tokens
 // of a workgroup's time (30-45 ns each): a round lasts its segment's length, a
 // round of states 0.3 of it, what a cut costs in launches about 300, the
 // joining of a segment's states about 20.  Measured, forward B=1 L=8192 H=16
 // 128x128 bf16: 286 us whole, 123 in 4, 80 in 8 (one round), 106 in 12, 96 in
 // 16; backward 573, 298, 263, 292, 299; forward B=1 L=512 H=8 64x64: 20 us
 // whole, 24 in 4.  A cut has to save 5%.
-LinearPlan plan(int64_t units, int64_t states, int64_t L) {
+LinearPlan plan(int64_t units, int64_t states, int64_t at_once, int64_t L) {
     LinearPlan best{1, up(L > 0 ? L : 1, linear::kSegment)};
     const auto cut = [L](int64_t n) {
         LinearPlan p;
@@ -42,7 +43,7 @@ LinearPlan plan(int64_t units, int64_t states, int64_t L) {
         const long n = strtol(e, nullptr, 10);
         if (n >= 1 && n <= 256) return n > 1 ? cut(n) : best;
     }
-    const auto rounds = [](int64_t n) { return (double)((n + kAtOnce - 1) / kAtOnce); };
+    const auto rounds = [at_once](int64_t n) { return (double)((n + at_once - 1) / at_once); };
     double least = 0.95 * rounds(units) * (double)L;
     for (int64_t n = 2; n <= 256 && n * linear::kSegment <= L; ++n) {
         const LinearPlan p = cut(n);
@@ -144,21 +145,21 @@ int pad(int64_t width) { return width <= 64 ? 64 : width <= 128 ? 128 : 256; }
 
 }  // namespace
 
-LinearPlan plan_linear_fwd(int64_t B, int64_t L, int64_t H, int64_t Dv) {
-    return plan(B * H * tiles_of(Dv), B * H * tiles_of(Dv), L);
+LinearPlan plan_linear_fwd(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv, bool bf16) {
+    return plan(B * H * tiles_of(Dv), B * H * tiles_of(Dv), at_once(bf16, Dk), L);
 }
 
-LinearPlan plan_linear_bwd(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv) {
-    return plan(B * H * (2 * tiles_of(Dk) + tiles_of(Dv)), 2 * B * H * tiles_of(Dv), L);
+LinearPlan plan_linear_bwd(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv, bool bf16) {
+    return plan(B * H * (2 * tiles_of(Dk) + tiles_of(Dv)), 2 * B * H * tiles_of(Dv), at_once(bf16, Dk > Dv ? Dk : Dv), L);
 }
 
-size_t linear_fwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv) {
-    return FwdSpace(nullptr, plan_linear_fwd(B, L, H, Dv), B, H, Dk * Dv).bytes;
+size_t linear_fwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv, bool bf16) {
+    return FwdSpace(nullptr, plan_linear_fwd(B, L, H, Dk, Dv, bf16), B, H, Dk * Dv).bytes;
 }
 
-size_t linear_bwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t G, int64_t Dk, int64_t Dv,
+size_t linear_bwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t G, int64_t Dk, int64_t Dv, bool bf16,
                                   bool by_head) {
-    return BwdSpace(nullptr, plan_linear_bwd(B, L, H, Dk, Dv), B, L, H, G, Dk, Dv, by_head).bytes;
+    return BwdSpace(nullptr, plan_linear_bwd(B, L, H, Dk, Dv, bf16), B, L, H, G, Dk, Dv, by_head).bytes;
 }
 
 hipError_t launch_linear_fwd(const LinearArgs& a, hipStream_t stream) {

@@ -60,6 +60,20 @@ def _check(device, parts, *specs):
     """Types, shapes and dtypes of every argument first, then devices and
     layout, as _args.check_args; `parts` may be parts of wider rows.  Returns
     their elements between tokens."""
+    rows = []
+    for _name, t, shape, dtype in parts:      # all as they should be, and dense: one pass
+        if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype
+                and t.device == device and t.is_contiguous()):
+            break
+        rows.append(shape[-2] * shape[-1])
+    else:
+        for _name, t, shape, dtype in specs:
+            if t is not None and not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype
+                                      and t.device == device and t.is_contiguous()):
+                break
+        else:
+            if device.type == "cuda":
+                return rows
     for name, t, shape, dtype in (*parts, *specs):
         if t is None:
             continue
@@ -78,12 +92,13 @@ def _sizes(q, v, lead, names):
     dt = _args.act_dtype("q", q)
     if not isinstance(v, torch.Tensor):
         raise TypeError("v must be a torch.Tensor")
-    if q.dim() != lead + 2 or v.dim() != lead + 2:
+    a, b = q.shape, v.shape
+    if len(a) != lead + 2 or len(b) != lead + 2:
         raise ValueError(f"q must be [{names}, G, Dk] and v [{names}, H, Dv]")
-    if tuple(q.shape[:lead]) != tuple(v.shape[:lead]):
-        raise ValueError(f"q is for {tuple(q.shape[:lead])} tokens, v for {tuple(v.shape[:lead])}")
-    G, Dk = q.shape[-2:]
-    H, Dv = v.shape[-2:]
+    if a[:lead] != b[:lead]:
+        raise ValueError(f"q is for {tuple(a[:lead])} tokens, v for {tuple(b[:lead])}")
+    G, Dk = a[lead:]
+    H, Dv = b[lead:]
     if G < 1 or H % G:
         raise ValueError(f"{H} heads do not share {G} groups of keys evenly")
     return dt, q.device, G, Dk, H, Dv
@@ -91,7 +106,8 @@ def _sizes(q, v, lead, names):
 
 def _by_head(log_decay) -> bool:
     """The decays' shape tells their kind: [H], or one for each token and head."""
-    _args.need(log_decay=log_decay)
+    if log_decay is None:
+        _args.need(log_decay=log_decay)
     return isinstance(log_decay, torch.Tensor) and log_decay.dim() == 1
 
 
@@ -219,9 +235,10 @@ def linear_state_update(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v
     rows = _check(dev, (("q", q, (Bt, G, Dk), dt), ("k", k, (Bt, G, Dk), dt), ("v", v, (Bt, H, Dv), dt)),
                   ("log_decay", log_decay, (H,) if by_head else (Bt, H), _F32), ("state", state, (n, H, Dk, Dv), _F32),
                   ("slots", slots, (Bt,), _I32), ("out", out, (Bt, H, Dv), dt))
-    o = out if out is not None else torch.empty((Bt, H, Dv), dtype=dt, device=dev)
+    o = out if out is not None else torch.empty_like(v, memory_format=torch.contiguous_format)
+    lib = _native.load()
     with _on(dev):
-        rc = _native.load().ssm_linear_state_update(
+        rc = lib.ssm_linear_state_update(
             _ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), int(by_head), _default_scale(scale, Dk),
             _ptr(slots), _ptr(o), *rows, Bt, n, H, G, Dk, Dv, _DT[dt], _args.stream_handle(dev))
     _native.check(rc, "ssm_linear_state_update")

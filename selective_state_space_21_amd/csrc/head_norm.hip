@@ -32,23 +32,32 @@ typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 constexpr int kThreads = 256;
 constexpr int kAngles = 1024;                                // of a workgroup's rows
 
-// N = 1 or 4 neighbouring elements (4: on a border of four)
-template <typename T, int N> __device__ __forceinline__ void load(const T* p, float (&x)[N]) {
-    if constexpr (N == 1) {
-        x[0] = Elem<T>::load(p, 0);
-    } else if constexpr (sizeof(T) == 4) {
-        const f32x4 v = *reinterpret_cast<const f32x4*>(p);
+// N = 1 or 4 neighbouring elements as they are stored (4: on a border of four)
+template <typename T, int N> struct Stored;
+template <typename T> struct Stored<T, 1> {
+    T x;
+    __device__ __forceinline__ void load(const T* p) { x = *p; }
+    __device__ __forceinline__ void widen(float (&f)[1]) const { f[0] = Elem<T>::load(&x, 0); }
+};
+template <> struct Stored<float, 4> {
+    f32x4 x;
+    __device__ __forceinline__ void load(const float* p) { x = *reinterpret_cast<const f32x4*>(p); }
+    __device__ __forceinline__ void widen(float (&f)[4]) const {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = v[j];
-    } else {
-        const u32x2 v = *reinterpret_cast<const u32x2*>(p);
+        for (int j = 0; j < 4; ++j) f[j] = x[j];
+    }
+};
+template <> struct Stored<uint16_t, 4> {
+    u32x2 x;
+    __device__ __forceinline__ void load(const uint16_t* p) { x = *reinterpret_cast<const u32x2*>(p); }
+    __device__ __forceinline__ void widen(float (&f)[4]) const {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            x[2 * j] = __uint_as_float(v[j] << 16);
-            x[2 * j + 1] = __uint_as_float(v[j] & 0xffff0000u);
+            f[2 * j] = __uint_as_float(x[j] << 16);
+            f[2 * j + 1] = __uint_as_float(x[j] & 0xffff0000u);
         }
     }
-}
+};
 template <typename T, int N> __device__ __forceinline__ void store(T* p, const float (&x)[N]) {
     if constexpr (N == 1) {
         Elem<T>::store(p, 0, x[0]);
@@ -63,39 +72,75 @@ template <typename T, int N> __device__ __forceinline__ void store(T* p, const f
     }
 }
 
-// VEC pairs p .. p + VEC - 1 of a head
-template <typename T, int VEC>
-struct Pairs {
-    float a[VEC], b[VEC];
-    __device__ __forceinline__ void read(const T* head, int p, bool halves, int half) {
-        if (halves) {
-            load<T, VEC>(head + p, a);
-            load<T, VEC>(head + p + half, b);
-        } else if constexpr (VEC == 4) {
-            float x[4], y[4];
-            load<T, 4>(head + 2 * p, x);
-            load<T, 4>(head + 2 * p + 4, y);
-            a[0] = x[0]; b[0] = x[1]; a[1] = x[2]; b[1] = x[3];
-            a[2] = y[0]; b[2] = y[1]; a[3] = y[2]; b[3] = y[3];
-        } else {
-            a[0] = Elem<T>::load(head, 2 * p);
-            b[0] = Elem<T>::load(head, 2 * p + 1);
-        }
-    }
-    __device__ __forceinline__ void write(T* head, int p, bool halves, int half) const {
-        if (halves) {
-            store<T, VEC>(head + p, a);
-            store<T, VEC>(head + p + half, b);
-        } else if constexpr (VEC == 4) {
-            const float x[4] = {a[0], b[0], a[1], b[1]}, y[4] = {a[2], b[2], a[3], b[3]};
-            store<T, 4>(head + 2 * p, x);
-            store<T, 4>(head + 2 * p + 4, y);
-        } else {
-            Elem<T>::store(head, 2 * p, a[0]);
-            Elem<T>::store(head, 2 * p + 1, b[0]);
-        }
+// Where a lane's VEC pairs p .. p + VEC - 1 of a head lie: VEC elements from `first` on and VEC from `second` on.
+// Those are the pairs' two sides (`apart`: elements that are not turned may be paired in any way) or pair after pair.
+struct Place {
+    int first, second;
+    bool apart, there;
+    __device__ __forceinline__ Place(const HeadNormArgs& a, int p, int vec) {
+        const int half = a.rotary / 2;
+        const bool halves = !a.interleaved && p < half;
+        apart = !a.interleaved;
+        first = halves ? p : 2 * p;
+        second = halves ? p + half : 2 * p + vec;
+        there = p < a.width / 2;
     }
 };
+
+template <int VEC>
+struct Pairs {
+    float a[VEC], b[VEC];
+    // from pair after pair, and back
+    __device__ __forceinline__ void part() {
+        if constexpr (VEC == 4) {
+            const float x[4] = {a[0], a[2], b[0], b[2]}, y[4] = {a[1], a[3], b[1], b[3]};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) a[j] = x[j], b[j] = y[j];
+        }
+    }
+    __device__ __forceinline__ void join() {
+        if constexpr (VEC == 4) {
+            const float x[4] = {a[0], b[0], a[1], b[1]}, y[4] = {a[2], b[2], a[3], b[3]};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) a[j] = x[j], b[j] = y[j];
+        }
+    }
+    template <typename T> __device__ __forceinline__ void write(T* head, const Place& at) {
+        if (!at.apart) join();
+        store<T, VEC>(head + at.first, a);
+        store<T, VEC>(head + at.second, b);
+    }
+};
+
+template <typename T, int VEC>
+struct Held {
+    Stored<T, VEC> u, w;
+    __device__ __forceinline__ void load(const T* head, const Place& at) {
+        u.load(head + at.first);
+        w.load(head + at.second);
+    }
+    __device__ __forceinline__ Pairs<VEC> pairs(const Place& at) const {
+        Pairs<VEC> x;
+        u.widen(x.a);
+        w.widen(x.b);
+        if (!at.apart) x.part();
+        return x;
+    }
+};
+
+// A lane's pairs of the norm's weight, ones where there is none.
+template <int VEC>
+__device__ __forceinline__ Pairs<VEC> weights(const float* w, const Place& at) {
+    Pairs<VEC> x;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) x.a[j] = x.b[j] = 1.0f;
+    if (w && at.there) {
+        Held<float, VEC> h;
+        h.load(w, at);
+        x = h.pairs(at);
+    }
+    return x;
+}
 
 __device__ __forceinline__ float group_sum(float x, int lanes) {
     for (int m = lanes / 2; m >= 1; m /= 2) x += __shfl_xor(x, m);
@@ -113,88 +158,109 @@ __device__ __forceinline__ void angles(const HeadNormArgs& a, int64_t row0, int 
     }
 }
 
-// NP: pieces of VEC pairs that a lane holds of a head
+// NP: pieces of VEC pairs that a lane holds of a head.  The first head's elements are on their way while the
+// angles are formed, later ones two at a time.
 template <typename T, int VEC, int NP>
 __global__ __launch_bounds__(kThreads) void head_norm_fwd(HeadNormArgs a, int lanes, int tokens) {
     __shared__ float2 angle[kAngles];
-    const int half = a.rotary / 2, pairs = a.width / 2;
+    const int half = a.rotary / 2;
     const int64_t row0 = (int64_t)blockIdx.x * tokens;
     const int n = a.rows - row0 < tokens ? (int)(a.rows - row0) : tokens;
-    angles(a, row0, n, half, angle);
     const int groups = kThreads / lanes, grp = threadIdx.x / lanes, lane = threadIdx.x % lanes;
     const float by = 1.0f / (float)a.width;
+    using Row = Held<T, VEC>[NP];
+    const auto place = [&](int m) { return Place(a, (lane + m * lanes) * VEC, VEC); };
+    const auto fetch = [&](Row& x, int which, int item) {
+        const int heads = (int)a.heads[which];
+        if (item >= n * heads) return;
+        const T* p = static_cast<const T*>(a.x[which]) + (row0 + item / heads) * a.x_row[which] +
+                     (int64_t)(item % heads) * a.width;
+#pragma unroll
+        for (int m = 0; m < NP; ++m)
+            if (place(m).there) x[m].load(p, place(m));
+    };
+    Row first[2];
+    Pairs<VEC> wt[2][NP];
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        fetch(first[which], which, grp);
+#pragma unroll
+        for (int m = 0; m < NP; ++m) wt[which][m] = weights<VEC>(a.weight[which], place(m));
+    }
+    angles(a, row0, n, half, angle);
     lds_barrier();
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
-        const int heads = (int)a.heads[which];
-        const float* w = a.weight[which];
-        Pairs<float, VEC> wt[NP];
-#pragma unroll
-        for (int m = 0; m < NP; ++m) {
-            const int p = (lane + m * lanes) * VEC;
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) wt[m].a[j] = wt[m].b[j] = 1.0f;
-            if (w && p < pairs) wt[m].read(w, p, !a.interleaved && p < half, half);
-        }
-        const int items = n * heads;
+        const int heads = (int)a.heads[which], items = n * heads;
 #pragma unroll 2
         for (int item = grp; item < items; item += groups) {
             const int r = item / heads, h = item % heads;
-            const T* x = static_cast<const T*>(a.x[which]) + (row0 + r) * a.x_row[which] + (int64_t)h * a.width;
             T* y = static_cast<T*>(a.y[which]) + ((row0 + r) * heads + h) * a.width;
-            Pairs<T, VEC> v[NP];
+            if (item != grp) fetch(first[which], which, item);
+            Pairs<VEC> v[NP];
             float sum = 0.0f;
 #pragma unroll
-            for (int m = 0; m < NP; ++m) {
-                const int p = (lane + m * lanes) * VEC;
-                if (p < pairs) {
-                    v[m].read(x, p, !a.interleaved && p < half, half);
+            for (int m = 0; m < NP; ++m)
+                if (place(m).there) {
+                    v[m] = first[which][m].pairs(place(m));
 #pragma unroll
                     for (int j = 0; j < VEC; ++j) sum = fmaf(v[m].a[j], v[m].a[j], fmaf(v[m].b[j], v[m].b[j], sum));
                 }
-            }
             const float rstd = 1.0f / sqrtf(fmaf(group_sum(sum, lanes), by, a.eps));
 #pragma unroll
             for (int m = 0; m < NP; ++m) {
                 const int p = (lane + m * lanes) * VEC;
-                if (p < pairs) {
+                if (place(m).there) {
 #pragma unroll
                     for (int j = 0; j < VEC; ++j) {
-                        const float f = v[m].a[j] * rstd * wt[m].a[j], g = v[m].b[j] * rstd * wt[m].b[j];
+                        const float f = v[m].a[j] * rstd * wt[which][m].a[j], g = v[m].b[j] * rstd * wt[which][m].b[j];
                         float2 cs = float2{1.0f, 0.0f};
                         if (p < half) cs = angle[r * half + p + j];
                         v[m].a[j] = f * cs.x - g * cs.y;
                         v[m].b[j] = g * cs.x + f * cs.y;
                     }
-                    v[m].write(y, p, !a.interleaved && p < half, half);
+                    v[m].write(y, place(m));
                 }
             }
         }
     }
 }
 
+// The elements of a head are on their way while the one before it is computed.
 template <typename T, int VEC, int NP>
 __global__ __launch_bounds__(kThreads) void head_norm_bwd(HeadNormArgs a, int lanes, int tokens) {
     __shared__ float2 angle[kAngles];
     __shared__ float share[2 * VEC * NP * kThreads];
-    const int half = a.rotary / 2, pairs = a.width / 2;
+    const int half = a.rotary / 2;
     const int groups = kThreads / lanes, grp = threadIdx.x / lanes, lane = threadIdx.x % lanes;
     const float by = 1.0f / (float)a.width;
-    Pairs<float, VEC> wt[2][NP], sum[2][NP];
+    using Row = Held<T, VEC>[NP];
+    const auto place = [&](int m) { return Place(a, (lane + m * lanes) * VEC, VEC); };
+    const auto fetch = [&](Row& x, Row& d, int which, int64_t row0, int n, int item) {
+        const int heads = (int)a.heads[which];
+        if (item >= n * heads) return;
+        const int64_t row = row0 + item / heads, h = item % heads;
+        const T* p = static_cast<const T*>(a.x[which]) + row * a.x_row[which] + h * a.width;
+        const T* dy = static_cast<const T*>(a.dy[which]) + (row * heads + h) * a.width;
+#pragma unroll
+        for (int m = 0; m < NP; ++m)
+            if (place(m).there) x[m].load(p, place(m)), d[m].load(dy, place(m));
+    };
+    Pairs<VEC> wt[2][NP], sum[2][NP];
 #pragma unroll
     for (int which = 0; which < 2; ++which)
 #pragma unroll
         for (int m = 0; m < NP; ++m) {
-            const int p = (lane + m * lanes) * VEC;
+            wt[which][m] = weights<VEC>(a.weight[which], place(m));
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                wt[which][m].a[j] = wt[which][m].b[j] = 1.0f;
-                sum[which][m].a[j] = sum[which][m].b[j] = 0.0f;
-            }
-            if (a.weight[which] && p < pairs) wt[which][m].read(a.weight[which], p, !a.interleaved && p < half, half);
+            for (int j = 0; j < VEC; ++j) sum[which][m].a[j] = sum[which][m].b[j] = 0.0f;
         }
-    for (int64_t row0 = (int64_t)blockIdx.x * tokens; row0 < a.rows; row0 += a.groups * tokens) {
-        const int n = a.rows - row0 < tokens ? (int)(a.rows - row0) : tokens;
+    const int64_t stop = (blockIdx.x + 1) * a.group_rows < a.rows ? (blockIdx.x + 1) * a.group_rows : a.rows;
+    for (int64_t row0 = blockIdx.x * a.group_rows; row0 < stop; row0 += tokens) {
+        const int n = stop - row0 < tokens ? (int)(stop - row0) : tokens;
+        Row first[2], first_d[2];
+#pragma unroll
+        for (int which = 0; which < 2; ++which) fetch(first[which], first_d[which], which, row0, n, grp);
         lds_barrier();                                       // the last rows' angles have been read
         angles(a, row0, n, half, angle);
         lds_barrier();
@@ -203,18 +269,17 @@ __global__ __launch_bounds__(kThreads) void head_norm_bwd(HeadNormArgs a, int la
             const int heads = (int)a.heads[which], items = n * heads;
             for (int item = grp; item < items; item += groups) {
                 const int r = item / heads, h = item % heads;
-                const T* x = static_cast<const T*>(a.x[which]) + (row0 + r) * a.x_row[which] + (int64_t)h * a.width;
-                const int64_t at = ((row0 + r) * heads + h) * a.width;
-                const T* dy = static_cast<const T*>(a.dy[which]) + at;
-                T* dx = static_cast<T*>(a.dx[which]) + at;
-                Pairs<T, VEC> v[NP], d[NP];
+                T* dx = static_cast<T*>(a.dx[which]) + ((row0 + r) * heads + h) * a.width;
+                Row next, next_d;
+                fetch(next, next_d, which, row0, n, item + groups);
+                Pairs<VEC> v[NP], d[NP];
                 float sq = 0.0f, dot = 0.0f;
 #pragma unroll
                 for (int m = 0; m < NP; ++m) {
                     const int p = (lane + m * lanes) * VEC;
-                    if (p < pairs) {
-                        v[m].read(x, p, !a.interleaved && p < half, half);
-                        d[m].read(dy, p, !a.interleaved && p < half, half);
+                    if (place(m).there) {
+                        v[m] = first[which][m].pairs(place(m));
+                        d[m] = first_d[which][m].pairs(place(m));
 #pragma unroll
                         for (int j = 0; j < VEC; ++j) {
                             float2 cs = float2{1.0f, 0.0f};
@@ -232,8 +297,7 @@ __global__ __launch_bounds__(kThreads) void head_norm_bwd(HeadNormArgs a, int la
                 const float c = group_sum(dot, lanes) * rstd * by;       // mean(w d n^)
 #pragma unroll
                 for (int m = 0; m < NP; ++m) {
-                    const int p = (lane + m * lanes) * VEC;
-                    if (p < pairs) {
+                    if (place(m).there) {
 #pragma unroll
                         for (int j = 0; j < VEC; ++j) {
                             const float na = v[m].a[j] * rstd, nb = v[m].b[j] * rstd;
@@ -242,8 +306,10 @@ __global__ __launch_bounds__(kThreads) void head_norm_bwd(HeadNormArgs a, int la
                             v[m].a[j] = rstd * (d[m].a[j] * wt[which][m].a[j] - na * c);
                             v[m].b[j] = rstd * (d[m].b[j] * wt[which][m].b[j] - nb * c);
                         }
-                        v[m].write(dx, p, !a.interleaved && p < half, half);
+                        v[m].write(dx, place(m));
                     }
+                    first[which][m] = next[m];
+                    first_d[which][m] = next_d[m];
                 }
             }
         }
@@ -253,10 +319,8 @@ __global__ __launch_bounds__(kThreads) void head_norm_bwd(HeadNormArgs a, int la
         if (!a.dweight[which]) continue;
         lds_barrier();
 #pragma unroll
-        for (int m = 0; m < NP; ++m) {
-            const int p = (lane + m * lanes) * VEC;
-            if (p < pairs) sum[which][m].write(share + grp * a.width, p, !a.interleaved && p < half, half);
-        }
+        for (int m = 0; m < NP; ++m)
+            if (place(m).there) sum[which][m].write(share + grp * a.width, place(m));
         lds_barrier();
         for (int c = threadIdx.x; c < a.width; c += kThreads) {
             float x = share[c];
@@ -272,21 +336,22 @@ int next_pow2(int n) {
     return p;
 }
 
-// Rows of a workgroup: enough heads to keep its lanes busy a few times over,
-// fewer while that leaves CUs idle, as many angles as LDS is given.
-int rows_of(const HeadNormArgs& a) {
-    int64_t n = a.rows / 2048;
+// Rows whose angles a workgroup forms at once: as many as LDS is given.
+int most_rows(const HeadNormArgs& a) {
     const int half = a.rotary / 2;
-    if (half > 0 && n > kAngles / half) n = kAngles / half;
-    return n < 1 ? 1 : n > 8 ? 8 : (int)n;
+    return half > 0 ? kAngles / half : kAngles;
 }
 
 template <typename T, int VEC, int NP>
 hipError_t launch(const HeadNormArgs& a, bool backward, int lanes, hipStream_t stream) {
-    const int tokens = rows_of(a);
+    const int most = most_rows(a);
     if (backward) {
+        const int tokens = a.group_rows < most ? (int)a.group_rows : most;
         head_norm_bwd<T, VEC, NP><<<dim3((unsigned)a.groups), kThreads, 0, stream>>>(a, lanes, tokens);
     } else {
+        // enough heads to keep the lanes busy a few times over, fewer while that leaves CUs idle
+        const int64_t share = a.rows / 2048 < 8 ? a.rows / 2048 : 8;
+        const int tokens = share < 1 ? 1 : share < most ? (int)share : most;
         const int64_t blocks = (a.rows + tokens - 1) / tokens;
         head_norm_fwd<T, VEC, NP><<<dim3((unsigned)blocks), kThreads, 0, stream>>>(a, lanes, tokens);
     }

@@ -230,6 +230,7 @@ int ssm_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const
     a.dy[0] = dq_out; a.dy[1] = dk_out; a.dx[0] = dq; a.dx[1] = dk;
     a.dweight[0] = dq_weight; a.dweight[1] = dk_weight;
     a.groups = ssm::head_norm_groups(rows);
+    a.group_rows = ssm::head_norm_group_rows(rows);
     a.part = static_cast<float*>(workspace);
     return status(ssm::launch_head_norm_bwd(a, static_cast<hipStream_t>(stream)));
 }

@@ -906,9 +906,11 @@ __global__ __launch_bounds__(256) void linear_join(LinearJoin j) {
 // dg of the token behind is <D, S> of the two states there, the differences
 // q . dq - k . dk add up token by token (in fp64: the sums of the two nearly
 // cancel where the memory is long).
-__global__ __launch_bounds__(256) void linear_decay_grad(LinearDecayGrad d) {
-    __shared__ double part[4];
-    __shared__ double total[4];
+constexpr int kGradThreads = 1024, kGradWaves = kGradThreads / 64;
+
+__global__ __launch_bounds__(kGradThreads) void linear_decay_grad(LinearDecayGrad d) {
+    __shared__ double part[kGradWaves];
+    __shared__ double total[2][kGradWaves];
     const int64_t unit = blockIdx.x, bh = unit / d.segments;
     const int seg = (int)(unit % d.segments);
     const int64_t b = bh / d.H;
@@ -923,57 +925,85 @@ __global__ __launch_bounds__(256) void linear_decay_grad(LinearDecayGrad d) {
     const int64_t last = from + d.seg_tokens < d.L ? from + d.seg_tokens : d.L;
     const int64_t to = last < len ? last : len;
 
+    // q . dq - k . dk of this thread's token before hi: over its column tiles, eight loads ahead of the sums
+    const auto difference = [&](int64_t hi) {
+        const int64_t t = hi - 1 - tid;                      // thread 0 has the last token
+        double x = 0.0;
+        if (t < from) return x;
+        const float *q = d.dot_q + bh * d.L + t, *k = d.dot_k + bh * d.L + t;
+        const int64_t step = d.B * d.H * d.L;
+        for (int n0 = 0; n0 < d.tiles; n0 += 4) {
+            float u[4], w[4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const int64_t n = n0 + m < d.tiles ? n0 + m : d.tiles - 1;
+                u[m] = q[n * step];
+                w[m] = k[n * step];
+            }
+#pragma unroll
+            for (int m = 0; m < 4; ++m) x += n0 + m < d.tiles ? (double)u[m] - (double)w[m] : 0.0;
+        }
+        return x;
+    };
+    double x = difference(to);
+
     const bool end = seg == d.segments - 1;
     const float* S = end ? d.S_last + bh * d.size : d.S + (unit + 1) * d.size;
     const float* D = d.segments > 1 ? d.D + unit * d.size : d.D_last ? d.D_last + bh * d.size : nullptr;
     double sum = 0.0;
     if (D && to > from) {
-        for (int e = tid * 4; e < d.size; e += 1024) {
-            float x = 0.0f;
+        for (int e = tid * 4; e < d.size; e += 4 * kGradThreads) {
+            float y = 0.0f;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) x = fmaf(S[e + r], D[e + r], x);
-            sum += (double)x;
+            for (int r = 0; r < 4; ++r) y = fmaf(S[e + r], D[e + r], y);
+            sum += (double)y;
         }
     }
 #pragma unroll
     for (int m = 32; m >= 1; m /= 2) sum += __shfl_xor(sum, m);
     if (lane == 0) part[wave] = sum;
     __syncthreads();
-    double carry = part[0] + part[1] + part[2] + part[3];
+    double carry = 0.0;
+#pragma unroll
+    for (int w = 0; w < kGradWaves; ++w) carry += part[w];
     if (to < len) {                                          // the token behind decays what D brings
-        const float x = d.g[d.by_head ? h : (b * d.L + to) * d.H + h] * kLog2e;
-        carry *= (double)fast_exp2(x < kMinLog2 ? kMinLog2 : x);
+        const float y = d.g[d.by_head ? h : (b * d.L + to) * d.H + h] * kLog2e;
+        carry *= (double)fast_exp2(y < kMinLog2 ? kMinLog2 : y);
     }
 
     double all = 0.0;                                       // of this thread's tokens
-    for (int64_t hi = to; hi > from; hi -= 256) {
-        const int64_t t = hi - 1 - tid;                      // thread 0 has the last token
-        double x = 0.0;
-        if (t >= from) {
-            for (int n = 0; n < d.q_tiles; ++n) x += (double)d.dot_q[((int64_t)n * d.B * d.H + bh) * d.L + t];
-            for (int n = 0; n < d.k_tiles; ++n) x -= (double)d.dot_k[((int64_t)n * d.B * d.H + bh) * d.L + t];
+    int turn = 0;
+    for (int64_t hi = to; hi > from; hi -= kGradThreads) {
+        const int64_t t = hi - 1 - tid;
+        const double y = wave_sums(x, lane);
+        if (lane == 63) total[turn][wave] = y;
+        __syncthreads();                                     // `total` has two copies: one barrier is enough
+        x = difference(hi - kGradThreads);
+        double before = carry;
+#pragma unroll
+        for (int w = 0; w < kGradWaves; ++w) {
+            before += w < wave ? total[turn][w] : 0.0;
+            carry += total[turn][w];
         }
-        x = wave_sums(x, lane);
-        __syncthreads();
-        if (lane == 63) total[wave] = x;
-        __syncthreads();
-        for (int w = 0; w < wave; ++w) x += total[w];
-        x += carry;
-        carry += total[0] + total[1] + total[2] + total[3];
         if (t >= from) {
-            all += x;
-            if (d.dg) d.dg[(b * d.L + t) * d.H + h] = (float)x;
+            all += before + y;
+            if (d.dg) d.dg[(b * d.L + t) * d.H + h] = (float)(before + y);
         }
+        turn ^= 1;
     }
     if (d.dg)
-        for (int64_t t = (from > len ? from : len) + tid; t < last; t += 256) d.dg[(b * d.L + t) * d.H + h] = 0.0f;
+        for (int64_t t = (from > len ? from : len) + tid; t < last; t += kGradThreads) d.dg[(b * d.L + t) * d.H + h] = 0.0f;
     if (d.part) {
 #pragma unroll
         for (int m = 32; m >= 1; m /= 2) all += __shfl_xor(all, m);
         __syncthreads();
         if (lane == 0) part[wave] = all;
         __syncthreads();
-        if (tid == 0) d.part[(b * d.segments + seg) * d.H + h] = (float)(part[0] + part[1] + part[2] + part[3]);
+        if (tid == 0) {
+            double x = 0.0;
+            for (int w = 0; w < kGradWaves; ++w) x += part[w];
+            d.part[(b * d.segments + seg) * d.H + h] = (float)x;
+        }
     }
 }
 
@@ -1020,7 +1050,7 @@ hipError_t launch_linear_join(const LinearJoin& j, hipStream_t stream) {
 }
 
 hipError_t launch_linear_decay_grad(const LinearDecayGrad& d, hipStream_t stream) {
-    linear_decay_grad<<<dim3((unsigned)(d.B * d.H * d.segments)), 256, 0, stream>>>(d);
+    linear_decay_grad<<<dim3((unsigned)(d.B * d.H * d.segments)), kGradThreads, 0, stream>>>(d);
     return hipGetLastError();
 }
 

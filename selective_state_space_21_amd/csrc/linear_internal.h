@@ -124,9 +124,9 @@ hipError_t launch_linear_join(const LinearJoin& j, hipStream_t stream);
 // dg from the tokens' dot products: dg_t = sum over s >= t of (a_s - b_s), from
 // <D, S> of the states at each segment's right end on.
 struct LinearDecayGrad {
-    const float* dot_q;          // [q_tiles][B, H, L]: q . dq
-    const float* dot_k;          // [k_tiles][B, H, L]: k . dk
-    int32_t q_tiles, k_tiles;
+    const float* dot_q;          // [tiles][B, H, L]: q . dq
+    const float* dot_k;          // [tiles][B, H, L]: k . dk
+    int32_t tiles;
     const float* S;              // states entering segments 1.. and after the last: [B, H, segments][size]
     const float* S_last;         // [B, H][size], after the last segment
     const float* D;              // states entering from the right: [B, H, segments][size]
@@ -186,9 +186,10 @@ struct HeadNormArgs {
     const void* dy[2];           // backward: [rows, heads, width]
     void* dx[2];                 // [rows, heads, width]
     float* dweight[2];           // [width] or NULL
-    int64_t groups;              // backward: workgroups that each sum a share of the rows
+    int64_t groups, group_rows;  // backward: workgroups, and the rows that each sums its share of
     float* part;                 // [groups][2][width]
 };
+int64_t head_norm_group_rows(int64_t rows);
 int64_t head_norm_groups(int64_t rows);
 hipError_t launch_head_norm(const HeadNormArgs& a, hipStream_t stream);
 hipError_t launch_head_norm_bwd(const HeadNormArgs& a, hipStream_t stream);

@@ -16,21 +16,38 @@ namespace {
 int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 int64_t tiles_of(int64_t width) { return (width + linear::kColumns - 1) / linear::kColumns; }
 
-// Workgroups that run at once: LDS and registers leave room for one on a CU,
-// or two where fp32 keys of up to 64 elements are contracted.
-int64_t at_once(bool bf16, int64_t keys) { return !bf16 && keys <= 64 ? 512 : 256; }
+int pad(int64_t width) { return width <= 64 ? 64 : width <= 128 ? 128 : 256; }
+
+// Nanoseconds a token of a launch with `units` workgroups that contract `keys`
+// elements.  256 run at once, one on a CU; fewer run faster by up to a quarter,
+// for they share the caches' and the memory's rate.  Where fp32 keys of up to
+// 64 elements are contracted, LDS and registers leave room for two on a CU,
+// which then take 1.6 of the time that one takes.  Measured with all CUs at
+// work: bf16 41 (64 keys), 51 (128), 64 (256); fp32 73 (64), 120 (128).
+double token_ns(int64_t units, int64_t keys, bool bf16) {
+    const int kd = pad(keys);
+    const double all = bf16 ? (kd == 64 ? 40.0 : kd == 128 ? 50.0 : 65.0) : (kd == 64 ? 75.0 : kd == 128 ? 125.0 : 250.0);
+    const bool pairs = !bf16 && kd == 64;
+    const int64_t at_once = pairs ? 512 : 256, rest = units % at_once;
+    const double one = pairs ? 1.6 : 1.0;
+    return all * ((double)(units / at_once) * one +
+                  (rest > 256 ? one : rest > 0 ? 0.75 + 0.25 * (double)rest / 256.0 : 0.0));
+}
 // Forced segments: what joins them, and their workgroups, go out as one launch.
 constexpr int64_t kMostCut = int64_t(1) << 14;
 
-// Where sequences are cut.  `units` workgroups a segment make the outputs,
-// `states` make the segments' states first, in rounds of those that run at once.  In tokens
-// of a workgroup's time (30-45 ns each): a round lasts its segment's length, a
-// round of states 0.3 of it, what a cut costs in launches about 300, the
-// joining of a segment's states about 20.  Measured, forward B=1 L=8192 H=16
-// 128x128 bf16: 286 us whole, 123 in 4, 80 in 8 (one round), 106 in 12, 96 in
-// 16; backward 573, 298, 263, 292, 299; forward B=1 L=512 H=8 64x64: 20 us
-// whole, 24 in 4.  A cut has to save 5%.
-LinearPlan plan(int64_t units, int64_t states, int64_t at_once, int64_t L) {
+// Where sequences are cut: `whole(n)` gives the time of a token of all launches
+// that make outputs, `states(n)` of the launch that makes the segments' states
+// first, both with n segments.  What a cut costs in launches is about 12 us, the
+// joining of a segment's states about 0.4.  Measured, forward bf16: B=1 L=8192
+// H=16 128x128 282 us whole, 128 in 4, 82 in 8 (one round), 110 in 12, 98 in 16;
+// B=4 L=2048 of the same 84 whole, 85 in 2; B=1 L=1024 H=8 64x64 32 whole, 24 in
+// 8, L=512 20 whole, 24 in 4; fp32 B=1 L=16384 H=16 64x64 129 in 16, 143 in 24,
+// 120 in 32.  Backward bf16: B=1 L=8192 H=16 128x128 848 whole, 291 in 4, 262 in
+// 8, 290 in 12; fp32 B=3 L=1001 H=6 48x112 216 whole, 84 in 6, 106 in 8.  A cut
+// has to save 5%.
+template <typename Whole, typename States>
+LinearPlan plan(int64_t units, int64_t L, Whole whole, States states) {
     LinearPlan best{1, up(L > 0 ? L : 1, linear::kSegment)};
     const auto cut = [L](int64_t n) {
         LinearPlan p;
@@ -43,12 +60,10 @@ LinearPlan plan(int64_t units, int64_t states, int64_t at_once, int64_t L) {
         const long n = strtol(e, nullptr, 10);
         if (n >= 1 && n <= 256) return n > 1 ? cut(n) : best;
     }
-    const auto rounds = [at_once](int64_t n) { return (double)((n + at_once - 1) / at_once); };
-    double least = 0.95 * rounds(units) * (double)L;
+    double least = 0.95 * whole(1) * (double)L;
     for (int64_t n = 2; n <= 256 && n * linear::kSegment <= L; ++n) {
         const LinearPlan p = cut(n);
-        const double cost = (rounds(units * p.segments) + 0.3 * rounds(states * p.segments)) * (double)p.seg_tokens +
-                            300.0 + 20.0 * p.segments;
+        const double cost = (whole(p.segments) + states(p.segments)) * (double)p.seg_tokens + 12000.0 + 400.0 * p.segments;
         if (cost < least) {
             least = cost;
             best = p;
@@ -141,16 +156,23 @@ hipError_t join(float* states, const float* decay, const float* first, const Lin
     return launch_linear_join(j, stream);
 }
 
-int pad(int64_t width) { return width <= 64 ? 64 : width <= 128 ? 128 : 256; }
-
 }  // namespace
 
+// The launch of states alone does 0.45 of the work of one with outputs.
 LinearPlan plan_linear_fwd(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv, bool bf16) {
-    return plan(B * H * tiles_of(Dv), B * H * tiles_of(Dv), at_once(bf16, Dk), L);
+    const int64_t units = B * H * tiles_of(Dv);
+    const auto whole = [=](int64_t n) { return token_ns(units * n, Dk, bf16); };
+    return plan(units, L, whole, [=](int64_t n) { return 0.45 * whole(n); });
 }
 
+// dq and dk in one launch (for bf16 with split operands, a fifth more work), dv in another.
 LinearPlan plan_linear_bwd(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv, bool bf16) {
-    return plan(B * H * (2 * tiles_of(Dk) + tiles_of(Dv)), 2 * B * H * tiles_of(Dv), at_once(bf16, Dk > Dv ? Dk : Dv), L);
+    const int64_t of_keys = 2 * B * H * tiles_of(Dk), of_values = B * H * tiles_of(Dv);
+    return plan(of_keys + of_values, L,
+                [=](int64_t n) {
+                    return (bf16 ? 1.2 : 1.0) * token_ns(of_keys * n, Dv, bf16) + token_ns(of_values * n, Dk, bf16);
+                },
+                [=](int64_t n) { return 0.45 * token_ns(2 * of_values * n, Dk, bf16); });
 }
 
 size_t linear_fwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv, bool bf16) {
@@ -266,7 +288,7 @@ hipError_t launch_linear_bwd(const LinearBwdArgs& a, hipStream_t stream) {
     if (a.dg) {
         LinearDecayGrad g{};
         g.dot_q = ws.dot_q; g.dot_k = ws.dot_k;
-        g.q_tiles = g.k_tiles = (int)((f.Dk + 15) / 16);
+        g.tiles = (int)((f.Dk + 15) / 16);
         g.S = ws.S; g.S_last = ws.S_last; g.D = ws.D; g.D_last = a.dh_last;
         g.g = f.g; g.by_head = f.by_head;
         g.seq_lens = f.seq_lens;
@@ -285,7 +307,12 @@ hipError_t launch_linear_bwd(const LinearBwdArgs& a, hipStream_t stream) {
     return hipSuccess;
 }
 
-int64_t head_norm_groups(int64_t rows) { return rows < 1 ? 1 : rows < 1024 ? rows : 1024; }
+// Four workgroups to a CU; their shares of the weights' gradients take another launch to join.
+int64_t head_norm_group_rows(int64_t rows) { return rows < 1024 ? 1 : (rows + 1023) / 1024; }
+int64_t head_norm_groups(int64_t rows) {
+    const int64_t per = head_norm_group_rows(rows);
+    return rows < 1 ? 1 : (rows + per - 1) / per;
+}
 
 SlotsCut slots_cut(const SlotsArgs& a) {
     const uint64_t at = reinterpret_cast<uintptr_t>(a.pool) | (uint64_t)a.slot_bytes;

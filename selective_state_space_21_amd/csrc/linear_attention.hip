@@ -171,8 +171,8 @@ struct Terms {
     }
 };
 
-// Chunks whose decays are held: as many as wavefronts, which form one each, and the one in use.
-constexpr int kDecays = kWaves + 1;
+// Chunks whose decays are held: as many as wavefronts, which form one each, and those in use.
+constexpr int kDecays = kWaves + 1, kDecaysOfPairs = kWaves + 2;
 
 // Tokens of a chunk.
 template <typename T, int KD> constexpr int kChunk = sizeof(T) == 2 && KD <= 128 ? 64 : 32;
@@ -205,7 +205,7 @@ struct ScoreRows {
     }
 };
 
-template <typename T, int KD, bool STATES, int TERMS>
+template <typename T, int KD, int TERMS>
 struct Lds {
     static constexpr int C = kChunk<T, KD>;
     static constexpr int E = 16 / sizeof(T);                 // elements of a 16-byte piece
@@ -214,17 +214,16 @@ struct Lds {
     static constexpr int kValue = linear::kColumns + E;      // row stride
     // two of what the next chunk's scores and decays need while this one's are in use
     alignas(16) T K[2][C * Keys::kStride];
-    alignas(16) T Q[STATES ? 1 : 2][STATES ? E : C * Keys::kStride];
+    alignas(16) T Q[2][C * Keys::kStride];
     // values too where LDS holds them: they are then ready a phase earlier
-    static constexpr bool kEarly = STATES || (sizeof(T) == 2 ? KD == 64 || TERMS == 1 : KD <= 128);
+    static constexpr bool kEarly = sizeof(T) == 2 ? KD == 64 || TERMS == 1 : KD <= 128;
     alignas(16) T V[kEarly ? 2 : 1][C * kValue];
-    alignas(16) T P[STATES ? 1 : 2][TERMS][STATES ? E : C * Scores::kStride];   // scores, in terms
-    alignas(16) f32x4 through[STATES ? 1 : kGroups * C / 16 * 64];     // the state's part of the outputs
+    alignas(16) T P[2][TERMS][C * Scores::kStride];          // scores, in terms
+    alignas(16) f32x4 through[kGroups * C / 16 * 64];        // the state's part of the outputs
     alignas(16) float hi[kDecays][C];                        // log2 of the decay since the chunk's start
     alignas(16) float lo[kDecays][C];                        // as two floats
     alignas(16) float until[kDecays][C];                     // the decay until the chunk's end times `fresh`
     float whole[kDecays];                                    // the chunk's decay
-    double whole_log2[STATES ? kWaves : 1];
 };
 
 // A chunk's rows as 16-byte pieces, spread over the workgroup: piece m of a
@@ -241,10 +240,13 @@ struct Rows {
     int step;
     __device__ __forceinline__ static int row_of(int m, int tid) { return (tid + m * kThreads) / PER_ROW; }
     __device__ __forceinline__ static int col_of(int m, int tid) { return (tid + m * kThreads) % PER_ROW * E; }
-    // from `token0` of the tensor on, `row` elements between tokens, the first `width` of each
-    __device__ __forceinline__ void place(const T* tensor, int64_t token0, int64_t row, int width, bool rev, int tid) {
-        base = reinterpret_cast<const char*>(tensor + token0 * row);
+    // from `token0` of the tensor on, `row` elements between tokens, the first `width` of each; every `every`-th
+    // chunk from `first` on
+    __device__ __forceinline__ void place(const T* tensor, int64_t token0, int64_t row, int width, bool rev, int tid,
+                                          int first = 0, int every = 1) {
         step = (rev ? -C : C) * (int)row * (int)sizeof(T);
+        base = reinterpret_cast<const char*>(tensor + token0 * row) + first * step;
+        step *= every;
 #pragma unroll
         for (int m = 0; m < N; ++m) {
             const int t = row_of(m, tid), c = col_of(m, tid);
@@ -279,6 +281,80 @@ __device__ __forceinline__ float held(float x) { return __int_as_float(held(__fl
 // Loads before it are issued before it, whatever uses them comes after.
 __device__ __forceinline__ void issue_point() { __builtin_amdgcn_sched_barrier(0); }
 
+// A workgroup's tokens: of one head and segment, or of its columns of one.
+struct Span {
+    int64_t bh, b, len, from, last, to, token0;
+    int h, seg, tokens, chunks;
+    // Local row i of chunk c is token from + c C + i, or to - 1 - c C - i.
+    __device__ __forceinline__ Span(const LinearRun& run, int64_t head, int segment, bool rev, int C) {
+        seg = segment;
+        bh = head;
+        b = bh / run.H;
+        h = (int)(bh % run.H);
+        len = run.L;
+        if (run.seq_lens) {
+            const int64_t given = run.seq_lens[b];
+            len = given < 0 ? 0 : given < len ? given : len;
+        }
+        from = seg * run.seg_tokens;
+        last = from + run.seg_tokens < run.L ? from + run.seg_tokens : run.L;
+        to = last < len ? last : len;
+        tokens = to > from ? (int)(to - from) : 0;
+        chunks = (tokens + C - 1) / C;
+        token0 = rev ? to - C : from;                        // the lowest that a whole chunk 0 spans
+    }
+};
+
+// The decays of a chunk, a token to a lane of one wavefront: read well ahead, then summed.
+template <int C>
+struct Decays {
+    const float* g;
+    float x = 0.0f;
+    __device__ __forceinline__ Decays(const LinearRun& run, const Span& at)
+        : g(run.by_head ? run.g + at.h : run.g + at.b * run.L * run.H + at.h) {}
+    __device__ __forceinline__ void fetch(const LinearRun& run, const Span& span, bool rev, int chunk, int lane) {
+        const int at = chunk * C + lane;                     // local
+        x = 0.0f;
+        if (lane < C && at < span.tokens) {
+            const int64_t t = rev ? span.to - at : span.from + at;   // reversed: the g of the token behind
+            if (t < span.len) x = run.by_head ? g[0] : g[t * run.H];
+        }
+    }
+    // hi + lo: log2 of the decay since the chunk's start; until: the decay until its end times `fresh`; gives log2 of
+    // the chunk's decay
+    __device__ __forceinline__ double form(int lane, float fresh, float* hi, float* lo, float* until, float* whole) {
+        double y = (double)x * 1.4426950408889634074;
+        if (y < (double)kMinLog2) y = (double)kMinLog2;              // a NaN stays
+        const double sum = wave_sums(y, lane), end = from_lane(sum, 63);
+        if (lane < C) {
+            if (hi) {
+                const float f = (float)sum;
+                hi[lane] = f;
+                lo[lane] = (float)(sum - (double)f);
+            }
+            until[lane] = fast_exp2((float)(end - sum)) * fresh;
+        }
+        if (lane == 0) *whole = fast_exp2((float)end);
+        return end;
+    }
+};
+
+// The operands of a chunk's part of the state: four or eight rows of a key's column, rows of the values.
+template <typename T, typename Keys>
+__device__ __forceinline__ typename Mat<T>::Frag down_keys(const T* tile, int row, int c8, int w, int i) {
+    if constexpr (sizeof(T) == 2)
+        return Mat<T>::down(&tile[Keys::at(row + i / 4, c8 + i % 4) + 4 * w], &tile[Keys::at(row + 4 + i / 4, c8 + i % 4) + 4 * w]);
+    else
+        return Mat<T>::down(&tile[Keys::at(row, c8 + i / 4) + 4 * w + i % 4], Keys::kStride);
+}
+template <typename T, int STRIDE>
+__device__ __forceinline__ typename Mat<T>::Frag down_values(const T* at, int i) {
+    if constexpr (sizeof(T) == 2)
+        return Mat<T>::down(at + i / 4 * STRIDE + 4 * (i % 4), at + (4 + i / 4) * STRIDE + 4 * (i % 4));
+    else
+        return Mat<T>::down(at + i, STRIDE);
+}
+
 // One team keeps the state (products with the queries, then the update), the
 // other everything that does not touch it (staging, scores, outputs): a SIMD
 // has a wavefront of each, so the one's matrix products run beside the other's
@@ -286,12 +362,12 @@ __device__ __forceinline__ void issue_point() { __builtin_amdgcn_sched_barrier(0
 //   A  state: queries x state -> LDS            other: the last chunk's outputs to memory
 //      both: stage the next chunk, fetch the one behind it
 //   B  state: update                            other: the next chunk's scores, this one's outputs
-template <typename T, int KD, bool STATES, bool SPLIT>
+template <typename T, int KD, bool SPLIT>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && KD == 64 ? 4 : 2) void linear_chunks(LinearRun run) {
     using M = Mat<T>;
     using Frag = typename M::Frag;
     constexpr int TERMS = SPLIT && sizeof(T) == 2 ? 3 : 1;   // of the scores and of the state as an operand
-    using L = Lds<T, KD, STATES, TERMS>;
+    using L = Lds<T, KD, TERMS>;
     using Keys = typename L::Keys;
     using Scores = typename L::Scores;
     constexpr int C = L::C, RT = C / 16, KB = C / 32, KK = KD / 32;
@@ -305,59 +381,26 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && KD == 64 ? 4 : 2) void 
     const int64_t id = blockIdx.x / 8, unit = id / ctiles * 8 + blockIdx.x % 8;
     const int tile = (int)(id % ctiles);
     if (unit >= run.B * run.H * run.segments) return;
-    const int seg = (int)(unit % run.segments);
-    if (STATES && seg == (job.reversed ? 0 : run.segments - 1)) return;    // no segment takes its state
-    const int64_t bh = unit / run.segments, b = bh / run.H;
-    const int h = (int)(bh % run.H);
     const int lane = threadIdx.x % 64, i = lane % 16, g = lane / 16;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int group = wave % kGroups, tid = threadIdx.x;
     const bool keeps = wave < kGroups;                       // the state's team
     const bool rev = job.reversed;
+    const Span span(run, unit / run.segments, (int)(unit % run.segments), rev, C);
+    const int64_t bh = span.bh, b = span.b, len = span.len, token0 = span.token0;
+    const int h = span.h, seg = span.seg, tokens = span.tokens, chunks = span.chunks;
     const int kd = held(job.kd), vd = held(job.vd);
     const float inner = held(job.inner), outer = held(job.outer), fresh = held(job.fresh);
     const int col0 = tile * linear::kColumns;                // the workgroup's columns
     const int col = col0 + 16 * group;                       // the wavefront's
     const bool live = col < vd;
 
-    int64_t len = run.L;
-    if (run.seq_lens) {
-        const int64_t given = run.seq_lens[b];
-        len = given < 0 ? 0 : given < len ? given : len;
-    }
-    const int64_t from = seg * run.seg_tokens;
-    const int64_t last = from + run.seg_tokens < run.L ? from + run.seg_tokens : run.L;
-    const int64_t to = last < len ? last : len;
-    const int tokens = to > from ? (int)(to - from) : 0;
-    const int chunks = (tokens + C - 1) / C;
-    // Local row i of chunk c is token from + c C + i, or to - 1 - c C - i.
-    const int64_t token0 = rev ? to - C : from;              // the lowest that a whole chunk 0 spans
-    const float* gb = run.by_head ? run.g + h : run.g + b * run.L * run.H + h;
-
-    // The decays of chunks c .. c + 7, one to a wavefront: loaded well ahead.
-    float gr = 0.0f;
-    const auto fetch_decays = [&](int c) {
-        const int at = (c + wave) * C + lane;                // local
-        gr = 0.0f;
-        if (lane < C && at < tokens) {
-            const int64_t t = rev ? to - at : from + at;     // reversed: the g of the token behind
-            if (t < len) gr = run.by_head ? gb[0] : gb[t * run.H];
-        }
-    };
-    double seg_decay = 0.0;
+    // the decays of chunks c .. c + 7, one to a wavefront
+    Decays<C> decay_rows(run, span);
+    const auto fetch_decays = [&](int c) { decay_rows.fetch(run, span, rev, c + wave, lane); };
     const auto decays = [&](int c) {
         const int at = (c + wave) % kDecays;
-        double x = (double)gr * 1.4426950408889634074;
-        if (x < (double)kMinLog2) x = (double)kMinLog2;              // a NaN stays
-        const double sum = wave_sums(x, lane), all = from_lane(sum, 63);
-        if (lane < C) {
-            const float hi = (float)sum;
-            s.hi[at][lane] = hi;
-            s.lo[at][lane] = (float)(sum - (double)hi);
-            s.until[at][lane] = fast_exp2((float)(all - sum)) * fresh;
-        }
-        if (lane == 0) s.whole[at] = fast_exp2((float)all);
-        seg_decay += all;
+        decay_rows.form(lane, fresh, s.hi[at], s.lo[at], s.until[at], &s.whole[at]);
     };
     fetch_decays(0);
     int slot = 0, until_decays = kWaves - 1;
@@ -374,9 +417,8 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && KD == 64 ? 4 : 2) void 
 
     Rows<T, KD, C> qr, kr;
     Rows<T, linear::kColumns, C> vr;
-    if constexpr (!STATES)
-        qr.place(static_cast<const T*>(job.q) + b * run.L * job.q_row + (int64_t)(h / job.q_per) * kd, token0,
-                 job.q_row, kd, rev, tid);
+    qr.place(static_cast<const T*>(job.q) + b * run.L * job.q_row + (int64_t)(h / job.q_per) * kd, token0,
+             job.q_row, kd, rev, tid);
     kr.place(static_cast<const T*>(job.k) + b * run.L * job.k_row + (int64_t)(h / job.k_per) * kd, token0,
              job.k_row, kd, rev, tid);
     vr.place(static_cast<const T*>(job.v) + b * run.L * job.v_row + (int64_t)(h / job.v_per) * vd + col0, token0,
@@ -386,15 +428,15 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && KD == 64 ? 4 : 2) void 
     int left = tokens;                                       // from this chunk on
     const auto stage = [&](int next) {                       // the next chunk; its values, or this one's where LDS holds one chunk's
         vr.stage(s.V[L::kEarly ? next : 0], tid, value_place);
-        if constexpr (!STATES) qr.stage(s.Q[next], tid, key_place);
+        qr.stage(s.Q[next], tid, key_place);
         kr.stage(s.K[next], tid, key_place);
     };
     const auto fetch = [&] {
-        if constexpr (!STATES) qr.fetch(left - 2 * C, tid);
+        qr.fetch(left - 2 * C, tid);
         kr.fetch(left - 2 * C, tid);
         vr.fetch(left - (L::kEarly ? 2 : 1) * C, tid);
     };
-    if constexpr (!STATES) qr.fetch(tokens, tid);
+    qr.fetch(tokens, tid);
     kr.fetch(tokens, tid);
     vr.fetch(tokens, tid);
 
@@ -420,7 +462,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && KD == 64 ? 4 : 2) void 
     const auto start = [&](Score& x, int at, int slot, int idx) {
         const int it = (idx >= 1) + (idx >= 3) + (idx >= 6), jt = idx - it * (it + 1) / 2;
         x.query = 16 * it + i, x.key = 16 * jt + 4 * g;
-        load(x, s.K[at], s.Q[STATES ? 0 : at], 0);
+        load(x, s.K[at], s.Q[at], 0);
         x.hq = s.hi[slot][x.query], x.lq = s.lo[slot][x.query];
         x.hk = *reinterpret_cast<const f32x4*>(&s.hi[slot][x.key]);
         x.lk = *reinterpret_cast<const f32x4*>(&s.lo[slot][x.key]);
@@ -430,7 +472,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && KD == 64 ? 4 : 2) void 
 #pragma unroll
         for (int group = 0; group * GS < KK; ++group) {
             if (group > 0) {
-                load(x, s.K[at], s.Q[STATES ? 0 : at], group);
+                load(x, s.K[at], s.Q[at], group);
                 issue_point();
             }
 #pragma unroll
@@ -449,7 +491,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && KD == 64 ? 4 : 2) void 
         }
 #pragma unroll
         for (int n = 0; n < TERMS; ++n) {
-            T* p = &s.P[STATES ? 0 : at][n][Scores::at(x.query, x.key / 8) + x.key % 8];
+            T* p = &s.P[at][n][Scores::at(x.query, x.key / 8) + x.key % 8];
             if constexpr (sizeof(T) == 4) {
                 *reinterpret_cast<f32x4*>(p) = acc;
             } else {
@@ -463,7 +505,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && KD == 64 ? 4 : 2) void 
     };
     // the first chunk's rows and decays, and the fetch of the second's
     const auto prologue = [&] {
-        if constexpr (!STATES) {
+        {
             // the score tiles right of the diagonal that a block of 32 keys reaches are zero throughout
             for (int e = tid; e < RT / 2 * 256; e += kThreads) {
                 const int c = 32 * (e / 256) + 16 + e % 16;
@@ -506,14 +548,14 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && KD == 64 ? 4 : 2) void 
         constexpr int GQ = KK * RT * REGS <= QREGS ? KK : QREGS / (RT * REGS);
         constexpr int KREGS = KD == 256 ? 16 : 32;
         constexpr int GK = KK * 2 * KB * REGS <= KREGS ? KK : KREGS / (2 * KB * REGS);
-        Frag q[STATES ? 1 : GQ][RT], k[KB][GK][2];
+        Frag q[GQ][RT], k[KB][GK][2];
         const int along = Keys::at(i, g);
         const auto load_queries = [&](const T* tile, int k0) {
 #pragma unroll
             for (int kk = 0; kk < GQ; ++kk)
 #pragma unroll
                 for (int it = 0; it < RT; ++it)
-                    if (!STATES) q[kk][it] = M::along(&tile[along + 16 * it * Keys::kStride + 32 * (k0 + kk)]);
+                    q[kk][it] = M::along(&tile[along + 16 * it * Keys::kStride + 32 * (k0 + kk)]);
         };
         const auto load_keys = [&](const T* tile, int k0) {
 #pragma unroll
@@ -557,16 +599,10 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && KD == 64 ? 4 : 2) void 
                     for (int n = 0; n < Terms<T, 3>::kN; ++n) w[b2][n] = x.term[n];
                 }
             };
-            if constexpr (!STATES) {
-                load_queries(s.Q[now], 0);
-                if constexpr (L::kEarly) load_values();
-                issue_point();
-            }
-            if constexpr (STATES) {
-                stage(next);
-                fetch();
-            }
-            if constexpr (!STATES) {
+            load_queries(s.Q[now], 0);
+            if constexpr (L::kEarly) load_values();
+            issue_point();
+            {
                 f32x4 out[RT];
 #pragma unroll
                 for (int it = 0; it < RT; ++it) out[it] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -595,13 +631,12 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && KD == 64 ? 4 : 2) void 
                 if constexpr (L::kEarly) decay_values();
             }
             more_decays(c);
-            if constexpr (!STATES) lds_barrier();
+            lds_barrier();
 
-            if constexpr (STATES || !L::kEarly) load_values();
+            if constexpr (!L::kEarly) load_values();
             const float decay = s.whole[slot];
-            if constexpr (STATES) load_keys(s.K[now], 0);
             issue_point();
-            if constexpr (STATES || !L::kEarly) decay_values();
+            if constexpr (!L::kEarly) decay_values();
 #pragma unroll
             for (int k0 = 0; k0 < KK; k0 += GK) {
                 if (k0 > 0) {
@@ -627,7 +662,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && KD == 64 ? 4 : 2) void 
 #pragma unroll
                         for (int r = 0; r < 4; ++r) state[k0 + kk][x][r] = fmaf(state[k0 + kk][x][r], decay, add[kk][x][r]);
             }
-            if (!STATES && TILES > 2 * kGroups && 2 * kGroups + group < TILES) {
+            if (TILES > 2 * kGroups && 2 * kGroups + group < TILES) {
                 Score x;
                 start(x, next, next_of(slot), 2 * kGroups + group);
                 issue_point();
@@ -645,17 +680,14 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && KD == 64 ? 4 : 2) void 
 
         float* p = nullptr;
         float by = 1.0f;
-        if constexpr (STATES) {
-            p = run.seg_state[blockIdx.y] + unit * kd * vd;
-        } else if (job.state_out && seg == (rev ? 0 : run.segments - 1)) {
+        if (job.state_out && seg == (rev ? 0 : run.segments - 1)) {
             p = job.state_out + bh * job.out_head;
             if (job.decay_out && len > 0) {
-                const float x = gb[0] * kLog2e;
+                const float x = decay_rows.g[0] * kLog2e;
                 by = fast_exp2(x < kMinLog2 ? kMinLog2 : x);
             }
         }
         if (p && live) {
-            const int64_t sk = STATES ? vd : job.sk, sv = STATES ? 1 : job.sv;
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
@@ -663,7 +695,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && KD == 64 ? 4 : 2) void 
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const int row = 32 * kk + 8 * g + 4 * u + r;
-                        if (row < kd) p[row * sk + (col + i) * sv] = state[kk][u][r] * by;
+                        if (row < kd) p[(int64_t)row * job.sk + (int64_t)(col + i) * job.sv] = state[kk][u][r] * by;
                     }
         }
     } else {
@@ -680,7 +712,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && KD == 64 ? 4 : 2) void 
         const char* dot_base = nullptr;
         float* dots = nullptr;
         int out_step = 0, dot_step = 0;
-        if constexpr (!STATES) {
+        {
 #pragma unroll
             for (int it = 0; it < RT; ++it) {
                 const int row = 16 * it + i, t = rev ? C - 1 - row : row;
@@ -700,7 +732,6 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && KD == 64 ? 4 : 2) void 
 
         if (chunks > 0) {
             prologue();
-            if constexpr (!STATES)
 #pragma unroll
                 for (int m = 0; m < MOST; ++m)
                     if (has(m)) {
@@ -737,11 +768,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && KD == 64 ? 4 : 2) void 
         };
         const auto step = [&](auto parity, int c) {
             constexpr int now = decltype(parity)::value, next = now ^ 1;
-            if constexpr (STATES) {
-                stage(next);
-                fetch();
-                more_decays(c);
-            } else {
+            {
                 stage(next);
                 issue_point();
                 if (c > 0) store(left + C);
@@ -830,11 +857,11 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && KD == 64 ? 4 : 2) void 
             step(std::integral_constant<int, 0>{}, c);
             if (c + 1 < chunks) step(std::integral_constant<int, 1>{}, c + 1);
         }
-        if (!STATES && chunks > 0) store(left + C);
-        if (!STATES && job.zero_tail) {
+        if (chunks > 0) store(left + C);
+        if (job.zero_tail) {
             const int width = vd - col0 < linear::kColumns ? vd - col0 : linear::kColumns;
-            const int64_t first = from > len ? from : len;
-            for (int64_t t = first + group; t < last; t += kGroups) {
+            const int64_t first = span.from > len ? span.from : len;
+            for (int64_t t = first + group; t < span.last; t += kGroups) {
                 const int64_t at = ((b * run.L + t) * run.H + h) * vd + col0 + lane;
                 if (lane < width) {
                     if (wide) static_cast<float*>(job.out)[at] = 0.0f;
@@ -843,14 +870,204 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && KD == 64 ? 4 : 2) void 
             }
         }
     }
-    if constexpr (STATES) {                                  // each wavefront has summed the chunks that it formed
-        if (lane == 0) s.whole_log2[wave] = seg_decay;
-        lds_barrier();
-        if (tile == 0 && threadIdx.x == 0) {
-            double all = 0.0;
-            for (int w = 0; w < kWaves; ++w) all += s.whole_log2[w];
-            run.seg_decay[blockIdx.y][unit] = (float)all;
+}
+
+// LDS of a pass over the states alone, two chunks at a time.
+template <typename T, int KD>
+struct StatesLds {
+    static constexpr int C = kChunk<T, KD>;
+    using Keys = KeyRows<T, KD>;
+    static constexpr int kValue = linear::kColumns + 16 / sizeof(T);
+    // two pairs of chunks where LDS holds them: the next one's rows are then written beside this one's products
+    static constexpr int kPairs = sizeof(T) == 4 && KD == 256 ? 1 : 2;
+    alignas(16) T K[kPairs][2][C * Keys::kStride];
+    alignas(16) T V[kPairs][2][C * kValue];
+    alignas(16) float until[kDecaysOfPairs][C];
+    float whole[kDecaysOfPairs];
+    double whole_log2[kWaves];
+};
+
+// The states of the segments alone, S = sum_j e^{G_end - G_j} k_j v_j^T: the
+// first pass over a sequence that is cut.  There are no outputs: both teams
+// keep states, of half the keys each, and take two chunks between barriers.
+template <typename T, int KD>
+__global__ __launch_bounds__(kThreads, sizeof(T) == 4 && KD == 64 ? 4 : 2) void linear_states(LinearRun run) {
+    using M = Mat<T>;
+    using Frag = typename M::Frag;
+    using L = StatesLds<T, KD>;
+    using Keys = typename L::Keys;
+    constexpr int C = L::C, KB = C / 32, KK = KD / 64;       // blocks of 32 keys of a wavefront
+    __shared__ L s;
+
+    const LinearJob& job = run.job[blockIdx.y];
+    const int ctiles = (job.vd + linear::kColumns - 1) / linear::kColumns;
+    const int64_t id = blockIdx.x / 8, nth = id / ctiles * 8 + blockIdx.x % 8;
+    const int tile = (int)(id % ctiles);
+    // the last segment's state goes into none: it has no workgroup
+    const int segments = run.segments - 1;
+    if (nth >= run.B * run.H * segments) return;
+    const bool rev = job.reversed;
+    const Span span(run, nth / segments, (int)(nth % segments) + (rev ? 1 : 0), rev, C);
+    const int64_t unit = span.bh * run.segments + span.seg;
+    const int tid = threadIdx.x, lane = tid % 64, i = lane % 16, g = lane / 16;
+    const int wave = __builtin_amdgcn_readfirstlane(tid / 64), group = wave % kGroups;
+    const int key0 = wave / kGroups * KK;
+    const int kd = held(job.kd), vd = held(job.vd);
+    const float fresh = held(job.fresh);
+    const int col0 = tile * linear::kColumns, col = col0 + 16 * group;
+
+    Decays<C> decay_rows(run, span);
+    Rows<T, KD, C> kr[2];
+    Rows<T, linear::kColumns, C> vr[2];
+    int left = span.tokens;
+    const auto fetch = [&](int ahead) {                      // the pair `ahead` chunks on
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            kr[n].fetch(left - (ahead + n) * C, tid);
+            vr[n].fetch(left - (ahead + n) * C, tid);
         }
+    };
+    const auto stage = [&](int at) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            vr[n].stage(s.V[at][n], tid, [](int row, int c) { return row * L::kValue + c; });
+            kr[n].stage(s.K[at][n], tid, [](int row, int c) { return Keys::piece(row, c); });
+        }
+    };
+    double seg_decay = 0.0;
+    const auto decays = [&](int c) {
+        const int at = (c + wave) % kDecaysOfPairs;
+        seg_decay += decay_rows.form(lane, fresh, nullptr, nullptr, s.until[at], &s.whole[at]);
+    };
+    f32x4 state[KK][2];
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) state[kk][0] = state[kk][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    constexpr int REGS = sizeof(T) == 2 ? 4 : 8, KREGS = 32;
+    constexpr int GK = KK * 2 * KB * REGS <= KREGS ? KK : KREGS / (2 * KB * REGS);
+    struct Chunk {
+        Frag v[KB], k[KB][GK][2];
+        f32x4 u[KB][2];
+        float decay;
+    };
+    const auto load_keys = [&](Chunk& x, const T* K, int k0) {
+#pragma unroll
+        for (int b2 = 0; b2 < KB; ++b2)
+#pragma unroll
+            for (int kk = 0; kk < GK; ++kk)
+#pragma unroll
+                for (int w = 0; w < 2; ++w) x.k[b2][kk][w] = down_keys<T, Keys>(K, 32 * b2 + 8 * g, 4 * (key0 + k0 + kk), w, i);
+    };
+    const auto load = [&](Chunk& x, const T* K, const T* V, int slot) {
+#pragma unroll
+        for (int b2 = 0; b2 < KB; ++b2) {
+            x.v[b2] = down_values<T, L::kValue>(&V[(32 * b2 + 8 * g) * L::kValue + 16 * group], i);
+            x.u[b2][0] = *reinterpret_cast<const f32x4*>(&s.until[slot][32 * b2 + 8 * g]);
+            x.u[b2][1] = *reinterpret_cast<const f32x4*>(&s.until[slot][32 * b2 + 8 * g + 4]);
+        }
+        x.decay = s.whole[slot];
+        load_keys(x, K, 0);
+    };
+    const auto update = [&](Chunk& x, const T* K) {
+        Frag w[KB][Terms<T, 3>::kN];                         // the values, decayed to the chunk's end
+#pragma unroll
+        for (int b2 = 0; b2 < KB; ++b2) {
+            const Terms<T, 3> y(M::widen(x.v[b2]) * __builtin_shufflevector(x.u[b2][0], x.u[b2][1], 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+            for (int n = 0; n < Terms<T, 3>::kN; ++n) w[b2][n] = y.term[n];
+        }
+#pragma unroll
+        for (int k0 = 0; k0 < KK; k0 += GK) {
+            if (k0 > 0) {
+                load_keys(x, K, k0);
+                issue_point();
+            }
+            f32x4 add[GK][2];                                // summed by themselves, as where outputs are formed
+#pragma unroll
+            for (int kk = 0; kk < GK; ++kk) add[kk][0] = add[kk][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int b2 = 0; b2 < KB; ++b2)
+#pragma unroll
+                for (int n = Terms<T, 3>::kN - 1; n >= 0; --n)
+#pragma unroll
+                    for (int kk = 0; kk < GK; ++kk)
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) add[kk][m] = M::mma(x.k[b2][kk][m], w[b2][n], add[kk][m]);
+#pragma unroll
+            for (int kk = 0; kk < GK; ++kk)
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) state[k0 + kk][m][r] = fmaf(state[k0 + kk][m][r], x.decay, add[kk][m][r]);
+        }
+    };
+
+    int slot = 0, until_decays = kWaves / 2 - 1;
+    const auto step = [&](auto parity, int c) {
+        constexpr int now = L::kPairs == 2 ? decltype(parity)::value : 0, next = L::kPairs == 2 ? now ^ 1 : 0;
+        const int second = slot + 1 == kDecaysOfPairs ? 0 : slot + 1;
+        Chunk x, y;
+        load(x, s.K[now][0], s.V[now][0], slot);
+        issue_point();
+        if constexpr (L::kPairs == 2) {
+            stage(next);
+            fetch(4);
+        }
+        update(x, s.K[now][0]);
+        load(y, s.K[now][1], s.V[now][1], second);
+        issue_point();
+        if (until_decays == 0) {                             // the next pair's are not there
+            decays(c + 2);
+            decay_rows.fetch(run, span, rev, c + 2 + kWaves + wave, lane);
+            until_decays = kWaves / 2;
+        }
+        --until_decays;
+        update(y, s.K[now][1]);
+        if constexpr (L::kPairs == 1) {
+            lds_barrier();
+            stage(next);
+            fetch(4);
+        }
+        lds_barrier();
+        slot = second + 1 == kDecaysOfPairs ? 0 : second + 1;
+        left -= 2 * C;
+    };
+    if (span.chunks > 0) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            kr[n].place(static_cast<const T*>(job.k) + span.b * run.L * job.k_row + (int64_t)(span.h / job.k_per) * kd,
+                        span.token0, job.k_row, kd, rev, tid, n, 2);
+            vr[n].place(static_cast<const T*>(job.v) + span.b * run.L * job.v_row + (int64_t)(span.h / job.v_per) * vd + col0,
+                        span.token0, job.v_row, vd - col0, rev, tid, n, 2);
+        }
+        decay_rows.fetch(run, span, rev, wave, lane);
+        fetch(0);
+        decays(0);
+        decay_rows.fetch(run, span, rev, kWaves + wave, lane);
+        stage(0);
+        fetch(2);
+        lds_barrier();
+    }
+    for (int c = 0; c < span.chunks; c += 4) {
+        step(std::integral_constant<int, 0>{}, c);
+        if (c + 2 < span.chunks) step(std::integral_constant<int, 1>{}, c + 2);
+    }
+
+    if (col < vd) {
+        float* p = run.seg_state[blockIdx.y] + unit * kd * vd;
+#pragma unroll
+        for (int n = 0; n < 2 * KK; ++n)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 32 * (key0 + n / 2) + 8 * g + 4 * (n % 2) + r;
+                if (row < kd) p[(int64_t)row * vd + col + i] = state[n / 2][n % 2][r];
+            }
+    }
+    if (lane == 0) s.whole_log2[wave] = seg_decay;           // each wavefront has summed the chunks that it formed
+    lds_barrier();
+    if (tile == 0 && tid == 0) {
+        double all = 0.0;
+        for (int w = 0; w < kWaves; ++w) all += s.whole_log2[w];
+        run.seg_decay[blockIdx.y][unit] = (float)all;
     }
 }
 
@@ -862,11 +1079,11 @@ hipError_t launch_width(const LinearRun& r, bool states_only, hipStream_t stream
         tiles = n > tiles ? n : tiles;
     }
     // jobs of fewer tiles leave the last workgroups without a unit
-    const int64_t units = (r.B * r.H * r.segments + 7) / 8 * 8;
+    const int64_t units = (r.B * r.H * (states_only ? r.segments - 1 : r.segments) + 7) / 8 * 8;
     const dim3 grid((unsigned)(units * tiles), (unsigned)r.jobs);
-    if (states_only) linear_chunks<T, KD, true, false><<<grid, kThreads, 0, stream>>>(r);
-    else if (sizeof(T) == 2 && r.split) linear_chunks<T, KD, false, sizeof(T) == 2><<<grid, kThreads, 0, stream>>>(r);
-    else linear_chunks<T, KD, false, false><<<grid, kThreads, 0, stream>>>(r);
+    if (states_only) linear_states<T, KD><<<grid, kThreads, 0, stream>>>(r);
+    else if (sizeof(T) == 2 && r.split) linear_chunks<T, KD, sizeof(T) == 2><<<grid, kThreads, 0, stream>>>(r);
+    else linear_chunks<T, KD, false><<<grid, kThreads, 0, stream>>>(r);
     return hipGetLastError();
 }
 

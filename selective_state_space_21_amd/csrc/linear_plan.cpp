@@ -158,11 +158,11 @@ hipError_t join(float* states, const float* decay, const float* first, const Lin
 
 }  // namespace
 
-// The launch of states alone does 0.45 of the work of one with outputs.
+// The launch of states alone does half of the work of one with outputs, for all segments but one.
 LinearPlan plan_linear_fwd(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv, bool bf16) {
     const int64_t units = B * H * tiles_of(Dv);
     const auto whole = [=](int64_t n) { return token_ns(units * n, Dk, bf16); };
-    return plan(units, L, whole, [=](int64_t n) { return 0.45 * whole(n); });
+    return plan(units, L, whole, [=](int64_t n) { return 0.5 * whole(n - 1); });
 }
 
 // dq and dk in one launch (for bf16 with split operands, a fifth more work), dv in another.
@@ -172,7 +172,7 @@ LinearPlan plan_linear_bwd(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t 
                 [=](int64_t n) {
                     return (bf16 ? 1.2 : 1.0) * token_ns(of_keys * n, Dv, bf16) + token_ns(of_values * n, Dk, bf16);
                 },
-                [=](int64_t n) { return 0.45 * token_ns(2 * of_values * n, Dk, bf16); });
+                [=](int64_t n) { return 0.5 * token_ns(2 * of_values * (n - 1), Dk, bf16); });
 }
 
 size_t linear_fwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv, bool bf16) {

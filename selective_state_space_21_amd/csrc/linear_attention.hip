@@ -58,7 +58,7 @@ typedef float f32x8 __attribute__((ext_vector_type(8)));
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kThreads = 512, kWaves = 8;
+constexpr int kThreads = 512, kWaves = 8, kTeam = kThreads / 2;
 constexpr int kGroups = linear::kColumns / 16;    // each team has a wavefront to 16 columns
 constexpr uint32_t kNoOffset = 0x80000000u;      // past every resource's end: loads give zeros
 constexpr uint32_t kRecords = 0x7ffffff0u;
@@ -230,16 +230,16 @@ struct Lds {
 // thread holds 16 bytes of local row t.  Rows are addressed from the lowest of
 // the C tokens that a whole chunk spans, and the address moves on by a chunk a
 // fetch: a chunk past the end has no rows and reads nothing.
-template <typename T, int WIDTH, int C>
+template <typename T, int WIDTH, int C, int THREADS>
 struct Rows {
     static constexpr int E = 16 / sizeof(T), PER_ROW = WIDTH / E, ALL = C * PER_ROW;
-    static constexpr int N = (ALL + kThreads - 1) / kThreads;
+    static constexpr int N = (ALL + THREADS - 1) / THREADS;
     u32x4 piece[N];
     uint32_t at[N];
     const char* base;
     int step;
-    __device__ __forceinline__ static int row_of(int m, int tid) { return (tid + m * kThreads) / PER_ROW; }
-    __device__ __forceinline__ static int col_of(int m, int tid) { return (tid + m * kThreads) % PER_ROW * E; }
+    __device__ __forceinline__ static int row_of(int m, int tid) { return (tid + m * THREADS) / PER_ROW; }
+    __device__ __forceinline__ static int col_of(int m, int tid) { return (tid + m * THREADS) % PER_ROW * E; }
     // from `token0` of the tensor on, `row` elements between tokens, the first `width` of each; every `every`-th
     // chunk from `first` on
     __device__ __forceinline__ void place(const T* tensor, int64_t token0, int64_t row, int width, bool rev, int tid,
@@ -265,7 +265,7 @@ struct Rows {
 #pragma unroll
         for (int m = 0; m < N; ++m) {
             const int t = row_of(m, tid);
-            if (ALL % kThreads == 0 || t < C) *reinterpret_cast<u32x4*>(&tile[place(t, col_of(m, tid))]) = piece[m];
+            if (ALL % THREADS == 0 || t < C) *reinterpret_cast<u32x4*>(&tile[place(t, col_of(m, tid))]) = piece[m];
         }
     }
 };
@@ -383,7 +383,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && KD == 64 ? 4 : 2) void 
     if (unit >= run.B * run.H * run.segments) return;
     const int lane = threadIdx.x % 64, i = lane % 16, g = lane / 16;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int group = wave % kGroups, tid = threadIdx.x;
+    const int group = wave % kGroups, tid = threadIdx.x, mate = tid % kTeam;
     const bool keeps = wave < kGroups;                       // the state's team
     const bool rev = job.reversed;
     const Span span(run, unit / run.segments, (int)(unit % run.segments), rev, C);
@@ -415,30 +415,16 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && KD == 64 ? 4 : 2) void 
     };
     const auto next_of = [](int n) { return n + 1 == kDecays ? 0 : n + 1; };
 
-    Rows<T, KD, C> qr, kr;
-    Rows<T, linear::kColumns, C> vr;
-    qr.place(static_cast<const T*>(job.q) + b * run.L * job.q_row + (int64_t)(h / job.q_per) * kd, token0,
-             job.q_row, kd, rev, tid);
-    kr.place(static_cast<const T*>(job.k) + b * run.L * job.k_row + (int64_t)(h / job.k_per) * kd, token0,
-             job.k_row, kd, rev, tid);
-    vr.place(static_cast<const T*>(job.v) + b * run.L * job.v_row + (int64_t)(h / job.v_per) * vd + col0, token0,
-             job.v_row, vd - col0, rev, tid);
+    // The state's team brings the values, the other the queries; the keys whichever has less to do otherwise.
+    constexpr bool KEYS_BY_STATE = TERMS > 1;
+    Rows<T, KD, C, kTeam> kr;
+    const auto place_keys = [&] {
+        kr.place(static_cast<const T*>(job.k) + b * run.L * job.k_row + (int64_t)(h / job.k_per) * kd, token0, job.k_row,
+                 kd, rev, mate);
+    };
     const auto key_place = [](int row, int col) { return Keys::piece(row, col); };
     const auto value_place = [](int row, int col) { return row * L::kValue + col; };
     int left = tokens;                                       // from this chunk on
-    const auto stage = [&](int next) {                       // the next chunk; its values, or this one's where LDS holds one chunk's
-        vr.stage(s.V[L::kEarly ? next : 0], tid, value_place);
-        qr.stage(s.Q[next], tid, key_place);
-        kr.stage(s.K[next], tid, key_place);
-    };
-    const auto fetch = [&] {
-        qr.fetch(left - 2 * C, tid);
-        kr.fetch(left - 2 * C, tid);
-        vr.fetch(left - (L::kEarly ? 2 : 1) * C, tid);
-    };
-    qr.fetch(tokens, tid);
-    kr.fetch(tokens, tid);
-    vr.fetch(tokens, tid);
 
     // A chunk's scores, transposed: a lane has four keys of one query.  The operands come in groups,
     // each on its way before the first of it is used.
@@ -503,31 +489,29 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && KD == 64 ? 4 : 2) void 
             }
         }
     };
-    // the first chunk's rows and decays, and the fetch of the second's
-    const auto prologue = [&] {
-        {
-            // the score tiles right of the diagonal that a block of 32 keys reaches are zero throughout
-            for (int e = tid; e < RT / 2 * 256; e += kThreads) {
-                const int c = 32 * (e / 256) + 16 + e % 16;
-                const int at = Scores::at(32 * (e / 256) + e % 256 / 16, c / 8) + c % 8;
+    // the score tiles right of the diagonal that a block of 32 keys reaches are zero throughout
+    const auto clear_scores = [&] {
+        for (int e = tid; e < RT / 2 * 256; e += kThreads) {
+            const int c = 32 * (e / 256) + 16 + e % 16;
+            const int at = Scores::at(32 * (e / 256) + e % 256 / 16, c / 8) + c % 8;
 #pragma unroll
-                for (int n = 0; n < 2 * TERMS; ++n) s.P[n % 2][n / 2][at] = T(0);
-            }
-            qr.stage(s.Q[0], tid, key_place);
-            qr.fetch(tokens - C, tid);
+            for (int n = 0; n < 2 * TERMS; ++n) s.P[n % 2][n / 2][at] = T(0);
         }
-        kr.stage(s.K[0], tid, key_place);
-        kr.fetch(tokens - C, tid);
-        if constexpr (L::kEarly) {
-            vr.stage(s.V[0], tid, value_place);
-            vr.fetch(tokens - C, tid);
-        }
+    };
+    const auto first_decays = [&] {
         decays(0);
         fetch_decays(kWaves);
-        lds_barrier();
     };
 
     if (keeps) {
+        Rows<T, linear::kColumns, C, kTeam> vr;
+        vr.place(static_cast<const T*>(job.v) + b * run.L * job.v_row + (int64_t)(h / job.v_per) * vd + col0, token0,
+                 job.v_row, vd - col0, rev, mate);
+        if constexpr (KEYS_BY_STATE) {
+            place_keys();
+            kr.fetch(tokens, mate);
+        }
+        vr.fetch(tokens, mate);
         f32x4 state[KK][2];
         {
             const float* p = job.state_in ? job.state_in + bh * job.in_head + seg * job.in_seg : nullptr;
@@ -572,7 +556,19 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && KD == 64 ? 4 : 2) void 
                             k[b2][kk][w] = M::down(&tile[Keys::at(row, c8 + i / 4) + 4 * w + i % 4], Keys::kStride);
                     }
         };
-        if (chunks > 0) prologue();
+        if (chunks > 0) {
+            clear_scores();
+            if constexpr (KEYS_BY_STATE) {
+                kr.stage(s.K[0], mate, key_place);
+                kr.fetch(tokens - C, mate);
+            }
+            if constexpr (L::kEarly) {
+                vr.stage(s.V[0], mate, value_place);
+                vr.fetch(tokens - C, mate);
+            }
+            first_decays();
+            lds_barrier();
+        }
         const auto step = [&](auto parity, int c) {
             constexpr int now = decltype(parity)::value, next = now ^ 1;
             const T* V = s.V[L::kEarly ? now : 0];
@@ -626,8 +622,13 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && KD == 64 ? 4 : 2) void 
                 for (int it = 0; it < RT; ++it) s.through[(group * RT + it) * 64 + lane] = out[it];
                 load_keys(s.K[now], 0);
                 issue_point();
-                stage(next);
-                fetch();
+                // the next chunk's values, or this one's where LDS holds one chunk's
+                vr.stage(s.V[L::kEarly ? next : 0], mate, value_place);
+                if constexpr (KEYS_BY_STATE) {
+                    kr.stage(s.K[next], mate, key_place);
+                    kr.fetch(left - 2 * C, mate);
+                }
+                vr.fetch(left - (L::kEarly ? 2 : 1) * C, mate);
                 if constexpr (L::kEarly) decay_values();
             }
             more_decays(c);
@@ -730,8 +731,25 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && KD == 64 ? 4 : 2) void 
             }
         }
 
+        Rows<T, KD, C, kTeam> qr;
+        qr.place(static_cast<const T*>(job.q) + b * run.L * job.q_row + (int64_t)(h / job.q_per) * kd, token0, job.q_row,
+                 kd, rev, mate);
+        if constexpr (!KEYS_BY_STATE) place_keys();
+        const auto stage = [&](int at) {
+            qr.stage(s.Q[at], mate, key_place);
+            if constexpr (!KEYS_BY_STATE) kr.stage(s.K[at], mate, key_place);
+        };
+        const auto fetch = [&](int rows) {
+            qr.fetch(rows, mate);
+            if constexpr (!KEYS_BY_STATE) kr.fetch(rows, mate);
+        };
+        fetch(tokens);
         if (chunks > 0) {
-            prologue();
+            clear_scores();
+            stage(0);
+            fetch(tokens - C);
+            first_decays();
+            lds_barrier();
 #pragma unroll
                 for (int m = 0; m < MOST; ++m)
                     if (has(m)) {
@@ -788,7 +806,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && KD == 64 ? 4 : 2) void 
                     }
                 }
                 issue_point();
-                fetch();
+                fetch(left - 2 * C);
                 more_decays(c);
                 lds_barrier();   // the state's part, this chunk's values and scores, the next one's rows are there
 
@@ -917,8 +935,8 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && KD == 64 ? 4 : 2) void 
     const int col0 = tile * linear::kColumns, col = col0 + 16 * group;
 
     Decays<C> decay_rows(run, span);
-    Rows<T, KD, C> kr[2];
-    Rows<T, linear::kColumns, C> vr[2];
+    Rows<T, KD, C, kThreads> kr[2];
+    Rows<T, linear::kColumns, C, kThreads> vr[2];
     int left = span.tokens;
     const auto fetch = [&](int ahead) {                      // the pair `ahead` chunks on
 #pragma unroll

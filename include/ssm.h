@@ -634,13 +634,14 @@ int ssm_layer_norm_bwd(const void* x, int x_dtype, const void* dy, const float* 
  *                tokens (clamped to [0, L]); the padding is not read, o there is
  *                left untouched, h_last is the state after the row's last token
  *   Dk, Dv multiples of 16, at most 256; H a multiple of G, at most 2^14;
- *   B * H at most 2^21; L at most 2^30.
+ *   B * H at most 2^20; L at most 2^30.
  *
- * Tokens are taken in chunks (64 bf16, 32 fp32) as masked products on the
- * matrix cores, the fp32 state carried between them: an infinity or NaN in a
- * token's v may make NaN of the same chunk's earlier tokens' outputs too.
- * For bf16, scores and state are rounded to bf16 as operands; what enters the
- * state is not (it keeps 2^-18).  With few heads long sequences are cut into
+ * Tokens are taken in chunks (64 for bf16 rows of up to 128 elements, else 32)
+ * as masked products on the matrix cores, the fp32 state carried between them:
+ * an infinity or NaN in a token's v may make NaN of the same chunk's earlier
+ * tokens' outputs too.  For bf16, scores and state are rounded to bf16 as
+ * operands of bf16 outputs; what enters the state is not (three bf16 terms,
+ * 2^-26).  With few heads long sequences are cut into
  * segments whose states are formed first; ssm_linear_attention_segments (and
  * _bwd_segments) return their number, a pure function of the sizes; the
  * environment variable SSM_LINEAR_SEGMENTS (1..256) overrides it for queries

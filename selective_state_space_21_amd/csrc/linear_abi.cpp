@@ -32,7 +32,7 @@ template <size_t N> bool all_aligned(const void* const (&ptrs)[N], uintptr_t a) 
 bool is_dtype(int dtype) { return dtype == SSM_F32 || dtype == SSM_BF16; }
 int status(hipError_t e) { return e == hipSuccess ? SSM_OK : SSM_ERR_HIP; }
 
-// rows of a launch of 256 threads each that go out as one
+// workgroups of 256 threads that go out as one launch
 constexpr int64_t kMaxBlocks = int64_t(1) << 24;
 
 int linear_check_sizes(int64_t B, int64_t L, int64_t H, int64_t G, int64_t Dk, int64_t Dv, int dtype) {
@@ -43,8 +43,8 @@ int linear_check_sizes(int64_t B, int64_t L, int64_t H, int64_t G, int64_t Dk, i
         return SSM_ERR_BAD_SHAPE;
     if (Dk % 16 || Dv % 16 || Dk > ssm::linear::kMaxWidth || Dv > ssm::linear::kMaxWidth) return SSM_ERR_UNSUPPORTED;
     if (H * ssm::linear::kMaxWidth > ssm::linear::kMaxRow) return SSM_ERR_UNSUPPORTED;
-    // a head of a row, up to four column tiles and a segment each, in one launch
-    if (B * H > kMaxBlocks / 8 || L > (int64_t(1) << 30)) return SSM_ERR_UNSUPPORTED;
+    // a head of a row has up to four column tiles of 512 threads, in one launch of less than 2^32
+    if (B * H > kMaxBlocks / 16 || L > (int64_t(1) << 30)) return SSM_ERR_UNSUPPORTED;
     return SSM_OK;
 }
 

@@ -11,13 +11,13 @@
 //   dv: q <- k, k <- q, v <- do and dk: q <- v, k <- do, v <- q, from the last
 //   token to the first (there token t enters with g of token t + 1).
 //
-// Work mapping: a workgroup of four wavefronts walks the chunks of one head
-// (or of one segment of it) with 64 columns of the state, 16 to a wavefront,
-// in fp32 matrix accumulators.  Every wavefront forms the outputs of all C
-// tokens for its columns, so the state never leaves its registers: the
-// accumulators' rows are laid out so that they are the next product's operand
-// as they stand (below).  The scores are shared through LDS.  The next chunk's
-// rows are on their way while this one is computed.
+// Work mapping: a workgroup of eight wavefronts walks the chunks of one head
+// (or of one segment of it) with 64 columns of the state.  Four of them keep
+// the state, 16 columns each in fp32 matrix accumulators, which are laid out so
+// that they are the next product's operand as they stand (below): the state
+// never leaves its registers.  The other four form scores and outputs.  Rows,
+// scores and the state's part of the outputs are handed over in LDS, two copies
+// of each, while the rows behind them are on their way.
 //
 // Products are v_mfma_f32_16x16x32_bf16, or eight v_mfma_f32_16x16x4_f32 for
 // fp32 (element j of every lane's eight makes one of them).  Lane l with
@@ -29,11 +29,19 @@
 // A operand of the product with the queries as it stands.
 //
 // Rounding: exponent sums are fp64 and kept as two floats, differences are
-// taken of those.  For bf16 the decayed values of the state update are split
-// in two bf16 halves (the fp32 state is then off by 2^-18 a term, not 2^-9).
-// The scores and the state as an operand are rounded to one bf16 where only
-// bf16 outputs come of them, like the outputs themselves, and split too where
-// the decay's gradient, an fp32 sum over tokens, is formed (`split`).
+// taken of those.  For bf16 the decayed values of the state update are three
+// bf16 terms each (2^-26 of a value; two, 2^-17, were measured at 2.3e-6 of the
+// state against 1.0e-7 now).  The scores and the state as an operand are rounded
+// to one bf16, 2^-9, where only bf16 outputs come of them, like the outputs
+// themselves, and are three terms too where the decay's gradient, an fp32 sum
+// over tokens, is formed (`split`).
+//
+// Bound: neither the matrix cores (a quarter busy) nor LDS nor HBM, but the
+// length of a chunk's dependent steps between its two barriers with one
+// workgroup a CU: 2.2 us per 64 tokens of 128x64 bf16 alone, 2.9 with all CUs
+// at work (64x64: 1.6, 2.2, then at 80% of the copy rate).  Tried and slower:
+// chunks of 32 tokens, wavefronts that each form all outputs of 16 columns,
+// eight of those with half the rows each.
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>
@@ -359,9 +367,11 @@ __device__ __forceinline__ typename Mat<T>::Frag down_values(const T* at, int i)
 // other everything that does not touch it (staging, scores, outputs): a SIMD
 // has a wavefront of each, so the one's matrix products run beside the other's
 // exponentials, and nothing is formed twice.  Two barriers a chunk:
-//   A  state: queries x state -> LDS            other: the last chunk's outputs to memory
-//      both: stage the next chunk, fetch the one behind it
-//   B  state: update                            other: the next chunk's scores, this one's outputs
+//   A  state: queries x state -> LDS, values      other: queries, keys, the last chunk's outputs to memory
+//      (rows: stage the next chunk's, fetch those behind them)
+//   B  state: update                              other: the next chunk's scores, this one's outputs
+// Measured: B=8 L=2048 H=16 128x128 bf16 89 us a call (3.0 TB/s of its 271 MB; 107 with the scores finished in one
+// piece, 142 with one copy of the rows), with split operands 62 us a thousand tokens of 256 workgroups.
 template <typename T, int KD, bool SPLIT>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && KD == 64 ? 4 : 2) void linear_chunks(LinearRun run) {
     using M = Mat<T>;
@@ -908,6 +918,8 @@ struct StatesLds {
 // The states of the segments alone, S = sum_j e^{G_end - G_j} k_j v_j^T: the
 // first pass over a sequence that is cut.  There are no outputs: both teams
 // keep states, of half the keys each, and take two chunks between barriers.
+// Bound like the kernel above: 29 us for 256 workgroups of 1024 tokens, 128x64
+// bf16, half of what forming the outputs takes.
 template <typename T, int KD>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && KD == 64 ? 4 : 2) void linear_states(LinearRun run) {
     using M = Mat<T>;
@@ -1106,7 +1118,8 @@ hipError_t launch_width(const LinearRun& r, bool states_only, hipStream_t stream
 }
 
 // The state entering every segment: a thread folds four elements of one head's
-// states over the segments, eight loads ahead of the sums.
+// states over the segments, eight loads ahead of the sums.  Bound by latency
+// where it is called (few heads): 6.7 us for 32 segments of 16 heads, 64x64.
 __global__ __launch_bounds__(256) void linear_join(LinearJoin j) {
     const int per = j.size / 4;
     const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -1140,7 +1153,9 @@ __global__ __launch_bounds__(256) void linear_join(LinearJoin j) {
 // The decay's gradient over one segment of a head: from its right end, where
 // dg of the token behind is <D, S> of the two states there, the differences
 // q . dq - k . dk add up token by token (in fp64: the sums of the two nearly
-// cancel where the memory is long).
+// cancel where the memory is long).  Bound by latency, a workgroup to a segment:
+// 9.4 us for 64 heads of 2048 tokens and 128 keys (37 with 256 threads and a
+// load after the other).
 constexpr int kGradThreads = 1024, kGradWaves = kGradThreads / 64;
 
 __global__ __launch_bounds__(kGradThreads) void linear_decay_grad(LinearDecayGrad d) {
@@ -1243,6 +1258,7 @@ __global__ __launch_bounds__(kGradThreads) void linear_decay_grad(LinearDecayGra
 }
 
 // Gradients of rows that several heads share: their heads' sum, in order.
+// Bound by the bytes, or the launch: 4.8 us for 3003 rows of 6 heads x 48.
 __global__ __launch_bounds__(256) void linear_group_sum(LinearGroupSum s) {
     const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
     const int64_t row = s.G * s.width;

@@ -57,8 +57,8 @@ struct LinearRun {
     int32_t segments;
     int64_t seg_tokens;          // a multiple of kSegment
     int32_t bf16;
-    int32_t split;               // products with operands split in two bf16 halves each
-    float* seg_state[2];         // states-only runs: [B, H, segments][kd][vd] per job
+    int32_t split;               // scores and state as three bf16 terms each
+    float* seg_state[2];         // states-only runs: [B, H, segments][kd][vd] per job, not written for the last segment
     float* seg_decay[2];         // and [B, H, segments], log2 of the segment's decay
 };
 

@@ -70,6 +70,14 @@ def test_sizes_and_pointers(lib, call):
     assert call(lib, g=ODD) == 5
 
 
+@pytest.mark.parametrize("call", [fwd, bwd, step])
+def test_heads_of_one_launch(lib, call):
+    """Four column tiles of 512 threads a head stay below 2^32 work-items: past 2^20 heads the call is refused."""
+    more = {"slots": FAKE} if call is step else {"L": 1}
+    assert call(lib, B=1 << 18, H=4, q=None, **more) == 1
+    assert call(lib, B=(1 << 18) + 1, H=4, q=None, **more) == 4
+
+
 def test_outputs(lib):
     assert fwd(lib, o=None) == 1 and fwd(lib, o=MIS) == 5
     for name in ("h0", "h", "lens"):

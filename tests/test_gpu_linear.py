@@ -375,3 +375,14 @@ def test_outputs_past_32_bits():
         x, y = ssm.linear_attention_fwd(q[b:b + 1], q[b:b + 1], v[b:b + 1, :, heads].contiguous(), g[:2].contiguous())
         near = (o[b:b + 1, :, heads].float() - x.float()).norm() / x.float().norm()
         assert float(near) < 5e-3 and float((h[b:b + 1, heads] - y).norm() / y.norm()) < 1e-5
+
+
+def test_the_most_heads():
+    """2^20 heads of the widest values: one launch of 2^31 work-items, every output of it exact."""
+    B, H, Dk, Dv = 64, 16384, 16, 256
+    g = torch.Generator(device="cuda").manual_seed(5)
+    q, k = (torch.randint(-2, 3, (B, 1, 1, Dk), generator=g, device="cuda").to(BF) for _ in range(2))
+    v = torch.randint(-4, 5, (B, 1, H, Dv), generator=g, device="cuda", dtype=torch.int8).to(BF)
+    o, _ = ssm.linear_attention_fwd(q, k, v, torch.zeros(H, device="cuda"), scale=1.0, return_last_state=False)
+    dots = (q.float() * k.float()).sum(-1)                        # at most 64 in size: products with v are exact in bf16
+    assert torch.equal(o, (dots.reshape(B, 1, 1, 1) * v.float()).to(BF))

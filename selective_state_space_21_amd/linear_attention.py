@@ -249,6 +249,8 @@ def _norm_args(q, k, q_weight, k_weight, positions, inv_freq, *more):
     """more: (name, tensor, 0 for queries or 1 for keys), dense tensors of their shapes."""
     dt = _args.act_dtype("q", q)
     _args.need(k=k)
+    if not isinstance(k, torch.Tensor):
+        raise TypeError("k must be a torch.Tensor")
     if q.dim() < 2 or k.dim() != q.dim():
         raise ValueError("q must be [..., q_heads, width] and k [..., k_heads, width]")
     lead, dev, width = tuple(q.shape[:-2]), q.device, q.shape[-1]

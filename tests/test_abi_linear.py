@@ -205,7 +205,7 @@ def test_attention_wrappers(kw, err):
 
 def test_other_wrappers():
     z = torch.zeros(5, 2, 16)
-    for kw, err in ((dict(), ValueError), (dict(k=None), TypeError), (dict(q=torch.zeros(5, 2, 16).half()), TypeError),
+    for kw, err in ((dict(), ValueError), (dict(k=None), TypeError), (dict(k=[z]), TypeError), (dict(q=torch.zeros(5, 2, 16).half()), TypeError),
                     (dict(k=torch.zeros(4, 2, 16)), ValueError), (dict(k=torch.zeros(5, 16)), ValueError),
                     (dict(inv_freq=torch.zeros(8)), (TypeError, ValueError))):
         with pytest.raises(err):

@@ -8,16 +8,16 @@
 //
 // Bound by the bytes, each element read and written once, where there are many
 // rows (16384 x 40 heads x 128 bf16 73.6 us, 4.6 TB/s), else by the way from the
-// positions to the angles to the first head (4099 x 15 x 96 bf16 11.6 us forward,
-// 17.9 backward, 27.8 with a head's loads behind the one before and angles two
+// positions to the angles to the first head (4099 x 15 x 96 bf16 11.1 us forward,
+// 18.3 backward, 27.8 with a head's loads behind the one before and angles two
 // rows at a time; the bytes take 4.3 and 6.5).  A group of lanes has one head of
 // one row; a lane holds whole pairs (elements p and p + R / 2, or 2p and 2p + 1),
 // VEC neighbouring ones to a load, so the rotation needs no exchange and the sum
-// over the width log2(lanes) of them.  A workgroup takes a
-// few rows: their angles are reduced once, in fp64 (a position of 10^6 leaves
-// an fp32 angle 4 bits behind the point), and their sines shared by the heads
-// through LDS.  The backward's workgroups sum their rows' shares of the
-// weights' gradients in registers, and a last launch adds those up in order.
+// over the width log2(lanes) of them.  A workgroup takes a few rows: their angles
+// are reduced once, in fp64 (a position of 10^6 leaves an fp32 angle 4 bits
+// behind the point), and their sines shared by the heads through LDS.  The
+// backward's workgroups sum their rows' shares of the weights' gradients in
+// registers, and a last launch adds those up in order.
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>
@@ -353,8 +353,9 @@ hipError_t launch(const HeadNormArgs& a, bool backward, int lanes, hipStream_t s
         const int tokens = a.group_rows < most ? (int)a.group_rows : most;
         head_norm_bwd<T, VEC, NP><<<dim3((unsigned)a.groups), kThreads, 0, stream>>>(a, lanes, tokens);
     } else {
-        // enough heads to keep the lanes busy a few times over, fewer while that leaves CUs idle
-        const int64_t share = a.rows / 2048 < 8 ? a.rows / 2048 : 8;
+        // enough heads to keep the lanes busy a few times over, fewer while that leaves CUs idle: four workgroups
+        // to a CU (eight, and half the rows each: 12.0 instead of 11.1 us for 4099 x 15 x 96, the same for 16384 x 40)
+        const int64_t share = a.rows / 1024 < 8 ? a.rows / 1024 : 8;
         const int tokens = share < 1 ? 1 : share < most ? (int)share : most;
         const int64_t blocks = (a.rows + tokens - 1) / tokens;
         head_norm_fwd<T, VEC, NP><<<dim3((unsigned)blocks), kThreads, 0, stream>>>(a, lanes, tokens);

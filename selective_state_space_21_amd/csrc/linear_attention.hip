@@ -351,7 +351,8 @@ struct Decays {
 template <typename T, typename Keys>
 __device__ __forceinline__ typename Mat<T>::Frag down_keys(const T* tile, int row, int c8, int w, int i) {
     if constexpr (sizeof(T) == 2)
-        return Mat<T>::down(&tile[Keys::at(row + i / 4, c8 + i % 4) + 4 * w], &tile[Keys::at(row + 4 + i / 4, c8 + i % 4) + 4 * w]);
+        return Mat<T>::down(&tile[Keys::at(row + i / 4, c8 + i % 4) + 4 * w],
+                            &tile[Keys::at(row + 4 + i / 4, c8 + i % 4) + 4 * w]);
     else
         return Mat<T>::down(&tile[Keys::at(row, c8 + i / 4) + 4 * w + i % 4], Keys::kStride);
 }
@@ -536,9 +537,10 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && KD == 64 ? 4 : 2) void 
                             p && live && row < kd ? p[(int64_t)row * job.sk + (int64_t)(col + i) * job.sv] : 0.0f;
                     }
         }
-        // operands in groups of up to 64 registers; the queries' are free when the keys' are read
+        // operands in groups of up to 64 registers, 32 beside a wider state or its terms (that one: 126 instead of 129 us
+        // for dq and dk of 4x2048x16x128); the queries' are free when the keys' are read
         constexpr int REGS = sizeof(T) == 2 ? 4 : 8;
-        constexpr int QREGS = KD == 256 ? 32 : 64;
+        constexpr int QREGS = KD == 256 || TERMS > 1 ? 32 : 64;
         constexpr int GQ = KK * RT * REGS <= QREGS ? KK : QREGS / (RT * REGS);
         constexpr int KREGS = KD == 256 ? 16 : 32;
         constexpr int GK = KK * 2 * KB * REGS <= KREGS ? KK : KREGS / (2 * KB * REGS);
@@ -557,14 +559,8 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && KD == 64 ? 4 : 2) void 
 #pragma unroll
                 for (int kk = 0; kk < GK; ++kk)
 #pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                        const int row = 32 * b2 + 8 * g, c8 = 4 * (k0 + kk);
-                        if constexpr (sizeof(T) == 2)
-                            k[b2][kk][w] = M::down(&tile[Keys::at(row + i / 4, c8 + i % 4) + 4 * w],
-                                                   &tile[Keys::at(row + 4 + i / 4, c8 + i % 4) + 4 * w]);
-                        else
-                            k[b2][kk][w] = M::down(&tile[Keys::at(row, c8 + i / 4) + 4 * w + i % 4], Keys::kStride);
-                    }
+                    for (int w = 0; w < 2; ++w)
+                        k[b2][kk][w] = down_keys<T, Keys>(tile, 32 * b2 + 8 * g, 4 * (k0 + kk), w, i);
         };
         if (chunks > 0) {
             clear_scores();
@@ -587,11 +583,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && KD == 64 ? 4 : 2) void 
             const auto load_values = [&] {
 #pragma unroll
                 for (int b2 = 0; b2 < KB; ++b2) {
-                    const T* at = &V[(32 * b2 + 8 * g) * L::kValue + 16 * group];
-                    if constexpr (sizeof(T) == 2)
-                        v[b2] = M::down(at + i / 4 * L::kValue + 4 * (i % 4), at + (4 + i / 4) * L::kValue + 4 * (i % 4));
-                    else
-                        v[b2] = M::down(at + i, L::kValue);
+                    v[b2] = down_values<T, L::kValue>(&V[(32 * b2 + 8 * g) * L::kValue + 16 * group], i);
                     u[b2][0] = *reinterpret_cast<const f32x4*>(&s.until[slot][32 * b2 + 8 * g]);
                     u[b2][1] = *reinterpret_cast<const f32x4*>(&s.until[slot][32 * b2 + 8 * g + 4]);
                 }
@@ -608,39 +600,37 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && KD == 64 ? 4 : 2) void 
             load_queries(s.Q[now], 0);
             if constexpr (L::kEarly) load_values();
             issue_point();
-            {
-                f32x4 out[RT];
+            f32x4 out[RT];
 #pragma unroll
-                for (int it = 0; it < RT; ++it) out[it] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int it = 0; it < RT; ++it) out[it] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int k0 = 0; k0 < KK; k0 += GQ) {
-                    if (k0 > 0) {
-                        load_queries(s.Q[now], k0);
-                        issue_point();
-                    }
-#pragma unroll
-                    for (int kk = 0; kk < GQ; ++kk) {
-                        const Terms<T, TERMS> x(__builtin_shufflevector(state[k0 + kk][0], state[k0 + kk][1],
-                                                                        0, 1, 2, 3, 4, 5, 6, 7));
-#pragma unroll
-                        for (int n = 0; n < TERMS; ++n)
-#pragma unroll
-                            for (int it = 0; it < RT; ++it) out[it] = M::mma(x.term[n], q[kk][it], out[it]);
-                    }
+            for (int k0 = 0; k0 < KK; k0 += GQ) {
+                if (k0 > 0) {
+                    load_queries(s.Q[now], k0);
+                    issue_point();
                 }
 #pragma unroll
-                for (int it = 0; it < RT; ++it) s.through[(group * RT + it) * 64 + lane] = out[it];
-                load_keys(s.K[now], 0);
-                issue_point();
-                // the next chunk's values, or this one's where LDS holds one chunk's
-                vr.stage(s.V[L::kEarly ? next : 0], mate, value_place);
-                if constexpr (KEYS_BY_STATE) {
-                    kr.stage(s.K[next], mate, key_place);
-                    kr.fetch(left - 2 * C, mate);
+                for (int kk = 0; kk < GQ; ++kk) {
+                    const Terms<T, TERMS> x(__builtin_shufflevector(state[k0 + kk][0], state[k0 + kk][1],
+                                                                    0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+                    for (int n = 0; n < TERMS; ++n)
+#pragma unroll
+                        for (int it = 0; it < RT; ++it) out[it] = M::mma(x.term[n], q[kk][it], out[it]);
                 }
-                vr.fetch(left - (L::kEarly ? 2 : 1) * C, mate);
-                if constexpr (L::kEarly) decay_values();
             }
+#pragma unroll
+            for (int it = 0; it < RT; ++it) s.through[(group * RT + it) * 64 + lane] = out[it];
+            load_keys(s.K[now], 0);
+            issue_point();
+            // the next chunk's values, or this one's where LDS holds one chunk's
+            vr.stage(s.V[L::kEarly ? next : 0], mate, value_place);
+            if constexpr (KEYS_BY_STATE) {
+                kr.stage(s.K[next], mate, key_place);
+                kr.fetch(left - 2 * C, mate);
+            }
+            vr.fetch(left - (L::kEarly ? 2 : 1) * C, mate);
+            if constexpr (L::kEarly) decay_values();
             more_decays(c);
             lds_barrier();
 
@@ -723,22 +713,20 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && KD == 64 ? 4 : 2) void 
         const char* dot_base = nullptr;
         float* dots = nullptr;
         int out_step = 0, dot_step = 0;
-        {
 #pragma unroll
-            for (int it = 0; it < RT; ++it) {
-                const int row = 16 * it + i, t = rev ? C - 1 - row : row;
-                out_at[it] = live ? (uint32_t)((t * (int)run.H * vd + 4 * g) * esize) : kNoOffset;
-                if constexpr (kDots)
-                    dot_at[it] = live ? (uint32_t)((t * (int)job.dot_row + 4 * g) * (int)sizeof(T)) : kNoOffset;
-            }
-            out_base = static_cast<char*>(job.out) + (((b * run.L + token0) * run.H + h) * vd + col) * esize;
-            out_step = (rev ? -C : C) * (int)run.H * vd * esize;
-            if (kDots && job.dots) {
-                dot_base = static_cast<const char*>(job.dot_with) +
-                           ((b * run.L + token0) * job.dot_row + (int64_t)(h / job.dot_per) * vd + col) * (int)sizeof(T);
-                dot_step = (rev ? -C : C) * (int)job.dot_row * (int)sizeof(T);
-                dots = job.dots + ((int64_t)(tile * kGroups + group) * run.B * run.H + bh) * run.L + token0;
-            }
+        for (int it = 0; it < RT; ++it) {
+            const int row = 16 * it + i, t = rev ? C - 1 - row : row;
+            out_at[it] = live ? (uint32_t)((t * (int)run.H * vd + 4 * g) * esize) : kNoOffset;
+            if constexpr (kDots)
+                dot_at[it] = live ? (uint32_t)((t * (int)job.dot_row + 4 * g) * (int)sizeof(T)) : kNoOffset;
+        }
+        out_base = static_cast<char*>(job.out) + (((b * run.L + token0) * run.H + h) * vd + col) * esize;
+        out_step = (rev ? -C : C) * (int)run.H * vd * esize;
+        if (kDots && job.dots) {
+            dot_base = static_cast<const char*>(job.dot_with) +
+                       ((b * run.L + token0) * job.dot_row + (int64_t)(h / job.dot_per) * vd + col) * (int)sizeof(T);
+            dot_step = (rev ? -C : C) * (int)job.dot_row * (int)sizeof(T);
+            dots = job.dots + ((int64_t)(tile * kGroups + group) * run.B * run.H + bh) * run.L + token0;
         }
 
         Rows<T, KD, C, kTeam> qr;
@@ -796,85 +784,79 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && KD == 64 ? 4 : 2) void 
         };
         const auto step = [&](auto parity, int c) {
             constexpr int now = decltype(parity)::value, next = now ^ 1;
-            {
-                stage(next);
-                issue_point();
-                if (c > 0) store(left + C);
-                u32x4 with[RT];                              // what the outputs' dot products are taken with
-                if (kDots && dots) {
-                    const __amdgpu_buffer_rsrc_t r = make_rsrc(dot_base, kRecords);
-                    dot_base += dot_step;
-#pragma unroll
-                    for (int it = 0; it < RT; ++it) {
-                        const int at = (int)(16 * it + i < left ? dot_at[it] : kNoOffset);
-                        if constexpr (sizeof(T) == 4) {
-                            with[it] = __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0);
-                        } else {
-                            const u32x2 z = __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, 0);
-                            with[it] = u32x4{z[0], z[1], 0, 0};
-                        }
-                    }
-                }
-                issue_point();
-                fetch(left - 2 * C);
-                more_decays(c);
-                lds_barrier();   // the state's part, this chunk's values and scores, the next one's rows are there
-
-                Score x[MINE];
-#pragma unroll
-                for (int m = 0; m < MINE; ++m)
-                    if (has(m)) start(x[m], next, next_of(slot), group + kGroups * m);
-                issue_point();
-#pragma unroll
-                for (int m = 0; m < MINE; ++m)
-                    if (has(m)) multiply(x[m], next);
-                Frag v[KB], p[RT][KB][TERMS];
-                float since[RT];
+            stage(next);
+            issue_point();
+            if (c > 0) store(left + C);
+            u32x4 with[RT];                              // what the outputs' dot products are taken with
+            if (kDots && dots) {
+                const __amdgpu_buffer_rsrc_t r = make_rsrc(dot_base, kRecords);
+                dot_base += dot_step;
 #pragma unroll
                 for (int it = 0; it < RT; ++it) {
-                    out[it] = s.through[(group * RT + it) * 64 + lane];
-                    since[it] = s.hi[slot][16 * it + i];
+                    const int at = (int)(16 * it + i < left ? dot_at[it] : kNoOffset);
+                    if constexpr (sizeof(T) == 4) {
+                        with[it] = __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0);
+                    } else {
+                        const u32x2 z = __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, 0);
+                        with[it] = u32x4{z[0], z[1], 0, 0};
+                    }
                 }
+            }
+            issue_point();
+            fetch(left - 2 * C);
+            more_decays(c);
+            lds_barrier();   // the state's part, this chunk's values and scores, the next one's rows are there
+
+            Score x[MINE];
 #pragma unroll
-                for (int b2 = 0; b2 < KB; ++b2) {
-                    const T* at = &s.V[L::kEarly ? now : 0][(32 * b2 + 8 * g) * L::kValue + 16 * group];
-                    if constexpr (sizeof(T) == 2)
-                        v[b2] = M::down(at + i / 4 * L::kValue + 4 * (i % 4), at + (4 + i / 4) * L::kValue + 4 * (i % 4));
-                    else
-                        v[b2] = M::down(at + i, L::kValue);
+            for (int m = 0; m < MINE; ++m)
+                if (has(m)) start(x[m], next, next_of(slot), group + kGroups * m);
+            issue_point();
 #pragma unroll
-                    for (int it = 2 * b2; it < RT; ++it)
+            for (int m = 0; m < MINE; ++m)
+                if (has(m)) multiply(x[m], next);
+            Frag v[KB], p[RT][KB][TERMS];
+            float since[RT];
 #pragma unroll
-                        for (int n = 0; n < TERMS; ++n)
-                            p[it][b2][n] = M::along(&s.P[now][n][Scores::at(16 * it + i, 4 * b2 + g)]);
-                }
-                issue_point();
+            for (int it = 0; it < RT; ++it) {
+                out[it] = s.through[(group * RT + it) * 64 + lane];
+                since[it] = s.hi[slot][16 * it + i];
+            }
 #pragma unroll
-                for (int m = 0; m < MINE; ++m)
-                    if (has(m)) finish(x[m], next);
+            for (int b2 = 0; b2 < KB; ++b2) {
+                v[b2] = down_values<T, L::kValue>(&s.V[L::kEarly ? now : 0][(32 * b2 + 8 * g) * L::kValue + 16 * group], i);
 #pragma unroll
-                for (int it = 0; it < RT; ++it) out[it] *= fast_exp2(since[it]) * outer;
-#pragma unroll
-                for (int b2 = 0; b2 < KB; ++b2)
+                for (int it = 2 * b2; it < RT; ++it)
 #pragma unroll
                     for (int n = 0; n < TERMS; ++n)
+                        p[it][b2][n] = M::along(&s.P[now][n][Scores::at(16 * it + i, 4 * b2 + g)]);
+            }
+            issue_point();
 #pragma unroll
-                        for (int it = 2 * b2; it < RT; ++it) out[it] = M::mma(v[b2], p[it][b2][n], out[it]);
-                if (kDots && dots) {
+            for (int m = 0; m < MINE; ++m)
+                if (has(m)) finish(x[m], next);
 #pragma unroll
-                    for (int it = 0; it < RT; ++it) {
-                        const u32x4 z = with[it];
-                        f32x4 y;
-                        if constexpr (sizeof(T) == 4)
-                            y = __builtin_bit_cast(f32x4, z);
-                        else
-                            y = f32x4{__uint_as_float(z[0] << 16), __uint_as_float(z[0] & 0xffff0000u),
-                                      __uint_as_float(z[1] << 16), __uint_as_float(z[1] & 0xffff0000u)};
-                        float sum = fmaf(out[it][3], y[3], fmaf(out[it][2], y[2], fmaf(out[it][1], y[1], out[it][0] * y[0])));
-                        sum += __shfl_xor(sum, 16);
-                        sum += __shfl_xor(sum, 32);
-                        dot[it] = sum;
-                    }
+            for (int it = 0; it < RT; ++it) out[it] *= fast_exp2(since[it]) * outer;
+#pragma unroll
+            for (int b2 = 0; b2 < KB; ++b2)
+#pragma unroll
+                for (int n = 0; n < TERMS; ++n)
+#pragma unroll
+                    for (int it = 2 * b2; it < RT; ++it) out[it] = M::mma(v[b2], p[it][b2][n], out[it]);
+            if (kDots && dots) {
+#pragma unroll
+                for (int it = 0; it < RT; ++it) {
+                    const u32x4 z = with[it];
+                    f32x4 y;
+                    if constexpr (sizeof(T) == 4)
+                        y = __builtin_bit_cast(f32x4, z);
+                    else
+                        y = f32x4{__uint_as_float(z[0] << 16), __uint_as_float(z[0] & 0xffff0000u),
+                                  __uint_as_float(z[1] << 16), __uint_as_float(z[1] & 0xffff0000u)};
+                    float sum = fmaf(out[it][3], y[3], fmaf(out[it][2], y[2], fmaf(out[it][1], y[1], out[it][0] * y[0])));
+                    sum += __shfl_xor(sum, 16);
+                    sum += __shfl_xor(sum, 32);
+                    dot[it] = sum;
                 }
             }
             lds_barrier();                                   // the next chunk's scores are there; this one's rows are free

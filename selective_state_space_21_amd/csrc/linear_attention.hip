@@ -39,7 +39,8 @@
 // Bound: neither the matrix cores (a quarter busy) nor LDS nor HBM, but the
 // length of a chunk's dependent steps between its two barriers with one
 // workgroup a CU: 2.2 us per 64 tokens of 128x64 bf16 alone, 2.9 with all CUs
-// at work (64x64: 1.6, 2.2, then at 80% of the copy rate).  Tried and slower:
+// at work, in the same cycles at a lower clock (64x64: 1.6, 2.2, then at 80% of
+// the copy rate).  Tried and slower:
 // chunks of 32 tokens, wavefronts that each form all outputs of 16 columns,
 // eight of those with half the rows each.
 #include <hip/hip_runtime.h>

@@ -372,7 +372,7 @@ __device__ __forceinline__ typename Mat<T>::Frag down_values(const T* at, int i)
 //   A  state: queries x state -> LDS, values      other: queries, keys, the last chunk's outputs to memory
 //      (rows: stage the next chunk's, fetch those behind them)
 //   B  state: update                              other: the next chunk's scores, this one's outputs
-// Measured: B=8 L=2048 H=16 128x128 bf16 89 us a call (3.0 TB/s of its 271 MB; 107 with the scores finished in one
+// Measured: B=8 L=2048 H=16 128x128 bf16 88 us a call (3.1 TB/s of its 278 MB; 107 with the scores finished in one
 // piece, 142 with one copy of the rows), with split operands 62 us a thousand tokens of 256 workgroups.
 template <typename T, int KD, bool SPLIT>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && KD == 64 ? 4 : 2) void linear_chunks(LinearRun run) {

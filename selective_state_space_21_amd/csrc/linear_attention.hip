@@ -1104,30 +1104,33 @@ hipError_t launch_width(const LinearRun& r, bool states_only, hipStream_t stream
 // states over the segments, eight loads ahead of the sums.  Bound by latency
 // where it is called (few heads): 6.7 us for 32 segments of 16 heads, 64x64.
 __global__ __launch_bounds__(256) void linear_join(LinearJoin j) {
-    const int per = j.size / 4;
+    const int which = blockIdx.y, per = j.size / 4;
     const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (at >= j.heads * per) return;
     const int64_t head = at / per;
     const int e = (int)(at % per) * 4;
+    float* states = j.seg_state[which];
+    const float *decays = j.seg_decay[which], *first = j.first[which];
+    const bool rev = j.reversed[which] != 0;
     f32x4 carry = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (j.first)
+    if (first)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) carry[r] = j.first[head * j.size + e + r];
+        for (int r = 0; r < 4; ++r) carry[r] = first[head * j.size + e + r];
     for (int n0 = 0; n0 < j.segments; n0 += 8) {
         f32x4 own[8];
         float decay[8];
 #pragma unroll
         for (int m = 0; m < 8; ++m)
             if (n0 + m < j.segments - 1) {                   // the last one's state enters none, and is not there
-                const int64_t s = head * j.segments + (j.reversed ? j.segments - 1 - n0 - m : n0 + m);
-                own[m] = *reinterpret_cast<const f32x4*>(j.seg_state + s * j.size + e);
-                decay[m] = j.seg_decay[s];
+                const int64_t s = head * j.segments + (rev ? j.segments - 1 - n0 - m : n0 + m);
+                own[m] = *reinterpret_cast<const f32x4*>(states + s * j.size + e);
+                decay[m] = decays[s];
             }
 #pragma unroll
         for (int m = 0; m < 8; ++m)
             if (n0 + m < j.segments) {
-                const int64_t s = head * j.segments + (j.reversed ? j.segments - 1 - n0 - m : n0 + m);
-                *reinterpret_cast<f32x4*>(j.seg_state + s * j.size + e) = carry;
+                const int64_t s = head * j.segments + (rev ? j.segments - 1 - n0 - m : n0 + m);
+                *reinterpret_cast<f32x4*>(states + s * j.size + e) = carry;
                 if (n0 + m < j.segments - 1) carry = carry * fast_exp2(decay[m]) + own[m];
             }
     }
@@ -1250,17 +1253,18 @@ __global__ __launch_bounds__(256) void linear_group_sum(LinearGroupSum s) {
     const int64_t grp = at % row / s.width;
     const int c = (int)(at % s.width);
     const int per = (int)(s.H / s.G);
-    const float* p = s.part + (t * s.H + grp * per) * s.width + c;
+    const float* p = s.part[blockIdx.y] + (t * s.H + grp * per) * s.width + c;
+    void* out = s.out[blockIdx.y];
     f32x4 x = *reinterpret_cast<const f32x4*>(p);
     for (int n = 1; n < per; ++n) x += *reinterpret_cast<const f32x4*>(p + (int64_t)n * s.width);
     if (s.bf16) {
         uint16_t y[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) y[r] = f32_to_bf16_bits(x[r]);
-        *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(s.out) + at) =
+        *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(out) + at) =
             u32x2{y[0] | (uint32_t)y[1] << 16, y[2] | (uint32_t)y[3] << 16};
     } else {
-        *reinterpret_cast<f32x4*>(static_cast<float*>(s.out) + at) = x;
+        *reinterpret_cast<f32x4*>(static_cast<float*>(out) + at) = x;
     }
 }
 
@@ -1279,7 +1283,7 @@ hipError_t launch_linear_run(const LinearRun& r, bool states_only, hipStream_t s
 
 hipError_t launch_linear_join(const LinearJoin& j, hipStream_t stream) {
     const int64_t n = j.heads * (j.size / 4);
-    linear_join<<<dim3((unsigned)((n + 255) / 256)), 256, 0, stream>>>(j);
+    linear_join<<<dim3((unsigned)((n + 255) / 256), (unsigned)j.n), 256, 0, stream>>>(j);
     return hipGetLastError();
 }
 
@@ -1291,7 +1295,7 @@ hipError_t launch_linear_decay_grad(const LinearDecayGrad& d, hipStream_t stream
 hipError_t launch_linear_group_sum(const LinearGroupSum& s, hipStream_t stream) {
     const int64_t n = s.rows * s.G * (s.width / 4);
     if (n == 0) return hipSuccess;
-    linear_group_sum<<<dim3((unsigned)((n + 255) / 256)), 256, 0, stream>>>(s);
+    linear_group_sum<<<dim3((unsigned)((n + 255) / 256), 2), 256, 0, stream>>>(s);
     return hipGetLastError();
 }
 

@@ -110,14 +110,15 @@ hipError_t launch_linear_bwd(const LinearBwdArgs& a, hipStream_t stream);
 hipError_t launch_linear_run(const LinearRun& r, bool states_only, hipStream_t stream);
 
 // seg_state[s] <- the state entering segment s: first (or zeros), then what
-// the segments before s leave (after s where reversed).
+// the segments before s leave (after s where reversed); one or two of these.
 struct LinearJoin {
-    float* seg_state;            // [heads, segments][size]
-    const float* seg_decay;      // [heads, segments]
-    const float* first;          // [heads][size] or NULL
+    float* seg_state[2];         // [heads, segments][size]
+    const float* seg_decay[2];   // [heads, segments]
+    const float* first[2];       // [heads][size] or NULL
+    int32_t reversed[2];
+    int32_t n;
     int64_t heads;
     int32_t segments, size;      // size: elements of a state, a multiple of 4
-    int32_t reversed;
 };
 hipError_t launch_linear_join(const LinearJoin& j, hipStream_t stream);
 
@@ -142,10 +143,10 @@ struct LinearDecayGrad {
 };
 hipError_t launch_linear_decay_grad(const LinearDecayGrad& d, hipStream_t stream);
 
-// out[row][g][c] = sum over the heads of group g of part[row][head][c]
+// out[row][g][c] = sum over the heads of group g of part[row][head][c], of both
 struct LinearGroupSum {
-    const float* part;           // [rows, H, width] fp32
-    void* out;                   // [rows, G, width] dtype
+    const float* part[2];        // [rows, H, width] fp32
+    void* out[2];                // [rows, G, width] dtype
     int64_t rows, H, G;
     int32_t width;               // a multiple of 16
     int bf16;

@@ -150,10 +150,12 @@ LinearJob job_of(const Rows& q, const Rows& k, const Rows& v) {
     return j;
 }
 
-hipError_t join(float* states, const float* decay, const float* first, const LinearArgs& a, bool reversed,
-                hipStream_t stream) {
-    LinearJoin j{states, decay, first, a.B * a.H, a.plan.segments, (int32_t)(a.Dk * a.Dv), reversed ? 1 : 0};
-    return launch_linear_join(j, stream);
+LinearJoin join_of(const LinearArgs& a) {
+    LinearJoin j{};
+    j.heads = a.B * a.H;
+    j.segments = a.plan.segments;
+    j.size = (int32_t)(a.Dk * a.Dv);
+    return j;
 }
 
 }  // namespace
@@ -165,14 +167,32 @@ LinearPlan plan_linear_fwd(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t 
     return plan(units, L, whole, [=](int64_t n) { return 0.5 * whole(n - 1); });
 }
 
-// dq and dk in one launch (for bf16 with split operands, a fifth more work), dv in another.
+// Workgroups of dq and dk, and of dv, for one segment.
+struct BwdUnits {
+    int64_t keys, values;
+    BwdUnits(int64_t B, int64_t H, int64_t Dk, int64_t Dv)
+        : keys(2 * B * H * tiles_of(Dk)), values(B * H * tiles_of(Dv)) {}
+};
+
+// dq, dk and dv go out as one launch where one kernel takes them: rows of one padded width.  `split` operands, which
+// dv does without, cost it more than a launch of its own unless all workgroups find a CU free.  bf16, whole: B=2 L=512
+// H=8 64x64 (48 workgroups) 49 us in two launches, 32 in one; B=1 L=2048 H=16 128x128 (96) 192 and 116; B=4 of those
+// (384) 229 and 237.  fp32, no split: B=8 L=512 H=8 64x64 95 and 56.
+bool bwd_at_once(const BwdUnits& units, int64_t segments, int64_t Dk, int64_t Dv, bool split) {
+    return pad(Dk) == pad(Dv) && (!split || (units.keys + units.values) * segments <= 256);
+}
+
+// For bf16 with split operands, a fifth more work, as the decay's gradient wants them.
 LinearPlan plan_linear_bwd(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv, bool bf16) {
-    const int64_t of_keys = 2 * B * H * tiles_of(Dk), of_values = B * H * tiles_of(Dv);
-    return plan(of_keys + of_values, L,
+    const BwdUnits units(B, H, Dk, Dv);
+    const double work = bf16 ? 1.2 : 1.0;
+    return plan(units.keys + units.values, L,
                 [=](int64_t n) {
-                    return (bf16 ? 1.2 : 1.0) * token_ns(of_keys * n, Dv, bf16) + token_ns(of_values * n, Dk, bf16);
+                    if (bwd_at_once(units, n, Dk, Dv, bf16))
+                        return work * token_ns((units.keys + units.values) * n, Dv, bf16);
+                    return work * token_ns(units.keys * n, Dv, bf16) + token_ns(units.values * n, Dk, bf16);
                 },
-                [=](int64_t n) { return 0.5 * token_ns(2 * of_values * (n - 1), Dk, bf16); });
+                [=](int64_t n) { return 0.5 * token_ns(2 * units.values * (n - 1), Dk, bf16); });
 }
 
 size_t linear_fwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv, bool bf16) {
@@ -205,7 +225,10 @@ hipError_t launch_linear_fwd(const LinearArgs& a, hipStream_t stream) {
         r.seg_decay[0] = ws.decay;
         r.job[0].state_in = nullptr;
         if ((e = launch_linear_run(r, true, stream)) != hipSuccess) return e;
-        if ((e = join(ws.state, ws.decay, a.h0, a, false, stream)) != hipSuccess) return e;
+        LinearJoin s = join_of(a);
+        s.n = 1;
+        s.seg_state[0] = ws.state; s.seg_decay[0] = ws.decay; s.first[0] = a.h0;
+        if ((e = launch_linear_join(s, stream)) != hipSuccess) return e;
         j.state_in = ws.state;
         j.in_head = a.plan.segments * a.Dk * a.Dv;
         j.in_seg = a.Dk * a.Dv;
@@ -239,8 +262,12 @@ hipError_t launch_linear_bwd(const LinearBwdArgs& a, hipStream_t stream) {
         r.seg_state[0] = ws.S; r.seg_decay[0] = ws.S_decay;
         r.seg_state[1] = ws.D; r.seg_decay[1] = ws.D_decay;
         if ((e = launch_linear_run(r, true, stream)) != hipSuccess) return e;
-        if ((e = join(ws.S, ws.S_decay, f.h0, f, false, stream)) != hipSuccess) return e;
-        if ((e = join(ws.D, ws.D_decay, a.dh_last, f, true, stream)) != hipSuccess) return e;
+        LinearJoin s = join_of(f);
+        s.n = 2;
+        s.seg_state[0] = ws.S; s.seg_decay[0] = ws.S_decay; s.first[0] = f.h0;
+        s.seg_state[1] = ws.D; s.seg_decay[1] = ws.D_decay; s.first[1] = a.dh_last;
+        s.reversed[1] = 1;
+        if ((e = launch_linear_join(s, stream)) != hipSuccess) return e;
     }
 
     LinearJob dq = job_of(d, v, k), dk = job_of(v, d, q), dv = job_of(k, q, d);
@@ -264,14 +291,13 @@ hipError_t launch_linear_bwd(const LinearBwdArgs& a, hipStream_t stream) {
     dv.state_out = a.dh0; dv.decay_out = 1;
     r = run_of(f);
     if (a.dg) {
-        r.split = 1;
+        r.split = f.bf16;
         dq.dot_with = f.q; dq.dot_row = f.q_row; dq.dot_per = per; dq.dots = ws.dot_q;
         dk.dot_with = f.k; dk.dot_row = f.k_row; dk.dot_per = per; dk.dots = ws.dot_k;
         dq.state_out = ws.S_last;
     }
-    // dv is of the inputs' type alone: it needs no split operands, nor a launch with those that do
     r.job[0] = dq; r.job[1] = dk; r.job[2] = dv;
-    r.jobs = !r.split && pad(f.Dk) == pad(f.Dv) ? 3 : 2;
+    r.jobs = bwd_at_once(BwdUnits(f.B, f.H, f.Dk, f.Dv), f.plan.segments, f.Dk, f.Dv, r.split != 0) ? 3 : 2;
     if ((e = launch_linear_run(r, false, stream)) != hipSuccess) return e;
     if (r.jobs == 2) {
         r.jobs = 1;
@@ -280,9 +306,7 @@ hipError_t launch_linear_bwd(const LinearBwdArgs& a, hipStream_t stream) {
         if ((e = launch_linear_run(r, false, stream)) != hipSuccess) return e;
     }
     if (shared) {
-        LinearGroupSum s{ws.dq, a.dq, f.B * f.L, f.H, f.G, (int32_t)f.Dk, f.bf16};
-        if ((e = launch_linear_group_sum(s, stream)) != hipSuccess) return e;
-        s.part = ws.dk; s.out = a.dk;
+        const LinearGroupSum s{{ws.dq, ws.dk}, {a.dq, a.dk}, f.B * f.L, f.H, f.G, (int32_t)f.Dk, f.bf16};
         if ((e = launch_linear_group_sum(s, stream)) != hipSuccess) return e;
     }
     if (a.dg) {

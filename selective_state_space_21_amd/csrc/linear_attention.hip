@@ -1244,7 +1244,7 @@ __global__ __launch_bounds__(kGradThreads) void linear_decay_grad(LinearDecayGra
 }
 
 // Gradients of rows that several heads share: their heads' sum, in order.
-// Bound by the bytes, or the launch: 4.8 us for 3003 rows of 6 heads x 48.
+// Bound by the bytes, or the launch: 4.8 us for 3003 rows of 6 heads x 48, twice.
 __global__ __launch_bounds__(256) void linear_group_sum(LinearGroupSum s) {
     const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
     const int64_t row = s.G * s.width;

@@ -43,8 +43,8 @@ constexpr int64_t kMostCut = int64_t(1) << 14;
 // H=16 128x128 282 us whole, 128 in 4, 82 in 8 (one round), 110 in 12, 98 in 16;
 // B=4 L=2048 of the same 84 whole, 85 in 2; B=1 L=1024 H=8 64x64 32 whole, 24 in
 // 8, L=512 20 whole, 24 in 4; fp32 B=1 L=16384 H=16 64x64 129 in 16, 143 in 24,
-// 120 in 32.  Backward bf16: B=1 L=8192 H=16 128x128 848 whole, 291 in 4, 262 in
-// 8, 290 in 12; fp32 B=3 L=1001 H=6 48x112 216 whole, 84 in 6, 106 in 8.  A cut
+// 120 in 32.  Backward bf16: B=1 L=8192 H=16 128x128 421 whole, 249 in 4, 229 in
+// 8, 279 in 16; fp32 B=3 L=1001 H=6 48x112 211 whole, 83 in 6, 103 in 8.  A cut
 // has to save 5%.
 template <typename Whole, typename States>
 LinearPlan plan(int64_t units, int64_t L, Whole whole, States states) {

@@ -20,13 +20,12 @@ int pad(int64_t width) { return width <= 64 ? 64 : width <= 128 ? 128 : 256; }
 
 // Nanoseconds a token of a launch with `units` workgroups that contract `keys`
 // elements.  256 run at once, one on a CU; fewer run faster by up to a quarter,
-// for they share the caches' and the memory's rate.  Where fp32 keys of up to
-// 64 elements are contracted, LDS and registers leave room for two on a CU,
-// which then take 1.6 of the time that one takes.  Measured with all CUs at
-// work: bf16 41 (64 keys), 51 (128), 64 (256); fp32 73 (64), 120 (128).
+// at a higher clock.  Where fp32 keys of up to 64 elements are contracted, LDS
+// and registers leave room for two on a CU, which then take 1.6 of the time that
+// one takes.  Measured with all CUs at work, one workgroup on each.
 double token_ns(int64_t units, int64_t keys, bool bf16) {
     const int kd = pad(keys);
-    const double all = bf16 ? (kd == 64 ? 40.0 : kd == 128 ? 50.0 : 65.0) : (kd == 64 ? 75.0 : kd == 128 ? 125.0 : 250.0);
+    const double all = bf16 ? (kd == 64 ? 36.0 : kd == 128 ? 52.0 : 74.0) : (kd == 64 ? 81.0 : kd == 128 ? 130.0 : 251.0);
     const bool pairs = !bf16 && kd == 64;
     const int64_t at_once = pairs ? 512 : 256, rest = units % at_once;
     const double one = pairs ? 1.6 : 1.0;

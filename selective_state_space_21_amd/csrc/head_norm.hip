@@ -9,7 +9,7 @@
 // Bound by the bytes, each element read and written once, where there are many
 // rows (16384 x 40 heads x 128 bf16 73.6 us, 4.6 TB/s), else by the way from the
 // positions to the angles to the first head (4099 x 15 x 96 bf16 11.1 us forward,
-// 18.3 backward, 27.8 with a head's loads behind the one before and angles two
+// 17.1 backward, 27.8 with a head's loads behind the one before and angles two
 // rows at a time; the bytes take 4.3 and 6.5).  A group of lanes has one head of
 // one row; a lane holds whole pairs (elements p and p + R / 2, or 2p and 2p + 1),
 // VEC neighbouring ones to a load, so the rotation needs no exchange and the sum
@@ -250,27 +250,30 @@ __global__ __launch_bounds__(kThreads) void head_norm_bwd(HeadNormArgs a, int la
         for (int m = 0; m < NP; ++m)
             if (place(m).there) x[m].load(p, place(m)), d[m].load(dy, place(m));
     };
-    Pairs<VEC> wt[2][NP], sum[2][NP];
-#pragma unroll
-    for (int which = 0; which < 2; ++which)
+    const int64_t start = blockIdx.x * a.group_rows;
+    const int64_t stop = start + a.group_rows < a.rows ? start + a.group_rows : a.rows;
+    // One kind of head after the other: with the weights and sums of both in registers a SIMD has room for a wavefront
+    // less (fp32 2048 rows of 32 heads x 64 18.8 us, 13.6 so).  Rows of few heads in more than one turn pay for their
+    // angles twice (65536 of 8 x 64 bf16 53 us, 55).
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
+        const int heads = (int)a.heads[which];
+        Pairs<VEC> wt[NP], sum[NP];
 #pragma unroll
         for (int m = 0; m < NP; ++m) {
-            wt[which][m] = weights<VEC>(a.weight[which], place(m));
+            wt[m] = weights<VEC>(a.weight[which], place(m));
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) sum[which][m].a[j] = sum[which][m].b[j] = 0.0f;
+            for (int j = 0; j < VEC; ++j) sum[m].a[j] = sum[m].b[j] = 0.0f;
         }
-    const int64_t stop = (blockIdx.x + 1) * a.group_rows < a.rows ? (blockIdx.x + 1) * a.group_rows : a.rows;
-    for (int64_t row0 = blockIdx.x * a.group_rows; row0 < stop; row0 += tokens) {
-        const int n = stop - row0 < tokens ? (int)(stop - row0) : tokens;
-        Row first[2], first_d[2];
-#pragma unroll
-        for (int which = 0; which < 2; ++which) fetch(first[which], first_d[which], which, row0, n, grp);
-        lds_barrier();                                       // the last rows' angles have been read
-        angles(a, row0, n, half, angle);
-        lds_barrier();
-#pragma unroll
-        for (int which = 0; which < 2; ++which) {
-            const int heads = (int)a.heads[which], items = n * heads;
+        for (int64_t row0 = start; row0 < stop; row0 += tokens) {
+            const int n = stop - row0 < tokens ? (int)(stop - row0) : tokens, items = n * heads;
+            Row first, first_d;
+            fetch(first, first_d, which, row0, n, grp);
+            if (which == 0 || stop - start > tokens) {       // else they are there
+                lds_barrier();                               // the last rows' angles have been read
+                angles(a, row0, n, half, angle);
+                lds_barrier();
+            }
             for (int item = grp; item < items; item += groups) {
                 const int r = item / heads, h = item % heads;
                 T* dx = static_cast<T*>(a.dx[which]) + ((row0 + r) * heads + h) * a.width;
@@ -282,8 +285,8 @@ __global__ __launch_bounds__(kThreads) void head_norm_bwd(HeadNormArgs a, int la
                 for (int m = 0; m < NP; ++m) {
                     const int p = (lane + m * lanes) * VEC;
                     if (place(m).there) {
-                        v[m] = first[which][m].pairs(place(m));
-                        d[m] = first_d[which][m].pairs(place(m));
+                        v[m] = first[m].pairs(place(m));
+                        d[m] = first_d[m].pairs(place(m));
 #pragma unroll
                         for (int j = 0; j < VEC; ++j) {
                             float2 cs = float2{1.0f, 0.0f};
@@ -292,8 +295,7 @@ __global__ __launch_bounds__(kThreads) void head_norm_bwd(HeadNormArgs a, int la
                             d[m].b[j] = d[m].b[j] * cs.x - d[m].a[j] * cs.y;
                             d[m].a[j] = f;
                             sq = fmaf(v[m].a[j], v[m].a[j], fmaf(v[m].b[j], v[m].b[j], sq));
-                            dot = fmaf(d[m].a[j] * wt[which][m].a[j], v[m].a[j],
-                                       fmaf(d[m].b[j] * wt[which][m].b[j], v[m].b[j], dot));
+                            dot = fmaf(d[m].a[j] * wt[m].a[j], v[m].a[j], fmaf(d[m].b[j] * wt[m].b[j], v[m].b[j], dot));
                         }
                     }
                 }
@@ -305,26 +307,23 @@ __global__ __launch_bounds__(kThreads) void head_norm_bwd(HeadNormArgs a, int la
 #pragma unroll
                         for (int j = 0; j < VEC; ++j) {
                             const float na = v[m].a[j] * rstd, nb = v[m].b[j] * rstd;
-                            sum[which][m].a[j] = fmaf(d[m].a[j], na, sum[which][m].a[j]);
-                            sum[which][m].b[j] = fmaf(d[m].b[j], nb, sum[which][m].b[j]);
-                            v[m].a[j] = rstd * (d[m].a[j] * wt[which][m].a[j] - na * c);
-                            v[m].b[j] = rstd * (d[m].b[j] * wt[which][m].b[j] - nb * c);
+                            sum[m].a[j] = fmaf(d[m].a[j], na, sum[m].a[j]);
+                            sum[m].b[j] = fmaf(d[m].b[j], nb, sum[m].b[j]);
+                            v[m].a[j] = rstd * (d[m].a[j] * wt[m].a[j] - na * c);
+                            v[m].b[j] = rstd * (d[m].b[j] * wt[m].b[j] - nb * c);
                         }
                         v[m].write(dx, place(m));
                     }
-                    first[which][m] = next[m];
-                    first_d[which][m] = next_d[m];
+                    first[m] = next[m];
+                    first_d[m] = next_d[m];
                 }
             }
         }
-    }
-#pragma unroll
-    for (int which = 0; which < 2; ++which) {
         if (!a.dweight[which]) continue;
-        lds_barrier();
+        lds_barrier();                                       // the other kind's sums have been read
 #pragma unroll
         for (int m = 0; m < NP; ++m)
-            if (place(m).there) sum[which][m].write(share + grp * a.width, place(m));
+            if (place(m).there) sum[m].write(share + grp * a.width, place(m));
         lds_barrier();
         for (int c = threadIdx.x; c < a.width; c += kThreads) {
             float x = share[c];

@@ -92,6 +92,13 @@ def test_forward_and_backward(shape, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F, BF])
+@pytest.mark.parametrize("shape", [(5203, 2, 1, 512, 512), (5203, 1, 2, 510, 510)])
+def test_rows_of_a_workgroup_in_turns(shape, dtype):
+    """More rows for a workgroup than it keeps angles of: both kinds of heads form them again, a turn at a time."""
+    check_all(*make(*shape, dtype, seed=3), False)
+
+
+@pytest.mark.parametrize("dtype", [F, BF])
 @pytest.mark.parametrize("offset", [0, 1, 4])
 def test_parts_of_a_projection(dtype, offset):
     """Heads taken out of a wider row, on any border: the dense copies' bits where the loads are the same."""
